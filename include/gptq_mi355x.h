@@ -38,7 +38,7 @@
 extern "C" {
 #endif
 
-#define GPTQ_ABI_VERSION 0x00020005u /* major 2, minor 5 */
+#define GPTQ_ABI_VERSION 0x00020006u /* major 2, minor 6 */
 
 typedef enum gptq_status {
   GPTQ_OK = 0,
@@ -379,6 +379,153 @@ gptq_status gptq_layer_error(const void* W, gptq_dtype wdt, int64_t m, int64_t n
                              const uint8_t* codes, const float* scales, const float* zeros,
                              int64_t ngroups, const int32_t* g_idx, const float* S, int64_t lds,
                              double* err, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit floating point with a scale per block of 128 -- "AWQ, MinMax, GPTQ
+ * calibration in Model Optimizer" (gtnt.cn news 115337), section 2 (the max
+ * calibrator: scale = amax / qmax, the 8-bit floating-point formats' grid).
+ * Codes are OCP e4m3 (largest value 448), one byte each.  For a block with
+ * a = max |x| over its finite values:
+ *   s = max(RN32(a / 448), 2^-126), 1 where a = 0
+ *   code = the e4m3 value nearest to the real quotient x / s, ties to even
+ * A non-finite x becomes the NaN code.  A code stands for code * s.
+ *
+ * fp8_quantize_rows: X[tokens, n] (row stride ldx, fp32 or bf16), one scale per
+ * token and 128 consecutive columns (the last block may be shorter).
+ * codes[tokens, n] (row stride ldc), scales[ceil(n / 128)][lds] with lds >=
+ * tokens: block after block, so that a product's tile finds its tokens' scales
+ * together.
+ * fp8_swiglu_quantize: the same of h = silu(gate) * up in fp32, gate and up
+ * [tokens, n] of one type (the MLP block's gated activation, not written in 16
+ * bits in between).
+ * fp8_quantize_blocks: W[m, n] (row stride ldw), one scale per 128 x 128 block;
+ * codes[m, n] (row stride ldc), scales[ceil(m / 128)][lds], lds >= ceil(n / 128).
+ * ---------------------------------------------------------------------- */
+gptq_status fp8_quantize_rows(const void* X, gptq_dtype xdt, int64_t tokens, int64_t n,
+                              int64_t ldx, uint8_t* codes, int64_t ldc, float* scales,
+                              int64_t lds, hipStream_t stream);
+gptq_status fp8_swiglu_quantize(const void* gate, int64_t ldg, const void* up, int64_t ldu,
+                                gptq_dtype dt, int64_t tokens, int64_t n, uint8_t* codes,
+                                int64_t ldc, float* scales, int64_t lds, hipStream_t stream);
+gptq_status fp8_quantize_blocks(const void* W, gptq_dtype wdt, int64_t m, int64_t n, int64_t ldw,
+                                uint8_t* codes, int64_t ldc, float* scales, int64_t lds,
+                                hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Product of block-scaled e4m3 matrices ("LLM quantization principles",
+ * section 5.2: low-bit operands multiplied without being written out in 16
+ * bits first):
+ *   Y[t, r] = sum_b xs[b][t] wscales[r / 128][b] sum_{k in block b} X[t, k] W[r, k]
+ * X[tokens, n] (row stride ldx) with xs[ceil(n / 128)][ldxs] as
+ * fp8_quantize_rows writes them, W[m, n] (row stride ldw) with
+ * wscales[ceil(m / 128)][ldws] as fp8_quantize_blocks writes them; Y[tokens, m]
+ * (row stride ldy, fp32 or bf16).  R[tokens, m] (row stride ldr, Y's type), where
+ * it is not NULL, is added before the rounding to Y's type; it may be Y itself.
+ * Sums are fp32 in a fixed order and NaN codes give NaN.  For fp32 Y a block's
+ * products are summed with fp32 accuracy; for bf16 Y and large batches by the
+ * 8-bit matrix instructions, which cut the products of 8 neighbouring columns
+ * at 2^-13 of the largest of them (1.5e-5 relative over normal data, against the
+ * 2^-8 of Y's rounding).
+ * n a multiple of 16 (else GPTQ_ERR_UNSUPPORTED); X and W 16-byte aligned with
+ * row strides that are multiples of 16 and below 2^24.
+ * fp8_linear: Y = X W^T from 16- or 32-bit activations: fp8_quantize_rows into
+ * the workspace, then the product.  X as in fp8_quantize_rows.
+ * Workspace: fp8_gemm_workspace_size / fp8_linear_workspace_size(tokens, m, n).
+ * ---------------------------------------------------------------------- */
+gptq_status fp8_gemm_workspace_size(int64_t tokens, int64_t m, int64_t n, size_t* bytes);
+gptq_status fp8_gemm(const uint8_t* X, int64_t tokens, int64_t n, int64_t ldx, const float* xs,
+                     int64_t ldxs, const uint8_t* W, int64_t m, int64_t ldw, const float* wscales,
+                     int64_t ldws, const void* R, int64_t ldr, void* Y, gptq_dtype ydt,
+                     int64_t ldy, void* ws, size_t ws_bytes, hipStream_t stream);
+gptq_status fp8_linear_workspace_size(int64_t tokens, int64_t m, int64_t n, size_t* bytes);
+gptq_status fp8_linear(const void* X, gptq_dtype xdt, int64_t tokens, int64_t n, int64_t ldx,
+                       const uint8_t* W, int64_t m, int64_t ldw, const float* wscales,
+                       int64_t ldws, void* Y, gptq_dtype ydt, int64_t ldy, void* ws,
+                       size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Quantized key/value cache -- "LLM quantization principles", section 2.1 (the
+ * affine grid) and "Calibration algorithms guide", section 2.2 (a range per
+ * group), applied to the keys and values of one token and head: head_dim values
+ * in groups of group_size, each with its own fp32 scale and, for integers with
+ * zero-points, an 8-bit zero.
+ *   GPTQ_KV_INT4, GPTQ_KV_INT8: rtn_minmax's grid, bit for bit (zeros given:
+ *     asymmetric, value (q - zero) * scale; zeros NULL: symmetric, zero 2^(b-1)).
+ *     4-bit codes lie two to a byte, the even column in the low half.  A NaN
+ *     counts as below the range (code 0); a group that holds an infinity has an
+ *     infinite scale, and no value read from it is finite.
+ *   GPTQ_KV_E4M3: fp8_quantize_rows' grid with the group as its block; zeros is
+ *     not used.
+ * The cache is paged: a token's place is a flat slot, page * page_size + offset
+ * with 0 <= slot < pages * page_size.  The slots' codes lie at
+ *   codes + page * page_stride + offset * slot_stride + head * head_stride (bytes),
+ * scales and zeros at
+ *   page * param_page_stride + offset * param_slot_stride + head * param_head_stride
+ *   + group (elements), any order of pages, slots and heads.
+ * head_dim: a multiple of 8, at most 1024.  group_size: a power of two in
+ * 16 .. 512 (the last group of a head may be shorter) or -1 = the whole head
+ * (head_dim <= 512).  codes 8-byte aligned (4-byte: INT4) and strides multiples
+ * of 8 (4) bytes.
+ *
+ * kv_cache_write: rows K and V [tokens][heads][head_dim] (strides in elements,
+ * fp32 or bf16) go to slots[tokens] of kc and vc.  A negative slot is padding
+ * and is not written.  Where a slot occurs twice the later token's row stays.
+ * kv_cache_read: the rows of slots[tokens] as K and V; a negative slot gives
+ * zeros, a slot may occur any number of times.  Either cache may be NULL (with
+ * its rows); two caches of a call have the same pages and page_size.
+ * A slot past the last is not accessed (write: skipped, read: zeros), and *info
+ * (a device int32 that the caller has cleared, may be NULL) becomes 1.
+ * Nothing but the given slots' rows is written.  tokens times the lanes of a
+ * token (heads * groups * group lanes of 8 values) must stay below 2^31, else
+ * GPTQ_ERR_UNSUPPORTED.  Workspace: kv_cache_write_workspace_size(tokens, kc),
+ * 0 for small calls.
+ * ---------------------------------------------------------------------- */
+typedef enum gptq_kv_format { GPTQ_KV_INT4 = 0, GPTQ_KV_INT8 = 1, GPTQ_KV_E4M3 = 2 } gptq_kv_format;
+
+typedef struct gptq_kv_cache {
+  uint8_t* codes;
+  float* scales;
+  uint8_t* zeros; /* may be NULL */
+  int64_t pages;
+  int64_t page_stride, slot_stride, head_stride;                   /* codes, bytes */
+  int64_t param_page_stride, param_slot_stride, param_head_stride; /* elements     */
+  int32_t page_size, heads, head_dim, group_size, format;
+} gptq_kv_cache;
+
+gptq_status kv_cache_write_workspace_size(int64_t tokens, const gptq_kv_cache* cache,
+                                          size_t* bytes);
+gptq_status kv_cache_write(const void* K, int64_t k_token_stride, int64_t k_head_stride,
+                           const void* V, int64_t v_token_stride, int64_t v_head_stride,
+                           gptq_dtype dt, int64_t tokens, const int64_t* slots,
+                           const gptq_kv_cache* kc, const gptq_kv_cache* vc, int32_t* info,
+                           void* ws, size_t ws_bytes, hipStream_t stream);
+gptq_status kv_cache_read(const gptq_kv_cache* kc, const gptq_kv_cache* vc, const int64_t* slots,
+                          int64_t tokens, void* K, int64_t k_token_stride, int64_t k_head_stride,
+                          void* V, int64_t v_token_stride, int64_t v_head_stride, gptq_dtype dt,
+                          int32_t* info, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Log probabilities of given tokens, entropy and top alternatives -- "Quantized
+ * deployment, 1.5 TB to 250 GB" (lmnt.cn news 123823), section 3.1 (perplexity,
+ * exp of the mean negative log probability, is how a quantized model is judged).
+ * For each row of logits[tokens, vocab] (row stride ldl, fp32 or bf16):
+ *   logprob[t] = log softmax(logits[t])[ids[t]]; 0 where ids[t] < 0 (a position
+ *                that is not asked for), NaN where ids[t] >= vocab
+ *   entropy[t] = -sum p log p in nats
+ *   top_ids[t][top], top_logprobs[t][top]: the `top` (0 .. 32, <= vocab) most
+ *                likely tokens in descending order, ties to the lower id
+ * fp32 sums in a fixed order.  -inf is a masked logit; a row of nothing else has
+ * logprob -inf and entropy 0 (its alternatives: the lowest ids, -inf).  A row
+ * that holds a NaN or +inf gives NaN throughout (ids rank NaN with -inf).
+ * ids with logprob, and entropy, may be NULL; top_ids and top_logprobs when
+ * top == 0.  Workspace: token_logprobs_workspace_size(tokens, vocab, top).
+ * ---------------------------------------------------------------------- */
+gptq_status token_logprobs_workspace_size(int64_t tokens, int64_t vocab, int32_t top,
+                                          size_t* bytes);
+gptq_status token_logprobs(const void* logits, gptq_dtype dt, int64_t tokens, int64_t vocab,
+                           int64_t ldl, const int64_t* ids, float* logprob, float* entropy,
+                           int32_t top, int32_t* top_ids, float* top_logprobs, void* ws,
+                           size_t ws_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

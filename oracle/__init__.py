@@ -60,3 +60,4 @@ from .pack import pack_ref, unpack_ref  # noqa: F401
 from .dequant import dequant_weights, dequant_matmul  # noqa: F401
 from . import stack  # noqa: F401,E402  (layer-sequential MLP stack)
 from . import awq  # noqa: F401,E402  (AWQ-lite scale search and clip)
+from . import lowp  # noqa: F401,E402  (e4m3 products, key/value cache, log probabilities)

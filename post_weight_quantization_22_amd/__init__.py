@@ -15,8 +15,17 @@ from ._lib import (  # noqa: F401
     awq_clip_quantize,
     awq_lite,
     awq_lite_workspace_size,
+    FP8_BLOCK,
+    fp8_gemm,
+    fp8_gemm_workspace_size,
+    fp8_linear,
+    fp8_linear_workspace_size,
+    fp8_quantize_blocks,
+    fp8_quantize_rows,
+    fp8_swiglu_quantize,
     GPTQConfig,
     GPTQError,
+    GPTQKVCache,
     GPTQ_ERR_WORKSPACE,
     GPTQ_NOALLOC_SCRATCH_BYTES,
     gptq_abi_version,
@@ -39,8 +48,14 @@ from ._lib import (  # noqa: F401
     gptq_residual_add,
     gptq_status_str,
     gptq_swiglu,
+    kv_cache_read,
+    kv_cache_write,
+    kv_cache_write_workspace_size,
     make_config,
+    make_kv_cache,
     rtn_minmax,
+    token_logprobs,
+    token_logprobs_workspace_size,
 )
 
 _lib.load()

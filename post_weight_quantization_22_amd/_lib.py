@@ -53,7 +53,25 @@ EXPORTED = (
     "rtn_minmax",
     "gptq_layer_error_workspace_size",
     "gptq_layer_error",
+    "fp8_quantize_rows",
+    "fp8_swiglu_quantize",
+    "fp8_quantize_blocks",
+    "fp8_gemm_workspace_size",
+    "fp8_gemm",
+    "fp8_linear_workspace_size",
+    "fp8_linear",
+    "kv_cache_write_workspace_size",
+    "kv_cache_write",
+    "kv_cache_read",
+    "token_logprobs_workspace_size",
+    "token_logprobs",
 )
+
+FP8_BLOCK = 128  # columns (and weight rows) that share a scale
+GPTQ_KV_INT4 = 0
+GPTQ_KV_INT8 = 1
+GPTQ_KV_E4M3 = 2
+_KV_FORMATS = {"int4": GPTQ_KV_INT4, "int8": GPTQ_KV_INT8, "e4m3": GPTQ_KV_E4M3}
 
 
 class GPTQConfig(ctypes.Structure):
@@ -65,6 +83,29 @@ class GPTQConfig(ctypes.Structure):
         ("desc_act", ctypes.c_int32),
         ("sym", ctypes.c_int32),
         ("static_groups", ctypes.c_int32),
+    ]
+
+
+class GPTQKVCache(ctypes.Structure):
+    """A quantized paged cache of keys or values (make_kv_cache builds one); it
+    keeps its tensors alive and may be kept for as long as they are in use."""
+
+    _fields_ = [
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("zeros", ctypes.c_void_p),
+        ("pages", ctypes.c_int64),
+        ("page_stride", ctypes.c_int64),
+        ("slot_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("param_page_stride", ctypes.c_int64),
+        ("param_slot_stride", ctypes.c_int64),
+        ("param_head_stride", ctypes.c_int64),
+        ("page_size", ctypes.c_int32),
+        ("heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("group_size", ctypes.c_int32),
+        ("format", ctypes.c_int32),
     ]
 
 
@@ -154,6 +195,36 @@ def load() -> ctypes.CDLL:
     lib.gptq_layer_error.restype = _i32
     lib.gptq_layer_error.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp,
                                      _i64, _vp, _vp, _sz, _vp]
+    lib.fp8_quantize_rows.restype = _i32
+    lib.fp8_quantize_rows.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp]
+    lib.fp8_swiglu_quantize.restype = _i32
+    lib.fp8_swiglu_quantize.argtypes = [_vp, _i64, _vp, _i64, _i32, _i64, _i64, _vp, _i64, _vp,
+                                        _i64, _vp]
+    lib.fp8_quantize_blocks.restype = _i32
+    lib.fp8_quantize_blocks.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp]
+    for name in ("fp8_gemm_workspace_size", "fp8_linear_workspace_size"):
+        getattr(lib, name).restype = _i32
+        getattr(lib, name).argtypes = [_i64, _i64, _i64, ctypes.POINTER(_sz)]
+    lib.fp8_gemm.restype = _i32
+    lib.fp8_gemm.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _vp,
+                             _i64, _vp, _i32, _i64, _vp, _sz, _vp]
+    lib.fp8_linear.restype = _i32
+    lib.fp8_linear.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i32,
+                               _i64, _vp, _sz, _vp]
+    _kvp = ctypes.POINTER(GPTQKVCache)
+    lib.kv_cache_write_workspace_size.restype = _i32
+    lib.kv_cache_write_workspace_size.argtypes = [_i64, _kvp, ctypes.POINTER(_sz)]
+    lib.kv_cache_write.restype = _i32
+    lib.kv_cache_write.argtypes = [_vp, _i64, _i64, _vp, _i64, _i64, _i32, _i64, _vp, _kvp, _kvp,
+                                   _vp, _vp, _sz, _vp]
+    lib.kv_cache_read.restype = _i32
+    lib.kv_cache_read.argtypes = [_kvp, _kvp, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i32,
+                                  _vp, _vp]
+    lib.token_logprobs_workspace_size.restype = _i32
+    lib.token_logprobs_workspace_size.argtypes = [_i64, _i64, _i32, ctypes.POINTER(_sz)]
+    lib.token_logprobs.restype = _i32
+    lib.token_logprobs.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _i32, _vp, _vp, _vp,
+                                   _sz, _vp]
     _lib = lib
     return lib
 
@@ -590,3 +661,304 @@ def gptq_layer_error(W, codes, scales, zeros, g_idx, S, err, ws=None, stream=Non
                                    _ptr(scales), _ptr(zeros), int(ng), _ptr(g_idx), _ptr(S),
                                    _ld(S), _ptr(err), _ptr(ws), nbytes, _stream(stream)),
            "gptq_layer_error")
+
+
+# ---------------------------------------------------------------------------
+# 8-bit floating point, the quantized cache, log probabilities
+# ---------------------------------------------------------------------------
+def _on_gpu(t, name: str):
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} is on {t.device}, expected a GPU tensor")
+    return t.device
+
+
+def _plane(t, name: str, rows: int, cols: int, kinds: str, device) -> int:
+    """Checks a 2-D operand (unit column stride, at least rows x cols, on
+    ``device``, a dtype among ``kinds``) and returns its row stride."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if _KIND.get(t.dtype) is None or _KIND[t.dtype] not in kinds:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    shape = t.shape
+    if len(shape) != 2 or shape[0] < rows or shape[1] < cols or (t.stride(1) != 1 and shape[1] > 1):
+        raise ValueError(f"{name}: expected a 2-D tensor of at least {rows} x {cols} with unit "
+                         f"column stride, got shape {tuple(shape)} strides {t.stride()}")
+    # the stride of a single row is not meaningful
+    return t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
+
+
+class _Kinds(dict):
+    """torch dtype -> one letter (filled on first use: this module does not
+    import torch before it is needed)."""
+
+    def get(self, key, default=None):
+        if not self:
+            import torch
+
+            self.update({torch.bfloat16: "b", torch.float32: "f", torch.float8_e4m3fn: "8",
+                         torch.uint8: "u", torch.int64: "l", torch.int32: "i"})
+        return super().get(key, default)
+
+
+_KIND = _Kinds()
+
+
+def _launch(name: str, device, stream, *args) -> None:
+    """Calls an entry point on ``stream`` (default: the current stream of the
+    tensors' device), with that device current."""
+    import torch
+
+    fn = getattr(_lib or load(), name)
+    index = device.index
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        if stream.device != device:
+            raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on {device}")
+        raw = stream.cuda_stream
+    if index == torch.cuda.current_device():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, raw)
+    if status != GPTQ_OK:
+        _check(status, name)
+
+
+def _space(name: str, ws, device, stream, *args):
+    """(pointer, bytes, tensor) of the caller's workspace, or of one for this call."""
+    if ws is None:
+        need = _sz(0)
+        _check(getattr(_lib or load(), name)(*args, ctypes.byref(need)), name)
+        ws = _workspace(need.value, device, stream)
+        return (None, 0, None) if ws is None else (ws.data_ptr(), need.value, ws)
+    if ws.device != device:
+        raise ValueError(f"ws is on {ws.device}, expected {device}")
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+
+
+def fp8_quantize_rows(X, codes, scales, stream=None) -> None:
+    """codes[tokens, n] (e4m3 or uint8) and scales[ceil(n / 128), tokens] (fp32) of
+    X[tokens, n] (bf16 or fp32): one scale per token and 128 columns."""
+    tokens, n = X.shape
+    d = _on_gpu(X, "X")
+    ldx = _plane(X, "X", tokens, n, "bf", d)
+    ldc = _plane(codes, "codes", tokens, n, "8u", d)
+    lds = _plane(scales, "scales", -(-n // FP8_BLOCK), tokens, "f", d)
+    _launch("fp8_quantize_rows", d, stream, X.data_ptr(), _dtype_code(X), tokens, n, ldx,
+            codes.data_ptr(), ldc, scales.data_ptr(), lds)
+
+
+def fp8_swiglu_quantize(gate, up, codes, scales, stream=None) -> None:
+    """fp8_quantize_rows of silu(gate) * up (both bf16 or both fp32, [tokens, n])."""
+    tokens, n = gate.shape
+    d = _on_gpu(gate, "gate")
+    ldg = _plane(gate, "gate", tokens, n, "bf", d)
+    ldu = _plane(up, "up", tokens, n, _KIND[gate.dtype], d)
+    ldc = _plane(codes, "codes", tokens, n, "8u", d)
+    lds = _plane(scales, "scales", -(-n // FP8_BLOCK), tokens, "f", d)
+    _launch("fp8_swiglu_quantize", d, stream, gate.data_ptr(), ldg, up.data_ptr(), ldu,
+            _dtype_code(gate), tokens, n, codes.data_ptr(), ldc, scales.data_ptr(), lds)
+
+
+def fp8_quantize_blocks(W, codes, scales, stream=None) -> None:
+    """codes[m, n] (e4m3 or uint8) and scales[ceil(m / 128), ceil(n / 128)] (fp32) of
+    W[m, n] (bf16 or fp32): one scale per 128 x 128 block."""
+    m, n = W.shape
+    d = _on_gpu(W, "W")
+    ldw = _plane(W, "W", m, n, "bf", d)
+    ldc = _plane(codes, "codes", m, n, "8u", d)
+    lds = _plane(scales, "scales", -(-m // FP8_BLOCK), -(-n // FP8_BLOCK), "f", d)
+    _launch("fp8_quantize_blocks", d, stream, W.data_ptr(), _dtype_code(W), m, n, ldw,
+            codes.data_ptr(), ldc, scales.data_ptr(), lds)
+
+
+def fp8_gemm_workspace_size(tokens: int, m: int, n: int) -> int:
+    out = _sz(0)
+    _check(load().fp8_gemm_workspace_size(tokens, m, n, ctypes.byref(out)),
+           "fp8_gemm_workspace_size")
+    return out.value
+
+
+def fp8_linear_workspace_size(tokens: int, m: int, n: int) -> int:
+    out = _sz(0)
+    _check(load().fp8_linear_workspace_size(tokens, m, n, ctypes.byref(out)),
+           "fp8_linear_workspace_size")
+    return out.value
+
+
+def fp8_gemm(X, xscales, W, wscales, Y, residual=None, ws=None, stream=None) -> None:
+    """Y[tokens, m] (fp32 or bf16) = X W^T of block-scaled e4m3 operands: X[tokens, n] with
+    xscales[ceil(n / 128), tokens], W[m, n] with wscales[ceil(m / 128), ceil(n / 128)]; plus
+    residual[tokens, m] (Y's type, may be Y) where it is given."""
+    tokens, n = X.shape
+    m = W.shape[0]
+    d = _on_gpu(X, "X")
+    nb = -(-n // FP8_BLOCK)
+    ldx = _plane(X, "X", tokens, n, "8u", d)
+    ldxs = _plane(xscales, "xscales", nb, tokens, "f", d)
+    ldw = _plane(W, "W", m, n, "8u", d)
+    ldws = _plane(wscales, "wscales", -(-m // FP8_BLOCK), nb, "f", d)
+    ldy = _plane(Y, "Y", tokens, m, "bf", d)
+    ldr = 0 if residual is None else _plane(residual, "residual", tokens, m, _KIND[Y.dtype], d)
+    p, nbytes, ws = _space("fp8_gemm_workspace_size", ws, d, stream, tokens, m, n)
+    _launch("fp8_gemm", d, stream, X.data_ptr(), tokens, n, ldx, xscales.data_ptr(), ldxs,
+            W.data_ptr(), m, ldw, wscales.data_ptr(), ldws, _ptr(residual), ldr, Y.data_ptr(),
+            _dtype_code(Y), ldy, p, nbytes)
+
+
+def fp8_linear(X, W, wscales, Y, ws=None, stream=None) -> None:
+    """Y[tokens, m] (fp32 or bf16) = X W^T with X[tokens, n] (bf16 or fp32) quantized as by
+    fp8_quantize_rows and W[m, n] e4m3 with wscales[ceil(m / 128), ceil(n / 128)]."""
+    tokens, n = X.shape
+    m = W.shape[0]
+    d = _on_gpu(X, "X")
+    ldx = _plane(X, "X", tokens, n, "bf", d)
+    ldw = _plane(W, "W", m, n, "8u", d)
+    ldws = _plane(wscales, "wscales", -(-m // FP8_BLOCK), -(-n // FP8_BLOCK), "f", d)
+    ldy = _plane(Y, "Y", tokens, m, "bf", d)
+    p, nbytes, ws = _space("fp8_linear_workspace_size", ws, d, stream, tokens, m, n)
+    _launch("fp8_linear", d, stream, X.data_ptr(), _dtype_code(X), tokens, n, ldx, W.data_ptr(), m,
+            ldw, wscales.data_ptr(), ldws, Y.data_ptr(), _dtype_code(Y), ldy, p, nbytes)
+
+
+def make_kv_cache(codes, scales, zeros, head_dim: int, fmt: str = "int8",
+                  group_size: int = 128) -> GPTQKVCache:
+    """The handle of a paged cache of keys or of values.
+
+    codes: uint8 [pages, page_size, heads, bytes], bytes = head_dim (int8, e4m3) or
+    head_dim / 2 (int4); scales: fp32 [pages, page_size, heads, groups]; zeros: uint8 of the
+    scales' shape and strides (integers with zero-points), or None.  Pages, slots and heads
+    may lie in any order; the last dimension is dense."""
+    if fmt not in _KV_FORMATS:
+        raise ValueError(f"fmt: {fmt!r}, expected one of {tuple(_KV_FORMATS)}")
+    head_dim, group_size = int(head_dim), int(group_size)
+    d = _on_gpu(codes, "codes")
+    nbytes = head_dim // 2 if fmt == "int4" else head_dim
+    groups = 1 if group_size <= 0 else -(-head_dim // group_size)
+    if _KIND.get(codes.dtype) not in ("u", "8"):
+        raise TypeError(f"codes: unsupported dtype {codes.dtype}")
+    if _KIND.get(scales.dtype) != "f":
+        raise TypeError(f"scales: dtype {scales.dtype}, expected float32")
+    if codes.dim() != 4 or codes.shape[3] != nbytes or codes.stride(3) != 1:
+        raise ValueError(f"codes: shape {tuple(codes.shape)} strides {codes.stride()}, expected "
+                         f"[pages, page_size, heads, {nbytes}] with a dense last dimension")
+    pages, page_size, heads = codes.shape[:3]
+    want = (pages, page_size, heads, groups)
+    for t, name in ((scales, "scales"), (zeros, "zeros")):
+        if t is None:
+            continue
+        if t.device != d:
+            raise ValueError(f"{name} is on {t.device}, expected {d}")
+        if tuple(t.shape) != want or (t.stride(3) != 1 and groups > 1):
+            raise ValueError(f"{name}: shape {tuple(t.shape)} strides {t.stride()}, expected "
+                             f"{want} with a dense last dimension")
+    if zeros is not None:
+        if fmt == "e4m3":
+            raise ValueError("zeros: e4m3 has none")
+        if _KIND.get(zeros.dtype) != "u":
+            raise TypeError(f"zeros: dtype {zeros.dtype}, expected uint8")
+        if zeros.stride()[:3] != scales.stride()[:3]:
+            raise ValueError("zeros must have the strides of scales")
+    cs, ps = codes.stride(), scales.stride()
+    c = GPTQKVCache(codes.data_ptr(), scales.data_ptr(),
+                    None if zeros is None else zeros.data_ptr(), pages, cs[0], cs[1], cs[2], ps[0],
+                    ps[1], ps[2], page_size, heads, head_dim, group_size, _KV_FORMATS[fmt])
+    c.tensors = (codes, scales, zeros)
+    return c
+
+
+def _kv_rows(t, name: str, cache: Optional[GPTQKVCache], tokens: int, device, dtype):
+    """(pointer, token stride, head stride) of rows [tokens, heads, head_dim]."""
+    if cache is None:
+        if t is not None:
+            raise ValueError(f"{name} is given without its cache")
+        return None, 0, 0
+    if t is None:
+        raise ValueError(f"{name} is required: its cache is given")
+    if cache.tensors[0].device != device or t.device != device:
+        raise ValueError(f"{name}: rows on {t.device}, cache on {cache.tensors[0].device}, "
+                         f"expected {device}")
+    if t.dtype != dtype or _KIND.get(dtype) not in ("b", "f"):
+        raise TypeError(f"{name}: dtype {t.dtype}, expected bfloat16 or float32 for keys and "
+                        "values alike")
+    if tuple(t.shape) != (tokens, cache.heads, cache.head_dim) or t.stride(2) != 1:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} strides {t.stride()}, expected "
+                         f"{(tokens, cache.heads, cache.head_dim)} with a dense last dimension")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _kv_call(K, V, slots, kc, vc, info):
+    rows = K if K is not None else V
+    if rows is None or (kc is None and vc is None):
+        raise ValueError("keys with their cache or values with theirs are required")
+    d = _on_gpu(slots, "slots")
+    if _KIND.get(slots.dtype) != "l" or slots.dim() != 1 or not slots.is_contiguous():
+        raise ValueError("slots: expected a contiguous 1-D int64 tensor")
+    _buf(info, "info", (1,), ("int32",), d)
+    tokens = slots.shape[0]
+    k = _kv_rows(K, "K", kc, tokens, d, rows.dtype)
+    v = _kv_rows(V, "V", vc, tokens, d, rows.dtype)
+    if kc is not None and vc is not None and (kc.pages != vc.pages
+                                              or kc.page_size != vc.page_size):
+        raise ValueError("the two caches differ in pages or page_size")
+    return (d, tokens, k, v, _dtype_code(rows), None if kc is None else ctypes.byref(kc),
+            None if vc is None else ctypes.byref(vc))
+
+
+def kv_cache_write_workspace_size(tokens: int, cache: GPTQKVCache) -> int:
+    out = _sz(0)
+    _check(load().kv_cache_write_workspace_size(tokens, ctypes.byref(cache), ctypes.byref(out)),
+           "kv_cache_write_workspace_size")
+    return out.value
+
+
+def kv_cache_write(K, V, slots, kc, vc, info=None, ws=None, stream=None) -> None:
+    """Quantize rows K, V [tokens, heads, head_dim] (bf16 or fp32) into slots[tokens] (int64,
+    negative: padding, not written) of the caches kc, vc (either may be None with its rows)."""
+    d, tokens, k, v, dt, pk, pv = _kv_call(K, V, slots, kc, vc, info)
+    p, nbytes, ws = _space("kv_cache_write_workspace_size", ws, d, stream, tokens, pk or pv)
+    _launch("kv_cache_write", d, stream, *k, *v, dt, tokens, slots.data_ptr(), pk, pv, _ptr(info),
+            p, nbytes)
+
+
+def kv_cache_read(kc, vc, slots, K, V, info=None, stream=None) -> None:
+    """Rows K, V [tokens, heads, head_dim] (bf16 or fp32) = the caches' values at slots[tokens]
+    (int64, negative: zeros)."""
+    d, tokens, k, v, dt, pk, pv = _kv_call(K, V, slots, kc, vc, info)
+    _launch("kv_cache_read", d, stream, pk, pv, slots.data_ptr(), tokens, *k, *v, dt, _ptr(info))
+
+
+def token_logprobs_workspace_size(tokens: int, vocab: int, top: int) -> int:
+    out = _sz(0)
+    _check(load().token_logprobs_workspace_size(tokens, vocab, top, ctypes.byref(out)),
+           "token_logprobs_workspace_size")
+    return out.value
+
+
+def token_logprobs(logits, ids, logprob, entropy=None, top_ids=None, top_logprobs=None, ws=None,
+                   stream=None) -> None:
+    """For each row of logits[tokens, vocab] (bf16 or fp32): logprob[tokens] of ids[tokens]
+    (int64, negative: not asked for, 0; either both or neither given), entropy[tokens], and the
+    top alternatives top_ids (int32) and top_logprobs [tokens, top], top <= 32."""
+    tokens, vocab = logits.shape
+    d = _on_gpu(logits, "logits")
+    ldl = _plane(logits, "logits", tokens, vocab, "bf", d)
+    _buf(ids, "ids", (tokens,), ("int64",), d, optional=logprob is None)
+    _buf(logprob, "logprob", (tokens,), ("float32",), d, optional=ids is None)
+    _buf(entropy, "entropy", (tokens,), ("float32",), d)
+    top = 0
+    if top_ids is not None or top_logprobs is not None:
+        if top_ids is None or top_ids.dim() != 2:
+            raise ValueError("top_ids: expected [tokens, top] together with top_logprobs")
+        top = top_ids.shape[1]
+        _buf(top_ids, "top_ids", (tokens, top), ("int32",), d)
+        _buf(top_logprobs, "top_logprobs", (tokens, top), ("float32",), d, optional=False)
+    p, nbytes, ws = _space("token_logprobs_workspace_size", ws, d, stream, tokens, vocab, top)
+    _launch("token_logprobs", d, stream, logits.data_ptr(), _dtype_code(logits), tokens, vocab,
+            ldl, _ptr(ids), _ptr(logprob), _ptr(entropy), top, _ptr(top_ids), _ptr(top_logprobs),
+            p, nbytes)

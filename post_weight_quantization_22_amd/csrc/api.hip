@@ -26,6 +26,57 @@ gptq_status check_ws(void* ws, size_t ws_bytes, size_t need) {
   return GPTQ_OK;
 }
 
+// what fp8_gemm and fp8_linear share; GPTQ_OK also where there is nothing to do
+gptq_status fp8_operands_ok(int64_t tokens, int64_t n, const void* W, int64_t m, int64_t ldw,
+                            const float* wscales, int64_t ldws, const void* Y, int ydt,
+                            int64_t ldy) {
+  if (bad_dim(tokens) || bad_dim(m) || n <= 0 || bad_dim(n) || !valid_dtype(ydt))
+    return GPTQ_ERR_INVALID_ARG;
+  if (n % 16 != 0) return GPTQ_ERR_UNSUPPORTED;
+  if (tokens == 0 || m == 0) return GPTQ_OK;
+  if (!W || !wscales || !Y || ldw < n || ldw % 16 != 0 || ldy < m ||
+      (reinterpret_cast<uintptr_t>(W) & 15) != 0 || ldws < ceil_div(n, int64_t(128)))
+    return GPTQ_ERR_INVALID_ARG;
+  // offsets within a tile are 32-bit
+  return ldw >= (int64_t(1) << 24) ? GPTQ_ERR_UNSUPPORTED : GPTQ_OK;
+}
+
+gptq_status kv_cache_ok(const gptq_kv_cache* c, int64_t tokens) {
+  if (!c || !c->codes || !c->scales || c->pages <= 0 || c->page_size <= 0 || c->heads <= 0 ||
+      c->head_dim <= 0 || c->pages > (int64_t(1) << 40) / c->page_size)
+    return GPTQ_ERR_INVALID_ARG;
+  if (c->format != GPTQ_KV_INT4 && c->format != GPTQ_KV_INT8 && c->format != GPTQ_KV_E4M3)
+    return GPTQ_ERR_INVALID_ARG;
+  const int32_t g = c->group_size;
+  if (g != -1 && (g < 16 || g > 512 || (g & (g - 1)) != 0)) return GPTQ_ERR_INVALID_ARG;
+  if (c->head_dim % 8 != 0 || c->head_dim > 1024 || (g == -1 && c->head_dim > 512) ||
+      c->heads > 65536)
+    return GPTQ_ERR_UNSUPPORTED;
+  const int a = c->format == GPTQ_KV_INT4 ? 4 : 8;
+  if ((reinterpret_cast<uintptr_t>(c->codes) % a) != 0 || c->page_stride % a != 0 ||
+      c->slot_stride % a != 0 || c->head_stride % a != 0)
+    return GPTQ_ERR_INVALID_ARG;
+  // a token's lanes: at most twice its 8-value chunks (a short last group)
+  if (tokens * c->heads * (c->head_dim / 8) * 2 >= (int64_t(1) << 31)) return GPTQ_ERR_UNSUPPORTED;
+  return GPTQ_OK;
+}
+
+gptq_status kv_call_ok(const void* K, const void* V, int dt, int64_t tokens, const int64_t* slots,
+                       const gptq_kv_cache* kc, const gptq_kv_cache* vc) {
+  if (bad_dim(tokens) || !valid_dtype(dt) || (!kc && !vc)) return GPTQ_ERR_INVALID_ARG;
+  for (const gptq_kv_cache* c : {kc, vc})
+    if (c) {
+      const gptq_status ok = kv_cache_ok(c, tokens);
+      if (ok != GPTQ_OK) return ok;
+    }
+  if (kc && vc && (kc->pages != vc->pages || kc->page_size != vc->page_size))
+    return GPTQ_ERR_INVALID_ARG;
+  if (tokens == 0) return GPTQ_OK;
+  if (!slots || (K != nullptr) != (kc != nullptr) || (V != nullptr) != (vc != nullptr))
+    return GPTQ_ERR_INVALID_ARG;
+  return GPTQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -316,6 +367,149 @@ gptq_status rtn_minmax(const void* W, gptq_dtype wdt, int64_t m, int64_t n, int6
   if (!W || !codes || !scales || !zeros || ldw < n) return GPTQ_ERR_INVALID_ARG;
   return hip_status(launch_rtn(W, wdt, m, n, ldw, bits, group_size, sym, codes, scales, zeros,
                                stream));
+}
+
+gptq_status fp8_quantize_rows(const void* X, gptq_dtype xdt, int64_t tokens, int64_t n,
+                              int64_t ldx, uint8_t* codes, int64_t ldc, float* scales,
+                              int64_t lds, hipStream_t stream) {
+  if (tokens < 0 || bad_dim(tokens) || n <= 0 || bad_dim(n) || !valid_dtype(xdt))
+    return GPTQ_ERR_INVALID_ARG;
+  if (tokens == 0) return GPTQ_OK;
+  if (!X || !codes || !scales || ldx < n || ldc < n || lds < tokens) return GPTQ_ERR_INVALID_ARG;
+  return hip_status(launch_fp8_rows(X, ldx, nullptr, 0, xdt, tokens, n, codes, ldc, scales, lds,
+                                    stream));
+}
+
+gptq_status fp8_swiglu_quantize(const void* gate, int64_t ldg, const void* up, int64_t ldu,
+                                gptq_dtype dt, int64_t tokens, int64_t n, uint8_t* codes,
+                                int64_t ldc, float* scales, int64_t lds, hipStream_t stream) {
+  if (tokens < 0 || bad_dim(tokens) || n <= 0 || bad_dim(n) || !valid_dtype(dt))
+    return GPTQ_ERR_INVALID_ARG;
+  if (tokens == 0) return GPTQ_OK;
+  if (!gate || !up || !codes || !scales || ldg < n || ldu < n || ldc < n || lds < tokens)
+    return GPTQ_ERR_INVALID_ARG;
+  return hip_status(launch_fp8_rows(gate, ldg, up, ldu, dt, tokens, n, codes, ldc, scales, lds,
+                                    stream));
+}
+
+gptq_status fp8_quantize_blocks(const void* W, gptq_dtype wdt, int64_t m, int64_t n, int64_t ldw,
+                                uint8_t* codes, int64_t ldc, float* scales, int64_t lds,
+                                hipStream_t stream) {
+  if (m < 0 || bad_dim(m) || n <= 0 || bad_dim(n) || !valid_dtype(wdt))
+    return GPTQ_ERR_INVALID_ARG;
+  if (m == 0) return GPTQ_OK;
+  if (!W || !codes || !scales || ldw < n || ldc < n || lds < ceil_div(n, int64_t(128)))
+    return GPTQ_ERR_INVALID_ARG;
+  return hip_status(launch_fp8_blocks(W, wdt, m, n, ldw, codes, ldc, scales, lds, stream));
+}
+
+gptq_status fp8_gemm_workspace_size(int64_t tokens, int64_t m, int64_t n, size_t* bytes) {
+  if (!bytes || tokens < 0 || bad_dim(tokens) || m < 0 || bad_dim(m) || n <= 0 || bad_dim(n))
+    return GPTQ_ERR_INVALID_ARG;
+  *bytes = tokens == 0 || m == 0 ? 0 : fp8_gemm_ws_bytes(tokens, m, n);
+  return GPTQ_OK;
+}
+
+gptq_status fp8_linear_workspace_size(int64_t tokens, int64_t m, int64_t n, size_t* bytes) {
+  if (!bytes || tokens < 0 || bad_dim(tokens) || m < 0 || bad_dim(m) || n <= 0 || bad_dim(n))
+    return GPTQ_ERR_INVALID_ARG;
+  *bytes = tokens == 0 || m == 0 ? 0 : fp8_linear_ws_bytes(tokens, m, n);
+  return GPTQ_OK;
+}
+
+gptq_status fp8_gemm(const uint8_t* X, int64_t tokens, int64_t n, int64_t ldx, const float* xs,
+                     int64_t ldxs, const uint8_t* W, int64_t m, int64_t ldw, const float* wscales,
+                     int64_t ldws, const void* R, int64_t ldr, void* Y, gptq_dtype ydt,
+                     int64_t ldy, void* ws, size_t ws_bytes, hipStream_t stream) {
+  const gptq_status ok = fp8_operands_ok(tokens, n, W, m, ldw, wscales, ldws, Y, ydt, ldy);
+  if (ok != GPTQ_OK || tokens == 0 || m == 0) return ok;
+  if (!X || !xs || ldx < n || ldx % 16 != 0 || (reinterpret_cast<uintptr_t>(X) & 15) != 0 ||
+      ldxs < tokens || (R && ldr < m) || (R == Y && ldr != ldy))
+    return GPTQ_ERR_INVALID_ARG;
+  if (ldx >= (int64_t(1) << 24)) return GPTQ_ERR_UNSUPPORTED;
+  const gptq_status w = check_ws(ws, ws_bytes, fp8_gemm_ws_bytes(tokens, m, n));
+  if (w != GPTQ_OK) return w;
+  Fp8GemmArgs g{X, ldx, tokens, n, xs, ldxs, W, ldw, m, wscales, ldws, Y, ydt, ldy, R, ldr, ws};
+  return hip_status(launch_fp8_gemm(g, stream));
+}
+
+gptq_status fp8_linear(const void* X, gptq_dtype xdt, int64_t tokens, int64_t n, int64_t ldx,
+                       const uint8_t* W, int64_t m, int64_t ldw, const float* wscales,
+                       int64_t ldws, void* Y, gptq_dtype ydt, int64_t ldy, void* ws,
+                       size_t ws_bytes, hipStream_t stream) {
+  const gptq_status ok = fp8_operands_ok(tokens, n, W, m, ldw, wscales, ldws, Y, ydt, ldy);
+  if (ok != GPTQ_OK) return ok;
+  if (!valid_dtype(xdt)) return GPTQ_ERR_INVALID_ARG;
+  if (tokens == 0 || m == 0) return GPTQ_OK;
+  if (!X || ldx < n) return GPTQ_ERR_INVALID_ARG;
+  const gptq_status w = check_ws(ws, ws_bytes, fp8_linear_ws_bytes(tokens, m, n));
+  if (w != GPTQ_OK) return w;
+  // the codes lie at the workspace's start and are read 16 bytes at a time
+  if ((reinterpret_cast<uintptr_t>(ws) & 15) != 0) return GPTQ_ERR_INVALID_ARG;
+  Fp8GemmArgs g{nullptr, 0, tokens, n, nullptr, 0, W, ldw, m, wscales, ldws, Y, ydt, ldy,
+                nullptr, 0, nullptr};
+  return hip_status(launch_fp8_linear(X, xdt, ldx, g, ws, stream));
+}
+
+gptq_status kv_cache_write_workspace_size(int64_t tokens, const gptq_kv_cache* cache,
+                                          size_t* bytes) {
+  if (!bytes || tokens < 0 || bad_dim(tokens)) return GPTQ_ERR_INVALID_ARG;
+  const gptq_status ok = kv_cache_ok(cache, tokens);
+  if (ok != GPTQ_OK) return ok;
+  *bytes = kv_write_ws_bytes(tokens, cache->pages * cache->page_size);
+  return GPTQ_OK;
+}
+
+gptq_status kv_cache_write(const void* K, int64_t k_token_stride, int64_t k_head_stride,
+                           const void* V, int64_t v_token_stride, int64_t v_head_stride,
+                           gptq_dtype dt, int64_t tokens, const int64_t* slots,
+                           const gptq_kv_cache* kc, const gptq_kv_cache* vc, int32_t* info,
+                           void* ws, size_t ws_bytes, hipStream_t stream) {
+  const gptq_status ok = kv_call_ok(K, V, dt, tokens, slots, kc, vc);
+  if (ok != GPTQ_OK || tokens == 0) return ok;
+  const gptq_kv_cache* c = kc ? kc : vc;
+  const gptq_status w = check_ws(ws, ws_bytes, kv_write_ws_bytes(tokens, c->pages * c->page_size));
+  if (w != GPTQ_OK) return w;
+  const KvRows k{const_cast<void*>(K), k_token_stride, k_head_stride};
+  const KvRows v{const_cast<void*>(V), v_token_stride, v_head_stride};
+  return hip_status(launch_kv_write(k, v, dt, tokens, slots, kc, vc, info, ws, stream));
+}
+
+gptq_status kv_cache_read(const gptq_kv_cache* kc, const gptq_kv_cache* vc, const int64_t* slots,
+                          int64_t tokens, void* K, int64_t k_token_stride, int64_t k_head_stride,
+                          void* V, int64_t v_token_stride, int64_t v_head_stride, gptq_dtype dt,
+                          int32_t* info, hipStream_t stream) {
+  const gptq_status ok = kv_call_ok(K, V, dt, tokens, slots, kc, vc);
+  if (ok != GPTQ_OK || tokens == 0) return ok;
+  const KvRows k{K, k_token_stride, k_head_stride}, v{V, v_token_stride, v_head_stride};
+  return hip_status(launch_kv_read(kc, vc, slots, tokens, k, v, dt, info, stream));
+}
+
+gptq_status token_logprobs_workspace_size(int64_t tokens, int64_t vocab, int32_t top,
+                                          size_t* bytes) {
+  if (!bytes || tokens < 0 || bad_dim(tokens) || vocab <= 0 || bad_dim(vocab) || top < 0 ||
+      top > 32 || top > vocab)
+    return GPTQ_ERR_INVALID_ARG;
+  *bytes = tokens == 0 ? 0 : logprobs_ws_bytes(tokens, vocab, top);
+  return GPTQ_OK;
+}
+
+gptq_status token_logprobs(const void* logits, gptq_dtype dt, int64_t tokens, int64_t vocab,
+                           int64_t ldl, const int64_t* ids, float* logprob, float* entropy,
+                           int32_t top, int32_t* top_ids, float* top_logprobs, void* ws,
+                           size_t ws_bytes, hipStream_t stream) {
+  if (tokens < 0 || bad_dim(tokens) || vocab <= 0 || bad_dim(vocab) || !valid_dtype(dt) ||
+      top < 0 || top > 32 || top > vocab)
+    return GPTQ_ERR_INVALID_ARG;
+  if (tokens == 0) return GPTQ_OK;
+  if (!logits || ldl < vocab || (ids != nullptr) != (logprob != nullptr) ||
+      (top > 0 && (!top_ids || !top_logprobs)))
+    return GPTQ_ERR_INVALID_ARG;
+  const gptq_status w = check_ws(ws, ws_bytes, logprobs_ws_bytes(tokens, vocab, top));
+  if (w != GPTQ_OK) return w;
+  if ((reinterpret_cast<uintptr_t>(ws) & 15) != 0) return GPTQ_ERR_INVALID_ARG;
+  return hip_status(launch_logprobs(logits, dt, tokens, vocab, ldl, ids, logprob, entropy, top,
+                                    top_ids, top_logprobs, ws, stream));
 }
 
 }  // extern "C"

@@ -115,4 +115,59 @@ hipError_t launch_swiglu(const float* G, int64_t ldg, const float* U, int64_t ld
 hipError_t launch_residual_add(const void* X, int64_t ldx, const float* Y, int64_t ldy,
                                int64_t rows, int64_t n, void* O, int64_t ldo, hipStream_t stream);
 
+// ---- fp8_quantize.hip -----------------------------------------------------
+// e4m3 codes of X (times silu-gated X2: gate X, up X2, when X2 is not null) with
+// a scale per row and 128 columns, scales [ceil(n / 128)][lds]
+hipError_t launch_fp8_rows(const void* X, int64_t ldx, const void* X2, int64_t ldx2, int dt,
+                           int64_t tokens, int64_t n, uint8_t* codes, int64_t ldc, float* scales,
+                           int64_t lds, hipStream_t stream);
+// e4m3 codes of W with a scale per 128 x 128 block, scales [ceil(m / 128)][lds]
+hipError_t launch_fp8_blocks(const void* W, int dt, int64_t m, int64_t n, int64_t ldw,
+                             uint8_t* codes, int64_t ldc, float* scales, int64_t lds,
+                             hipStream_t stream);
+
+// ---- fp8_gemm.hip ---------------------------------------------------------
+struct Fp8GemmArgs {
+  const uint8_t* X;  // [tokens, ldx]
+  int64_t ldx, tokens, n;
+  const float* sx;  // [ceil(n / 128)][lds]
+  int64_t lds;
+  const uint8_t* W;  // [m, ldw]
+  int64_t ldw, m;
+  const float* sw;  // [ceil(m / 128)][ldsw]
+  int64_t ldsw;
+  void* Y;
+  int ydt;
+  int64_t ldy;
+  const void* R;  // [tokens, ldr] of Y's type, added to the product; may be null, may be Y
+  int64_t ldr;
+  void* ws;
+};
+size_t fp8_gemm_ws_bytes(int64_t tokens, int64_t m, int64_t n);
+hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, hipStream_t stream);
+// quantizes X into the workspace and multiplies (g's X, ldx, sx, lds are not read)
+size_t fp8_linear_ws_bytes(int64_t tokens, int64_t m, int64_t n);
+hipError_t launch_fp8_linear(const void* X, int xdt, int64_t ldx, const Fp8GemmArgs& g, void* ws,
+                             hipStream_t stream);
+
+// ---- kv_cache.hip ---------------------------------------------------------
+// rows [tokens][heads][head_dim] of a cache, in elements
+struct KvRows {
+  void* p;  // may be null: that cache is not touched
+  int64_t token_stride, head_stride;
+};
+size_t kv_write_ws_bytes(int64_t tokens, int64_t slots);
+hipError_t launch_kv_write(const KvRows& k, const KvRows& v, int dt, int64_t tokens,
+                           const int64_t* slots, const gptq_kv_cache* kc, const gptq_kv_cache* vc,
+                           int32_t* info, void* ws, hipStream_t stream);
+hipError_t launch_kv_read(const gptq_kv_cache* kc, const gptq_kv_cache* vc, const int64_t* slots,
+                          int64_t tokens, const KvRows& k, const KvRows& v, int dt, int32_t* info,
+                          hipStream_t stream);
+
+// ---- logprobs.hip ---------------------------------------------------------
+size_t logprobs_ws_bytes(int64_t tokens, int64_t vocab, int top);
+hipError_t launch_logprobs(const void* X, int dt, int64_t tokens, int64_t vocab, int64_t ldx,
+                           const int64_t* ids, float* logprob, float* entropy, int top,
+                           int32_t* top_ids, float* top_logprobs, void* ws, hipStream_t stream);
+
 }  // namespace gptq

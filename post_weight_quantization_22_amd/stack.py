@@ -187,3 +187,90 @@ def quantize_stack(x0: torch.Tensor, weights: Sequence[Tuple[torch.Tensor, torch
         blocks.append(QuantizedBlock(gate, up, down, x if keep else None, h if keep else None))
         x = x_next
     return blocks, x
+
+
+# ---------------------------------------------------------------------------
+# The same stack in 8-bit floating point: weights and activations in e4m3 with
+# a scale per 128 x 128 block and per token and 128 columns ("AWQ, MinMax, GPTQ
+# calibration in Model Optimizer", section 2: the max calibrator needs no
+# calibration data, so a layer's weights are quantized on their own).
+#
+#     x8 = e4m3(x)                     fp8_quantize_rows
+#     g = x8 Wg8^T, u = x8 Wu8^T       fp8_gemm, bf16
+#     h8 = e4m3(silu(g) * u)           fp8_swiglu_quantize
+#     x' = bf16(x + h8 Wd8^T)          fp8_gemm with x as its residual
+#
+# g and u are held in bf16: half a step of 2^-8 relative, before h is rounded to
+# e4m3's 2^-4; the activations between the products then take half the bytes.
+# ---------------------------------------------------------------------------
+@dataclasses.dataclass
+class Fp8Layer:
+    codes: torch.Tensor   # e4m3 [m, n], row stride a multiple of 16
+    scales: torch.Tensor  # fp32 [ceil(m / 128), ceil(n / 128)]
+
+
+@dataclasses.dataclass
+class Fp8Block:
+    gate: Fp8Layer
+    up: Fp8Layer
+    down: Fp8Layer
+
+
+def quantize_layer_fp8(W: torch.Tensor, stream=None) -> Fp8Layer:
+    """W[m, n] (bf16 or fp32) as e4m3 codes and block scales."""
+    m, n = W.shape
+    ld = -(-n // 16) * 16
+    codes = torch.empty((m, ld), dtype=torch.float8_e4m3fn, device=W.device)[:, :n]
+    scales = torch.empty((-(-m // _lib.FP8_BLOCK), -(-n // _lib.FP8_BLOCK)), dtype=torch.float32,
+                         device=W.device)
+    _lib.fp8_quantize_blocks(W, codes, scales, stream=stream)
+    return Fp8Layer(codes, scales)
+
+
+def forward_block_fp8(x: torch.Tensor, block: Fp8Block, out: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """x' [tokens, d] (bf16) of one block for x [tokens, d] (bf16); d and f multiples of 16.
+    Enqueued on ``stream`` (default: the current stream of x's device)."""
+    if stream is None:
+        stream = torch.cuda.current_stream(x.device)
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"x: dtype {x.dtype}, expected bfloat16")
+    T, d = x.shape
+    f = block.gate.codes.shape[0]
+    with torch.cuda.stream(stream):  # the buffers between the steps belong to the stream
+        def buf(rows, cols, dtype):
+            return torch.empty((rows, cols), dtype=dtype, device=x.device)
+
+        if out is None:
+            out = buf(T, d, torch.bfloat16)
+        x8, xs = buf(T, d, torch.float8_e4m3fn), buf(-(-d // _lib.FP8_BLOCK), T, torch.float32)
+        _lib.fp8_quantize_rows(x, x8, xs)
+        g, u = buf(T, f, torch.bfloat16), buf(T, f, torch.bfloat16)
+        _lib.fp8_gemm(x8, xs, block.gate.codes, block.gate.scales, g)
+        _lib.fp8_gemm(x8, xs, block.up.codes, block.up.scales, u)
+        h8, hs = buf(T, f, torch.float8_e4m3fn), buf(-(-f // _lib.FP8_BLOCK), T, torch.float32)
+        _lib.fp8_swiglu_quantize(g, u, h8, hs)
+        _lib.fp8_gemm(h8, hs, block.down.codes, block.down.scales, out, residual=x)
+    return out
+
+
+def quantize_stack_fp8(x0: torch.Tensor, weights: Sequence[Tuple[torch.Tensor, torch.Tensor,
+                                                                 torch.Tensor]],
+                       chunk_tokens: int = 16384, stream=None
+                       ) -> Tuple[List[Fp8Block], torch.Tensor]:
+    """Quantize every block of the stack to e4m3 and carry x0 (bf16 [tokens, d]) through it;
+    returns the blocks and the quantized network's output activations."""
+    if stream is None:
+        stream = torch.cuda.current_stream(x0.device)
+    blocks = []
+    x = x0
+    for ws in weights:
+        with torch.cuda.stream(stream):
+            block = Fp8Block(*(quantize_layer_fp8(W, stream) for W in ws))
+            x_next = torch.empty_like(x)
+            for t0 in range(0, x.shape[0], chunk_tokens):
+                t1 = min(x.shape[0], t0 + chunk_tokens)
+                forward_block_fp8(x[t0:t1], block, x_next[t0:t1], stream)
+        blocks.append(block)
+        x = x_next
+    return blocks, x
