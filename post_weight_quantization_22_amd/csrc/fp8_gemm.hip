@@ -35,6 +35,7 @@ struct GemmArgs {
   int ybf16;
   const void* R;  // residual of Y's type, or null
   int64_t ldr;
+  float* part;  // [ks][tokens][m], K splits only
   int64_t nb, ntm, ntt;  // blocks of n, tiles of weight rows and of tokens
 };
 
@@ -54,18 +55,6 @@ __device__ __forceinline__ bf16x8 to_bf16(int lo, int hi) {
   return u.v;
 }
 
-// The block's products of 16 weight rows and 16 tokens, summed with fp32
-// accuracy.  Lane l holds 32 codes of weight row (token) l % 16, the same k on
-// both sides; the result's lane l holds weight rows 4 (l / 16) + e, token l % 16.
-__device__ __forceinline__ f32x4 block_exact(i32x8 w, i32x8 x) {
-  f32x4 d = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(to_bf16(w[2 * i], w[2 * i + 1]),
-                                                to_bf16(x[2 * i], x[2 * i + 1]), d, 0, 0, 0);
-  return d;
-}
-
 __device__ __forceinline__ void store4(const GemmArgs& a, int64_t t, int64_t r, f32x4 v) {
   if (t >= a.tokens) return;
 #pragma unroll
@@ -82,47 +71,248 @@ __device__ __forceinline__ void store4(const GemmArgs& a, int64_t t, int64_t r, 
   }
 }
 
-// 64 weight rows x 64 tokens a workgroup, 4 waves of 16 weight rows, operands
-// straight from global memory.
-__global__ __launch_bounds__(256) void fp8_gemm_direct_kernel(GemmArgs a) {
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+// ---------------------------------------------------------------------------
+// Tiles of TM weight rows x TT tokens, WM x WT waves of MI x NJ 16 x 16 results.
+// A block (128 columns, one scale) of both operands arrives by LDS DMA in rows of
+// 128 bytes whose 16-byte segments are XOR-swizzled by the row, two buffers: block
+// c + 1 is on its way while block c is multiplied.  The results lie transposed
+// (weight rows along a lane's registers), so that a lane has one token a column
+// tile: one scale product per column tile and block, then one fma an element.
+// Rows past the end are re-read from the last one and their results dropped; past
+// n the last block's segments re-read the row's last ones and meet zeros in X.
+constexpr int kRow = 128;  // bytes of a row of a block
+constexpr int64_t kXcds = 8;
+
+__device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
+
+// the 8-bit instruction: k = 128, the block, from a zero accumulator
+__device__ __forceinline__ f32x4 block_fast(i32x8 w, i32x8 x) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0,
+                                                          0, 0, 0);
+}
+
+struct Bf32 {
+  bf16x8 k[4];
+};
+
+__device__ __forceinline__ Bf32 widen(i32x8 v) {
+  Bf32 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o.k[i] = to_bf16(v[2 * i], v[2 * i + 1]);
+  return o;
+}
+
+template <int TM, int TT, int WM, int WT, bool EXACT>
+__global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a) {
+  constexpr int MI = TM / WM / 16, NJ = TT / WT / 16, NW = WM * WT;
+  constexpr int W_BYTES = TM * kRow, X_BYTES = TT * kRow, STAGE = W_BYTES + X_BYTES;
+  static_assert(TM % (8 * NW) == 0 && TT % (8 * NW) == 0, "each wave fills whole 8-row pieces");
+  static_assert(TM / WM <= kFp8Block, "a wave's rows share their scales");
+  __shared__ __align__(16) uint8_t smem[2 * STAGE];
+
+  // tiles in runs per XCD; within a run, groups of 4 token tiles walked before the
+  // next row tile, so that the workgroups of an XCD share both operands in its L2
+  const int64_t ntiles = a.ntm * a.ntt, b = blockIdx.x;
+  const int64_t xcd = b % kXcds, idx = b / kXcds;
+  const int64_t per = ntiles / kXcds, rem = ntiles % kXcds;
+  if (idx >= per + (xcd < rem ? 1 : 0)) return;
+  const int64_t L = xcd * per + (xcd < rem ? xcd : rem) + idx;
+  const int64_t grp = L / (4 * a.ntm), in = L - grp * 4 * a.ntm;
+  const int64_t gsz = min((int64_t)4, a.ntt - 4 * grp);
+  const int64_t tok0 = (4 * grp + in % gsz) * TT, row0 = in / gsz * TM;
+  // the split's blocks
+  const int nb = (int)a.nb, ks = gridDim.y, z = blockIdx.y;
+  const int c0 = (int)((int64_t)nb * z / ks), c1 = (int)((int64_t)nb * (z + 1) / ks);
+
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wv / WT, wt = wv % WT;
   const int q = lane >> 4, l16 = lane & 15;
-  const int64_t row0 = (int64_t)blockIdx.x * 64 + 16 * wv, tok0 = (int64_t)blockIdx.y * 64;
-  const int64_t wr = row0 + l16 < a.m ? row0 + l16 : a.m - 1;
-  const uint8_t* w = a.W + wr * a.ldw;
-  const int64_t swrow = (row0 < a.m ? row0 : a.m - 1) / kFp8Block * a.ldsw;
-  f32x4 acc[4];
-  for (int j = 0; j < 4; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto ld = [&](const uint8_t* row, int64_t k0) {
-    i32x8 v;
-    for (int h = 0; h < 2; ++h) {
-      const int64_t k = k0 + 32 * q + 16 * h;
-      i32x4 u = {0, 0, 0, 0};
-      if (k < a.n) u = *reinterpret_cast<const i32x4*>(row + k);
-      for (int e = 0; e < 4; ++e) v[4 * h + e] = u[e];
-    }
-    return v;
+  const int n = (int)a.n;
+  const int rmax = (int)min((int64_t)TM - 1, a.m - 1 - row0);
+  const int tmax = (int)min((int64_t)TT - 1, a.tokens - 1 - tok0);
+  const uint8_t* wbase = a.W + row0 * a.ldw;
+  const uint8_t* xbase = a.X + tok0 * a.ldx;
+  const uint32_t lds0 = lds_addr(smem);
+
+  // lane l of a DMA lands on row l / 8, physical segment l % 8 of an 8-row piece,
+  // so it loads the logical segment (l % 8) ^ swz(row)
+  auto src = [&](int row, int last, int64_t ld, int k0) -> uint32_t {
+    const int sg = 16 * ((lane & 7) ^ swz(row));
+    const int at = k0 + kRow > n ? min(sg, n - 16 - k0) : sg;
+    return (uint32_t)(min(row, last) * ld + at);
   };
-  for (int64_t b = 0; b < a.nb; ++b) {
-    const i32x8 wf = ld(w, b * kFp8Block);
-    const float sw = a.sw[swrow + b];
+  auto issue = [&](int c) {
+    const int k0 = c * kRow;
+    const uint32_t dst = lds0 + ((c - c0) & 1) * STAGE;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t t = tok0 + 16 * j + l16;
-      const int64_t tc = t < a.tokens ? t : a.tokens - 1;
-      const f32x4 d = block_exact(wf, ld(a.X + tc * a.ldx, b * kFp8Block));
-      const float s = a.sx[b * a.lds + tc] * sw;
+    for (int j = 0; j < TM / 8 / NW; ++j) {
+      const int piece = wv * (TM / 8 / NW) + j;
+      lds_dma16(wbase + k0, src(8 * piece + (lane >> 3), rmax, a.ldw, k0), dst + 1024 * piece);
+    }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(d[e], s, acc[j][e]);
+    for (int j = 0; j < TT / 8 / NW; ++j) {
+      const int piece = wv * (TT / 8 / NW) + j;
+      lds_dma16(xbase + k0, src(8 * piece + (lane >> 3), tmax, a.ldx, k0),
+                dst + W_BYTES + 1024 * piece);
+    }
+  };
+  // the scales of this lane's tokens, times the weights' one
+  const float* sxp[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+    sxp[j] = a.sx + tok0 + min(16 * (wt * NJ + j) + l16, tmax);
+  const int64_t wrow = row0 + wm * (TM / WM);
+  const float* swp = a.sw + (wrow < a.m ? wrow : a.m - 1) / kFp8Block * a.ldsw;
+
+  const int seg0 = (q ^ swz(l16)) << 4, seg1 = ((4 + q) ^ swz(l16)) << 4;
+  auto frag = [&](const uint8_t* st, int row) {
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(st + row * kRow + seg0);
+    const i32x4 hi = *reinterpret_cast<const i32x4*>(st + row * kRow + seg1);
+    return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  };
+
+  f32x4 acc[MI][NJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  float sx[NJ], sw;
+  issue(c0);
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) sx[j] = sxp[j][c0 * a.lds];
+  sw = swp[c0];
+  for (int c = c0; c < c1; ++c) {
+    float s[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) s[j] = sx[j] * sw;
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's share of block c is there
+    __syncthreads();                     // everyone's, and block c - 1 has been read
+    uint8_t* st = smem + ((c - c0) & 1) * STAGE;
+    if (c + 1 < c1) {
+      issue(c + 1);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) sx[j] = sxp[j][(c + 1) * a.lds];
+      sw = swp[c + 1];
+    } else if ((c + 1) * kRow > n) {  // the row's end: zeros in X past it
+      for (int i = threadIdx.x; i < TT * 8; i += NW * 64) {
+        const int row = i >> 3, sg = i & 7;
+        if (c * kRow + 16 * sg >= n)
+          *reinterpret_cast<i32x4*>(st + W_BYTES + row * kRow + ((sg ^ swz(row)) << 4)) =
+              i32x4{0, 0, 0, 0};
+      }
+      __syncthreads();
+    }
+    if (EXACT) {
+      Bf32 x[NJ];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) x[j] = widen(frag(st + W_BYTES, 16 * (wt * NJ + j) + l16));
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const Bf32 w = widen(frag(st, wm * (TM / WM) + 16 * i + l16));
+        f32x4 d[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) d[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            d[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.k[k], x[j].k[k], d[j], 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[j][e], s[j], acc[i][j][e]);
+      }
+    } else {
+      i32x8 x[NJ];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) x[j] = frag(st + W_BYTES, 16 * (wt * NJ + j) + l16);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const i32x8 w = frag(st, wm * (TM / WM) + 16 * i + l16);
+        f32x4 d[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) d[j] = block_fast(w, x[j]);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[j][e], s[j], acc[i][j][e]);
+      }
     }
   }
+  if (ks > 1) {
+    float* part = a.part + z * a.tokens * a.m;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) store4(a, tok0 + 16 * j + l16, row0 + 4 * q, acc[j]);
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int64_t t = tok0 + 16 * (wt * NJ + j) + l16, r = wrow + 16 * i + 4 * q;
+        if (t >= a.tokens) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (r + e < a.m) part[t * a.m + r + e] = acc[i][j][e];
+      }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      store4(a, tok0 + 16 * (wt * NJ + j) + l16, wrow + 16 * i + 4 * q, acc[i][j]);
+}
+
+// Y = R + the splits' partial sums in their order, 4 outputs of a row a lane.
+__global__ __launch_bounds__(256) void fp8_gemm_reduce_kernel(GemmArgs a, int ks) {
+  const int64_t per_row = (a.m + 3) / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.tokens * per_row) return;
+  const int64_t t = i / per_row, r = 4 * (i - t * per_row);
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  for (int z = 0; z < ks; ++z) {
+    const float* p = a.part + (z * a.tokens + t) * a.m + r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (r + e < a.m) v[e] += p[e];
+  }
+  store4(a, t, r, v);
+}
+
+// How a product is cut: tile, and K splits where the tiles do not fill the chip.
+struct Plan {
+  int tile;  // 256, 128 or 64 tokens
+  int ks;
+};
+
+Plan plan_of(int64_t tokens, int64_t m, int64_t n, bool exact) {
+  const int64_t nb = ceil_div(n, (int64_t)kFp8Block);
+  Plan p;
+  const int64_t t256 = ceil_div(tokens, (int64_t)256) * ceil_div(m, (int64_t)256);
+  p.tile = !exact && t256 >= 160 ? 256 : 128;
+  p.ks = 1;
+  if (p.tile == 128) {
+    const int64_t tiles = ceil_div(tokens, (int64_t)128) * ceil_div(m, (int64_t)128);
+    p.ks = (int)hmax(1, hmin(hmin(512 / tiles, nb / 4), 16));
+  }
+  return p;
+}
+
+template <int TM, int TT, int WM, int WT, bool EXACT>
+void launch_tile(GemmArgs a, int ks, hipStream_t stream) {
+  a.ntm = ceil_div(a.m, (int64_t)TM);
+  a.ntt = ceil_div(a.tokens, (int64_t)TT);
+  const int64_t grid = ceil_div(a.ntm * a.ntt, kXcds) * kXcds;
+  hipLaunchKernelGGL((fp8_gemm_tile_kernel<TM, TT, WM, WT, EXACT>), dim3((unsigned)grid, (unsigned)ks),
+                     dim3(WM * WT * 64), 0, stream, a);
 }
 
 }  // namespace
 
-size_t fp8_gemm_ws_bytes(int64_t, int64_t, int64_t) { return 0; }
+size_t fp8_gemm_ws_bytes(int64_t tokens, int64_t m, int64_t n) {
+  // either type of Y
+  const Plan e = plan_of(tokens, m, n, true), f = plan_of(tokens, m, n, false);
+  const int ks = e.ks > f.ks ? e.ks : f.ks;
+  return ks == 1 ? 0 : (size_t)ks * tokens * m * 4;
+}
 
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, hipStream_t stream) {
   GemmArgs a;
@@ -132,19 +322,17 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, hipStream_t stream) {
   a.sw = g.sw; a.ldsw = g.ldsw;
   a.Y = g.Y; a.ldy = g.ldy; a.ybf16 = g.ydt == GPTQ_BF16;
   a.R = g.R; a.ldr = g.ldr;
+  a.part = static_cast<float*>(g.ws);
   a.nb = ceil_div(g.n, (int64_t)kFp8Block);
-  a.ntm = ceil_div(g.m, (int64_t)64);
-  a.ntt = ceil_div(g.tokens, (int64_t)64);
-  const int64_t per = 65535;
-  for (int64_t t0 = 0; t0 < a.ntt; t0 += per) {
-    GemmArgs p = a;
-    p.X = a.X + t0 * 64 * a.ldx;
-    p.sx = a.sx + t0 * 64;
-    p.tokens = a.tokens - t0 * 64;
-    p.Y = reinterpret_cast<char*>(a.Y) + t0 * 64 * a.ldy * (a.ybf16 ? 2 : 4);
-    if (a.R) p.R = reinterpret_cast<const char*>(a.R) + t0 * 64 * a.ldr * (a.ybf16 ? 2 : 4);
-    const dim3 grid((unsigned)a.ntm, (unsigned)hmin(a.ntt - t0, per));
-    hipLaunchKernelGGL(fp8_gemm_direct_kernel, grid, dim3(256), 0, stream, p);
+  const bool exact = !a.ybf16;
+  const Plan p = plan_of(g.tokens, g.m, g.n, exact);
+  if (p.tile == 256) launch_tile<256, 256, 2, 4, false>(a, 1, stream);
+  else if (exact) launch_tile<128, 128, 2, 2, true>(a, p.ks, stream);
+  else launch_tile<128, 128, 2, 2, false>(a, p.ks, stream);
+  if (p.ks > 1) {
+    const int64_t total = g.tokens * ceil_div(g.m, (int64_t)4);
+    hipLaunchKernelGGL(fp8_gemm_reduce_kernel, dim3((unsigned)ceil_div(total, (int64_t)256)), dim3(256), 0,
+                       stream, a, p.ks);
   }
   return hipGetLastError();
 }
