@@ -262,6 +262,177 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
       store4(a, tok0 + 16 * (wt * NJ + j) + l16, wrow + 16 * i + 4 * q, acc[i][j]);
 }
 
+// ---------------------------------------------------------------------------
+// Decode batches (at most 32 tokens): bound by the weights' HBM stream.  A
+// workgroup of 8 waves owns 16 RT weight rows over the whole K range, so nothing
+// is split across workgroups and no second kernel joins sums; the waves take
+// every eighth block, their sums meet in LDS in wave order.  A lane loads the
+// weights and codes of its matrix operand straight into registers (segments q
+// and q + 4 of row l % 16 of the block: an instruction covers 64 bytes of 16
+// rows), D blocks ahead.  SRC says where the activations come from: codes in
+// memory, or bf16 / fp32 rows that the workgroup quantizes into LDS itself while
+// its first weights are on their way (few tokens: every workgroup repeats that).
+constexpr int SRC_CODES = -1;
+constexpr int kGemvWaves = 8;
+
+struct GemvArgs {
+  GemmArgs g;
+  const void* src;  // bf16 or fp32 rows, fused quantization only
+  int64_t ldsrc;
+  int vec;
+};
+
+template <int NT, int RT, int SRC>
+__global__ __launch_bounds__(kGemvWaves * 64) void fp8_gemv_kernel(GemvArgs v) {
+  const GemmArgs& a = v.g;
+  constexpr int D = RT * (SRC == SRC_CODES ? NT : 1) == 1 ? 4 : 2;  // by the registers
+  extern __shared__ __align__(16) uint8_t dyn[];
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane >> 4, l16 = lane & 15;
+  const int nb = (int)a.nb, n = (int)a.n, T = (int)a.tokens;
+  const int64_t row0 = (int64_t)blockIdx.x * 16 * RT;
+  const uint8_t* wp[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+    wp[i] = a.W + min(row0 + 16 * i + l16, a.m - 1) * a.ldw;
+  const float* swp = a.sw + row0 / kFp8Block * a.ldsw;
+  // past n the row's last segment is read again and meets zeros in X
+  auto load = [&](const uint8_t* p, int c) -> i32x8 {
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(p + min(kRow * c + 16 * q, n - 16));
+    const i32x4 hi = *reinterpret_cast<const i32x4*>(p + min(kRow * c + 16 * q + 64, n - 16));
+    return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  };
+  struct Blk {
+    i32x8 w[RT], x[SRC == SRC_CODES ? NT : 1];
+    float sw, sx[SRC == SRC_CODES ? NT : 1];
+  };
+  const uint8_t* xp[NT];
+  const float* sxp[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int t = min(16 * j + l16, T - 1);
+    xp[j] = a.X + t * a.ldx;
+    sxp[j] = a.sx + t;
+  }
+  auto fetch = [&](int c) {
+    Blk o;
+    const int cc = min(c, nb - 1);  // past the end: re-read, never used
+#pragma unroll
+    for (int i = 0; i < RT; ++i) o.w[i] = load(wp[i], cc);
+    o.sw = swp[cc];
+    if (SRC == SRC_CODES) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        o.x[j] = load(xp[j], cc);
+        o.sx[j] = sxp[j][cc * a.lds];
+      }
+    }
+    return o;
+  };
+
+  Blk cur[D];
+#pragma unroll
+  for (int d = 0; d < D; ++d) cur[d] = fetch(wv + kGemvWaves * d);
+
+  // fused: codes [T][nb * 128 + 32], then scales [T][nb]
+  const int xrow = nb * kRow + 32;
+  float* xs = reinterpret_cast<float*>(dyn + T * xrow);
+  if (SRC != SRC_CODES) {
+    constexpr int DT = SRC == GPTQ_BF16 ? GPTQ_BF16 : GPTQ_F32;
+    constexpr int esz = DT == GPTQ_BF16 ? 2 : 4;
+    for (int u = threadIdx.x >> 4; u < T * nb; u += kGemvWaves * 4) {
+      const int t = u / nb, b = u - t * nb, c0 = b * kRow + 8 * l16;
+      const Vals8 x =
+          load_vals8<DT>(reinterpret_cast<const char*>(v.src) + t * v.ldsrc * esz, c0, n, v.vec);
+      float am = amax_finite8(x);
+#pragma unroll
+      for (int off = 1; off < 16; off <<= 1) am = fmaxf(am, __shfl_xor(am, off, 16));
+      const float s = e4m3_scale(am);
+      *reinterpret_cast<uint2*>(dyn + t * xrow + c0) = e4m3_codes8(x, s, 1.0f / s);
+      if (l16 == 0) xs[t * nb + b] = s;
+    }
+    __syncthreads();
+  }
+
+  f32x4 acc[RT][NT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int c = wv; c < nb; c += kGemvWaves * D) {
+    Blk nxt[D];
+    if (c + kGemvWaves * D < nb) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) nxt[d] = fetch(c + kGemvWaves * (D + d));
+    }
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int cd = c + kGemvWaves * d;
+      if (cd >= nb) break;
+      // (before the block's first matrix instruction: with this branch between one
+      // and the reader of its result, the compiler left out the wait states that
+      // the reader needs on the path that takes the branch)
+      if (SRC == SRC_CODES && kRow * (cd + 1) > n) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (kRow * cd + 16 * q + (e < 4 ? 0 : 64) >= n) cur[d].x[j][e] = 0;
+      }
+      Bf32 w[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) w[i] = widen(cur[d].w[i]);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        Bf32 x;
+        float s;
+        if (SRC == SRC_CODES) {
+          x = widen(cur[d].x[j]);
+          s = cur[d].sx[j] * cur[d].sw;
+        } else {
+          const int t = min(16 * j + l16, T - 1);
+          const uint8_t* p = dyn + t * xrow + kRow * cd + 16 * q;
+          const i32x4 lo = *reinterpret_cast<const i32x4*>(p);
+          const i32x4 hi = *reinterpret_cast<const i32x4*>(p + 64);
+          x = widen(i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+          s = xs[t * nb + cd] * cur[d].sw;
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          f32x4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i].k[k], x.k[k], p, 0, 0, 0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], s, acc[i][j][e]);
+        }
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < D; ++d) cur[d] = nxt[d];
+  }
+  // the waves' sums in wave order (the activations' LDS is reused)
+  __syncthreads();
+  f32x4* part = reinterpret_cast<f32x4*>(dyn);
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) part[((wv * RT + i) * NT + j) * 64 + lane] = acc[i][j];
+  __syncthreads();
+  if (wv < RT * NT) {
+    f32x4 sum = part[wv * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < kGemvWaves; ++w) {
+      const f32x4 p = part[(w * RT * NT + wv) * 64 + lane];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += p[e];
+    }
+    const int i = wv / NT, j = wv % NT;
+    store4(a, 16 * j + l16, row0 + 16 * i + 4 * q, sum);
+  }
+}
+
 // Y = R + the splits' partial sums in their order, 4 outputs of a row a lane.
 __global__ __launch_bounds__(256) void fp8_gemm_reduce_kernel(GemmArgs a, int ks) {
   const int64_t per_row = (a.m + 3) / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -275,6 +446,34 @@ __global__ __launch_bounds__(256) void fp8_gemm_reduce_kernel(GemmArgs a, int ks
       if (r + e < a.m) v[e] += p[e];
   }
   store4(a, t, r, v);
+}
+
+// Decode batches go through fp8_gemv_kernel.
+constexpr int64_t kGemvTokens = 32;
+
+// 32 weight rows a workgroup (the activations' codes read half as often) where
+// that still gives one to every CU
+template <int SRC>
+hipError_t launch_gemv(const GemvArgs& v, size_t lds, hipStream_t stream) {
+  constexpr bool codes = SRC == SRC_CODES;  // only these come with more than 16 tokens
+  const int nt = codes && v.g.tokens > 16 ? 2 : 1, rt = v.g.m >= 8192 ? 2 : 1;
+  lds = lds > (size_t)kGemvWaves * rt * nt * 1024 ? lds : (size_t)kGemvWaves * rt * nt * 1024;
+  const dim3 grid((unsigned)ceil_div(v.g.m, (int64_t)16 * rt)), block(kGemvWaves * 64);
+  if (nt == 1 && rt == 1)
+    hipLaunchKernelGGL((fp8_gemv_kernel<1, 1, SRC>), grid, block, lds, stream, v);
+  else if (nt == 1)
+    hipLaunchKernelGGL((fp8_gemv_kernel<1, 2, SRC>), grid, block, lds, stream, v);
+  else if (rt == 1)
+    hipLaunchKernelGGL((fp8_gemv_kernel<codes ? 2 : 1, 1, SRC>), grid, block, lds, stream, v);
+  else
+    hipLaunchKernelGGL((fp8_gemv_kernel<codes ? 2 : 1, 2, SRC>), grid, block, lds, stream, v);
+  return hipGetLastError();
+}
+
+// Few enough activations that every workgroup quantizes them itself (and their
+// codes fit its LDS): no kernel before the product.
+bool quantizes_itself(int64_t tokens, int64_t n) {
+  return tokens <= 16 && tokens * (ceil_div(n, (int64_t)kFp8Block) * (kRow + 4) + 32) <= 32768;
 }
 
 // How a product is cut: tile, and K splits where the tiles do not fill the chip.
@@ -308,13 +507,14 @@ void launch_tile(GemmArgs a, int ks, hipStream_t stream) {
 }  // namespace
 
 size_t fp8_gemm_ws_bytes(int64_t tokens, int64_t m, int64_t n) {
+  if (tokens <= kGemvTokens) return 0;
   // either type of Y
   const Plan e = plan_of(tokens, m, n, true), f = plan_of(tokens, m, n, false);
   const int ks = e.ks > f.ks ? e.ks : f.ks;
   return ks == 1 ? 0 : (size_t)ks * tokens * m * 4;
 }
 
-hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, hipStream_t stream) {
+static GemmArgs gemm_args(const Fp8GemmArgs& g) {
   GemmArgs a;
   a.X = g.X; a.ldx = g.ldx; a.tokens = g.tokens; a.n = g.n;
   a.sx = g.sx; a.lds = g.lds;
@@ -324,6 +524,12 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, hipStream_t stream) {
   a.R = g.R; a.ldr = g.ldr;
   a.part = static_cast<float*>(g.ws);
   a.nb = ceil_div(g.n, (int64_t)kFp8Block);
+  return a;
+}
+
+hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, hipStream_t stream) {
+  const GemmArgs a = gemm_args(g);
+  if (g.tokens <= kGemvTokens) return launch_gemv<SRC_CODES>(GemvArgs{a, nullptr, 0, 0}, 0, stream);
   const bool exact = !a.ybf16;
   const Plan p = plan_of(g.tokens, g.m, g.n, exact);
   if (p.tile == 256) launch_tile<256, 256, 2, 4, false>(a, 1, stream);
@@ -341,6 +547,7 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, hipStream_t stream) {
 static int64_t linear_ldc(int64_t n) { return (n + 127) / 128 * 128; }
 
 size_t fp8_linear_ws_bytes(int64_t tokens, int64_t m, int64_t n) {
+  if (quantizes_itself(tokens, n)) return 0;
   return align_up((size_t)tokens * linear_ldc(n), 256) +
          align_up((size_t)ceil_div(n, (int64_t)kFp8Block) * tokens * 4, 256) +
          fp8_gemm_ws_bytes(tokens, m, n);
@@ -349,6 +556,14 @@ size_t fp8_linear_ws_bytes(int64_t tokens, int64_t m, int64_t n) {
 hipError_t launch_fp8_linear(const void* X, int xdt, int64_t ldx, const Fp8GemmArgs& g, void* ws,
                              hipStream_t stream) {
   Fp8GemmArgs p = g;
+  if (quantizes_itself(g.tokens, g.n)) {
+    GemvArgs v{gemm_args(g), X, ldx, 0};
+    const int per16 = xdt == GPTQ_BF16 ? 8 : 4;
+    v.vec = (reinterpret_cast<uintptr_t>(X) & 15) == 0 && ldx % per16 == 0;
+    const size_t lds = (size_t)(g.tokens * (v.g.nb * (kRow + 4) + 32));
+    return xdt == GPTQ_BF16 ? launch_gemv<GPTQ_BF16>(v, lds, stream)
+                            : launch_gemv<GPTQ_F32>(v, lds, stream);
+  }
   uint8_t* codes = static_cast<uint8_t*>(ws);
   const int64_t ldc = linear_ldc(g.n);
   float* sx = reinterpret_cast<float*>(codes + align_up((size_t)g.tokens * ldc, 256));

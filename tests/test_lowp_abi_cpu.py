@@ -64,9 +64,10 @@ def test_products():
     assert linear(n=40) == UNSUP
     for kw in (dict(X=None), dict(dt=5), dict(ldx=255), dict(ws=FAKE + 4)):
         assert linear(**kw) == BAD, kw
-    assert linear(nbytes=16) == WS and linear(ws=None) == WS
-    assert gq.fp8_linear_workspace_size(4, 8, 256) >= 4 * 256
+    assert linear(t=100, nbytes=16) == WS and linear(t=100, ws=None) == WS
+    assert gq.fp8_linear_workspace_size(100, 8, 256) >= 100 * 256
     assert gq.fp8_linear_workspace_size(0, 8, 256) == 0
+    assert gq.fp8_linear_workspace_size(1, 8, 4096) == 0  # quantized inside the product
     with pytest.raises(gq.GPTQError):
         gq.fp8_gemm_workspace_size(4, 8, 0)
 
