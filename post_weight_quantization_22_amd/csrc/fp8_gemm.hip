@@ -178,6 +178,13 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+  f32x4 dp[NJ];
+  float sp[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    dp[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    sp[j] = 0.f;
+  }
   float sx[NJ], sw;
   issue(c0);
 #pragma unroll
@@ -225,21 +232,39 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
           for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[j][e], s[j], acc[i][j][e]);
       }
     } else {
+      // a row tile's fmas run under the next one's matrix instructions; the last
+      // one's under the first of the next block
       i32x8 x[NJ];
 #pragma unroll
       for (int j = 0; j < NJ; ++j) x[j] = frag(st + W_BYTES, 16 * (wt * NJ + j) + l16);
+      i32x8 w = frag(st, wm * (TM / WM) + l16);
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
-        const i32x8 w = frag(st, wm * (TM / WM) + 16 * i + l16);
+        i32x8 wn = w;
+        if (i + 1 < MI) wn = frag(st, wm * (TM / WM) + 16 * (i + 1) + l16);
         f32x4 d[NJ];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) d[j] = block_fast(w, x[j]);
+        for (int j = 0; j < NJ; ++j) {
+          d[j] = block_fast(w, x[j]);
+          const int ip = i > 0 ? i - 1 : MI - 1;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
+          for (int e = 0; e < 4; ++e)
+            acc[ip][j][e] = fmaf(dp[j][e], i > 0 ? s[j] : sp[j], acc[ip][j][e]);
+          __builtin_amdgcn_sched_barrier(0);  // keeps the two streams interleaved
+        }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[j][e], s[j], acc[i][j][e]);
+        for (int j = 0; j < NJ; ++j) dp[j] = d[j];
+        w = wn;
       }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) sp[j] = s[j];
     }
+  }
+  if (!EXACT) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[MI - 1][j][e] = fmaf(dp[j][e], sp[j], acc[MI - 1][j][e]);
   }
   if (ks > 1) {
     float* part = a.part + z * a.tokens * a.m;
