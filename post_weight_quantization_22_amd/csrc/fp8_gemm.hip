@@ -35,12 +35,14 @@ struct GemmArgs {
   int ybf16;
   const void* R;  // residual of Y's type, or null
   int64_t ldr;
+  int vec4;  // rows of Y and R start on 4-element borders
   float* part;  // [ks][tokens][m], K splits only
   int64_t nb, ntm, ntt;  // blocks of n, tiles of weight rows and of tokens
 };
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
 // 8 e4m3 codes as bf16
 __device__ __forceinline__ bf16x8 to_bf16(int lo, int hi) {
@@ -55,20 +57,50 @@ __device__ __forceinline__ bf16x8 to_bf16(int lo, int hi) {
   return u.v;
 }
 
+// Y[t, r .. r + 3] = R + v, in one access where a.vec4 allows (rows of Y and R on
+// 4-element borders)
 __device__ __forceinline__ void store4(const GemmArgs& a, int64_t t, int64_t r, f32x4 v) {
-  if (t >= a.tokens) return;
+  if (t >= a.tokens || r >= a.m) return;
+  const int64_t o = t * a.ldy + r, ro = t * a.ldr + r;
+  if (a.vec4 && r + 4 <= a.m) {
+    if (a.ybf16) {
+      if (a.R) {
+        const bf16x4 res = *reinterpret_cast<const bf16x4*>(static_cast<const __bf16*>(a.R) + ro);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += (float)res[e];
+      }
+      bf16x4 y;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = (__bf16)v[e];
+      *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(a.Y) + o) = y;
+    } else {
+      if (a.R) v += *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.R) + ro);
+      *reinterpret_cast<f32x4*>(static_cast<float*>(a.Y) + o) = v;
+    }
+    return;
+  }
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     if (r + e >= a.m) continue;
     if (a.ybf16) {
-      const float res =
-          a.R ? (float)reinterpret_cast<const __bf16*>(a.R)[t * a.ldr + r + e] : 0.0f;
-      reinterpret_cast<__bf16*>(a.Y)[t * a.ldy + r + e] = (__bf16)(res + v[e]);
+      const float res = a.R ? (float)static_cast<const __bf16*>(a.R)[ro + e] : 0.0f;
+      static_cast<__bf16*>(a.Y)[o + e] = (__bf16)(v[e] + res);
     } else {
-      const float res = a.R ? reinterpret_cast<const float*>(a.R)[t * a.ldr + r + e] : 0.0f;
-      reinterpret_cast<float*>(a.Y)[t * a.ldy + r + e] = res + v[e];
+      const float res = a.R ? static_cast<const float*>(a.R)[ro + e] : 0.0f;
+      static_cast<float*>(a.Y)[o + e] = v[e] + res;
     }
   }
+}
+
+// a split's partial sums of 4 weight rows, `left` of them inside
+__device__ __forceinline__ void store_part(float* p, int64_t left, int64_t m, f32x4 v) {
+  if (left >= 4 && m % 4 == 0) {
+    *reinterpret_cast<f32x4*>(p) = v;
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (e < left) p[e] = v[e];
 }
 
 // ---------------------------------------------------------------------------
@@ -80,6 +112,15 @@ __device__ __forceinline__ void store4(const GemmArgs& a, int64_t t, int64_t r, 
 // tile: one scale product per column tile and block, then one fma an element.
 // Rows past the end are re-read from the last one and their results dropped; past
 // n the last block's segments re-read the row's last ones and meet zeros in X.
+//
+// What bounds the 256 x 256 tile is LDS: a block is 2048 matrix cycles, 192 KB of
+// operand reads and 64 KB of DMA.  So that the three run beside each other
+//  - a wave issues its DMA one instruction at a time between matrix instructions
+//    (all at once they hold it behind the CU's address unit);
+//  - the fmas of a row tile stand between the next one's matrix instructions, and
+//    the last one's between the first of the next block;
+//  - no branch comes between matrix instructions: past the last block the last
+//    one is fetched again into buffers that nothing reads.
 constexpr int kRow = 128;  // bytes of a row of a block
 constexpr int64_t kXcds = 8;
 
@@ -102,13 +143,21 @@ __device__ __forceinline__ Bf32 widen(i32x8 v) {
   return o;
 }
 
+// a scalar load (uniform p, memory that this kernel does not write)
+__device__ __forceinline__ float const_load(const float* p) {
+  return *(const __attribute__((address_space(4))) float*)(uintptr_t)p;
+}
+
 template <int TM, int TT, int WM, int WT, bool EXACT>
 __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a) {
   constexpr int MI = TM / WM / 16, NJ = TT / WT / 16, NW = WM * WT;
   constexpr int W_BYTES = TM * kRow, X_BYTES = TT * kRow, STAGE = W_BYTES + X_BYTES;
-  static_assert(TM % (8 * NW) == 0 && TT % (8 * NW) == 0, "each wave fills whole 8-row pieces");
-  static_assert(TM / WM <= kFp8Block, "a wave's rows share their scales");
-  __shared__ __align__(16) uint8_t smem[2 * STAGE];
+  constexpr int PW = TM / 8 / NW, PX = TT / 8 / NW;  // a wave's DMA instructions, 8 rows each
+  static_assert(PW % 2 == 0 || PW == 1, "the swizzle of a piece goes by its parity");
+  static_assert(PX % 2 == 0 || PX == 1, "the swizzle of a piece goes by its parity");
+  static_assert(TM / WM <= kFp8Block && kFp8Block % (TM / WM) == 0, "a wave's rows share a scale");
+  static_assert(TT % 64 == 0 && TT / 64 <= NW, "a wave fetches the scales of 64 tokens");
+  __shared__ __align__(16) uint8_t smem[2 * STAGE + 2 * TT * 4];
 
   // tiles in runs per XCD; within a run, groups of 4 token tiles walked before the
   // next row tile, so that the workgroups of an XCD share both operands in its L2
@@ -137,31 +186,25 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
 
   // lane l of a DMA lands on row l / 8, physical segment l % 8 of an 8-row piece,
   // so it loads the logical segment (l % 8) ^ swz(row)
-  auto src = [&](int row, int last, int64_t ld, int k0) -> uint32_t {
-    const int sg = 16 * ((lane & 7) ^ swz(row));
-    const int at = k0 + kRow > n ? min(sg, n - 16 - k0) : sg;
-    return (uint32_t)(min(row, last) * ld + at);
+  auto issue = [&](const uint8_t* base, int64_t ld, int last, int piece0, int j, int c,
+                   uint32_t dst) {
+    const int k0 = c * kRow, row = 8 * (piece0 + j) + (lane >> 3);
+    const int sg = min(16 * ((lane & 7) ^ swz(row)), n - 16 - k0);
+    lds_dma16(base + k0, __umul24(min(row, last), (uint32_t)ld) + sg, dst + 1024 * (piece0 + j));
   };
-  auto issue = [&](int c) {
-    const int k0 = c * kRow;
-    const uint32_t dst = lds0 + ((c - c0) & 1) * STAGE;
-#pragma unroll
-    for (int j = 0; j < TM / 8 / NW; ++j) {
-      const int piece = wv * (TM / 8 / NW) + j;
-      lds_dma16(wbase + k0, src(8 * piece + (lane >> 3), rmax, a.ldw, k0), dst + 1024 * piece);
-    }
-#pragma unroll
-    for (int j = 0; j < TT / 8 / NW; ++j) {
-      const int piece = wv * (TT / 8 / NW) + j;
-      lds_dma16(xbase + k0, src(8 * piece + (lane >> 3), tmax, a.ldx, k0),
-                dst + W_BYTES + 1024 * piece);
-    }
+  auto issue_x = [&](int j, int c, int buf) {
+    issue(xbase, a.ldx, tmax, wv * PX, j, c, lds0 + buf * STAGE + W_BYTES);
   };
-  // the scales of this lane's tokens, times the weights' one
-  const float* sxp[NJ];
-#pragma unroll
-  for (int j = 0; j < NJ; ++j)
-    sxp[j] = a.sx + tok0 + min(16 * (wt * NJ + j) + l16, tmax);
+  auto issue_w = [&](int j, int c, int buf) {
+    issue(wbase, a.ldw, rmax, wv * PW, j, c, lds0 + buf * STAGE);
+  };
+  // scales of the tile's tokens, 64 by each of the first waves
+  const uint32_t so = 4 * (uint32_t)min(64 * wv + lane, tmax);
+  auto issue_s = [&](int c, int buf) {
+    if (wv < TT / 64)
+      lds_dma4(a.sx + tok0 + c * a.lds, so, lds0 + 2 * STAGE + buf * TT * 4 + 256 * wv);
+  };
+  const float* sxl = reinterpret_cast<const float*>(smem + 2 * STAGE);
   const int64_t wrow = row0 + wm * (TM / WM);
   const float* swp = a.sw + (wrow < a.m ? wrow : a.m - 1) / kFp8Block * a.ldsw;
 
@@ -172,52 +215,53 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
     return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   };
 
-  f32x4 acc[MI][NJ];
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  f32x4 dp[NJ];
+  f32x4 acc[MI][NJ], dp[NJ];
   float sp[NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     dp[j] = f32x4{0.f, 0.f, 0.f, 0.f};
     sp[j] = 0.f;
   }
-  float sx[NJ], sw;
-  issue(c0);
+  issue_s(c0, 0);
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) sx[j] = sxp[j][c0 * a.lds];
-  sw = swp[c0];
+  for (int j = 0; j < PX; ++j) issue_x(j, c0, 0);
+#pragma unroll
+  for (int j = 0; j < PW; ++j) issue_w(j, c0, 0);
+  float sw = const_load(swp + c0);
+  int buf = 0;
   for (int c = c0; c < c1; ++c) {
-    float s[NJ];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) s[j] = sx[j] * sw;
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's share of block c is there
     __syncthreads();                     // everyone's, and block c - 1 has been read
-    uint8_t* st = smem + ((c - c0) & 1) * STAGE;
-    if (c + 1 < c1) {
-      issue(c + 1);
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) sx[j] = sxp[j][(c + 1) * a.lds];
-      sw = swp[c + 1];
-    } else if ((c + 1) * kRow > n) {  // the row's end: zeros in X past it
+    const uint8_t* wst = smem + buf * STAGE;
+    uint8_t* xst = smem + buf * STAGE + W_BYTES;
+    if ((c + 1) * kRow > n) {  // the row's end: zeros in X past it
       for (int i = threadIdx.x; i < TT * 8; i += NW * 64) {
         const int row = i >> 3, sg = i & 7;
         if (c * kRow + 16 * sg >= n)
-          *reinterpret_cast<i32x4*>(st + W_BYTES + row * kRow + ((sg ^ swz(row)) << 4)) =
+          *reinterpret_cast<i32x4*>(xst + row * kRow + ((sg ^ swz(row)) << 4)) =
               i32x4{0, 0, 0, 0};
       }
       __syncthreads();
     }
+    const int cn = min(c + 1, c1 - 1), nbuf = buf ^ 1;
+    float s[NJ];
     if (EXACT) {
+      issue_s(cn, nbuf);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) s[j] = sxl[buf * TT + 16 * (wt * NJ + j) + l16] * sw;
+      sw = const_load(swp + cn);
       Bf32 x[NJ];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) x[j] = widen(frag(st + W_BYTES, 16 * (wt * NJ + j) + l16));
+      for (int j = 0; j < NJ; ++j) x[j] = widen(frag(xst, 16 * (wt * NJ + j) + l16));
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
-        const Bf32 w = widen(frag(st, wm * (TM / WM) + 16 * i + l16));
+        const Bf32 w = widen(frag(wst, wm * (TM / WM) + 16 * i + l16));
+#pragma unroll
+        for (int j = i * PX / MI; j < (i + 1) * PX / MI; ++j) issue_x(j, cn, nbuf);
+#pragma unroll
+        for (int j = i * PW / MI; j < (i + 1) * PW / MI; ++j) issue_w(j, cn, nbuf);
         f32x4 d[NJ];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) d[j] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -232,16 +276,19 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
           for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[j][e], s[j], acc[i][j][e]);
       }
     } else {
-      // a row tile's fmas run under the next one's matrix instructions; the last
-      // one's under the first of the next block
       i32x8 x[NJ];
+      i32x8 w = frag(wst, wm * (TM / WM) + l16);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) x[j] = frag(st + W_BYTES, 16 * (wt * NJ + j) + l16);
-      i32x8 w = frag(st, wm * (TM / WM) + l16);
+      for (int j = 0; j < NJ; ++j) x[j] = frag(xst, 16 * (wt * NJ + j) + l16);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) s[j] = sxl[buf * TT + 16 * (wt * NJ + j) + l16] * sw;
+      sw = const_load(swp + cn);
+      __builtin_amdgcn_sched_barrier(0);
+      issue_s(cn, nbuf);
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
         i32x8 wn = w;
-        if (i + 1 < MI) wn = frag(st, wm * (TM / WM) + 16 * (i + 1) + l16);
+        if (i + 1 < MI) wn = frag(wst, wm * (TM / WM) + 16 * (i + 1) + l16);
         f32x4 d[NJ];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
@@ -250,16 +297,25 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             acc[ip][j][e] = fmaf(dp[j][e], i > 0 ? s[j] : sp[j], acc[ip][j][e]);
-          __builtin_amdgcn_sched_barrier(0);  // keeps the two streams interleaved
+          // one DMA instruction after every second matrix instruction, X's first
+          if (j & 1) {
+            const int k = (i * NJ + j) / 2;
+            if (k < PX) issue_x(k, cn, nbuf);
+            else if (k < PX + PW) issue_w(k - PX, cn, nbuf);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int j = 0; j < NJ; ++j) dp[j] = d[j];
         w = wn;
       }
+      static_assert(EXACT || PX + PW <= MI * NJ / 2, "the block has room for its DMA");
 #pragma unroll
       for (int j = 0; j < NJ; ++j) sp[j] = s[j];
     }
+    buf = nbuf;
   }
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // no DMA into this LDS outlives the workgroup
   if (!EXACT) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
@@ -273,10 +329,7 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         const int64_t t = tok0 + 16 * (wt * NJ + j) + l16, r = wrow + 16 * i + 4 * q;
-        if (t >= a.tokens) continue;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (r + e < a.m) part[t * a.m + r + e] = acc[i][j][e];
+        if (t < a.tokens) store_part(part + t * a.m + r, a.m - r, a.m, acc[i][j]);
       }
     return;
   }
@@ -458,17 +511,30 @@ __global__ __launch_bounds__(kGemvWaves * 64) void fp8_gemv_kernel(GemvArgs v) {
   }
 }
 
-// Y = R + the splits' partial sums in their order, 4 outputs of a row a lane.
+// Y = R + the splits' partial sums in their order, 4 outputs of a row a lane; the
+// loads of up to 8 splits are in flight at once.
 __global__ __launch_bounds__(256) void fp8_gemm_reduce_kernel(GemmArgs a, int ks) {
   const int64_t per_row = (a.m + 3) / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= a.tokens * per_row) return;
   const int64_t t = i / per_row, r = 4 * (i - t * per_row);
+  const float* p = a.part + t * a.m + r;
+  const int64_t step = a.tokens * a.m;
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
-  for (int z = 0; z < ks; ++z) {
-    const float* p = a.part + (z * a.tokens + t) * a.m + r;
+  if (a.m % 4 == 0) {
+    for (int z0 = 0; z0 < ks; z0 += 8) {
+      f32x4 u[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (r + e < a.m) v[e] += p[e];
+      for (int z = 0; z < 8; ++z)
+        if (z0 + z < ks) u[z] = *reinterpret_cast<const f32x4*>(p + (z0 + z) * step);
+#pragma unroll
+      for (int z = 0; z < 8; ++z)
+        if (z0 + z < ks) v += u[z];
+    }
+  } else {
+    for (int z = 0; z < ks; ++z)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (r + e < a.m) v[e] += p[z * step + e];
   }
   store4(a, t, r, v);
 }
@@ -548,6 +614,9 @@ static GemmArgs gemm_args(const Fp8GemmArgs& g) {
   a.Y = g.Y; a.ldy = g.ldy; a.ybf16 = g.ydt == GPTQ_BF16;
   a.R = g.R; a.ldr = g.ldr;
   a.part = static_cast<float*>(g.ws);
+  const uintptr_t four = a.ybf16 ? 8 : 16;  // bytes of 4 elements
+  a.vec4 = reinterpret_cast<uintptr_t>(g.Y) % four == 0 && g.ldy % 4 == 0 &&
+           (!g.R || (reinterpret_cast<uintptr_t>(g.R) % four == 0 && g.ldr % 4 == 0));
   a.nb = ceil_div(g.n, (int64_t)kFp8Block);
   return a;
 }
