@@ -430,7 +430,11 @@ gptq_status fp8_quantize_blocks(const void* W, gptq_dtype wdt, int64_t m, int64_
  * row strides that are multiples of 16 and below 2^24.
  * fp8_linear: Y = X W^T from 16- or 32-bit activations: fp8_quantize_rows into
  * the workspace, then the product.  X as in fp8_quantize_rows.
- * Workspace: fp8_gemm_workspace_size / fp8_linear_workspace_size(tokens, m, n).
+ * fp8_gated_gemm: the codes and scales (as fp8_swiglu_quantize writes them) of
+ * h = silu(X Wg^T) * (X Wu^T), both products rounded to bf16: the first half of a
+ * gated MLP block without its two products in memory.
+ * Workspace (16-byte aligned): fp8_gemm_workspace_size,
+ * fp8_linear_workspace_size, fp8_gated_gemm_workspace_size(tokens, m, n).
  * ---------------------------------------------------------------------- */
 gptq_status fp8_gemm_workspace_size(int64_t tokens, int64_t m, int64_t n, size_t* bytes);
 gptq_status fp8_gemm(const uint8_t* X, int64_t tokens, int64_t n, int64_t ldx, const float* xs,
@@ -442,6 +446,13 @@ gptq_status fp8_linear(const void* X, gptq_dtype xdt, int64_t tokens, int64_t n,
                        const uint8_t* W, int64_t m, int64_t ldw, const float* wscales,
                        int64_t ldws, void* Y, gptq_dtype ydt, int64_t ldy, void* ws,
                        size_t ws_bytes, hipStream_t stream);
+gptq_status fp8_gated_gemm_workspace_size(int64_t tokens, int64_t m, int64_t n, size_t* bytes);
+gptq_status fp8_gated_gemm(const uint8_t* X, int64_t tokens, int64_t n, int64_t ldx,
+                           const float* xs, int64_t ldxs, const uint8_t* Wg, int64_t m,
+                           int64_t ldwg, const float* gscales, int64_t ldgs, const uint8_t* Wu,
+                           int64_t ldwu, const float* uscales, int64_t ldus, uint8_t* codes,
+                           int64_t ldc, float* scales, int64_t lds, void* ws, size_t ws_bytes,
+                           hipStream_t stream);
 
 /* ------------------------------------------------------------------------
  * Quantized key/value cache -- "LLM quantization principles", section 2.1 (the

@@ -16,6 +16,8 @@ from ._lib import (  # noqa: F401
     awq_lite,
     awq_lite_workspace_size,
     FP8_BLOCK,
+    fp8_gated_gemm,
+    fp8_gated_gemm_workspace_size,
     fp8_gemm,
     fp8_gemm_workspace_size,
     fp8_linear,

@@ -60,6 +60,8 @@ EXPORTED = (
     "fp8_gemm",
     "fp8_linear_workspace_size",
     "fp8_linear",
+    "fp8_gated_gemm_workspace_size",
+    "fp8_gated_gemm",
     "kv_cache_write_workspace_size",
     "kv_cache_write",
     "kv_cache_read",
@@ -202,7 +204,8 @@ def load() -> ctypes.CDLL:
                                         _i64, _vp]
     lib.fp8_quantize_blocks.restype = _i32
     lib.fp8_quantize_blocks.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp]
-    for name in ("fp8_gemm_workspace_size", "fp8_linear_workspace_size"):
+    for name in ("fp8_gemm_workspace_size", "fp8_linear_workspace_size",
+                 "fp8_gated_gemm_workspace_size"):
         getattr(lib, name).restype = _i32
         getattr(lib, name).argtypes = [_i64, _i64, _i64, ctypes.POINTER(_sz)]
     lib.fp8_gemm.restype = _i32
@@ -211,6 +214,9 @@ def load() -> ctypes.CDLL:
     lib.fp8_linear.restype = _i32
     lib.fp8_linear.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i32,
                                _i64, _vp, _sz, _vp]
+    lib.fp8_gated_gemm.restype = _i32
+    lib.fp8_gated_gemm.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64,
+                                   _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _sz, _vp]
     _kvp = ctypes.POINTER(GPTQKVCache)
     lib.kv_cache_write_workspace_size.restype = _i32
     lib.kv_cache_write_workspace_size.argtypes = [_i64, _kvp, ctypes.POINTER(_sz)]
@@ -824,6 +830,35 @@ def fp8_linear(X, W, wscales, Y, ws=None, stream=None) -> None:
     p, nbytes, ws = _space("fp8_linear_workspace_size", ws, d, stream, tokens, m, n)
     _launch("fp8_linear", d, stream, X.data_ptr(), _dtype_code(X), tokens, n, ldx, W.data_ptr(), m,
             ldw, wscales.data_ptr(), ldws, Y.data_ptr(), _dtype_code(Y), ldy, p, nbytes)
+
+
+def fp8_gated_gemm_workspace_size(tokens: int, m: int, n: int) -> int:
+    out = _sz(0)
+    _check(load().fp8_gated_gemm_workspace_size(tokens, m, n, ctypes.byref(out)),
+           "fp8_gated_gemm_workspace_size")
+    return out.value
+
+
+def fp8_gated_gemm(X, xscales, Wg, gscales, Wu, uscales, codes, scales, ws=None,
+                   stream=None) -> None:
+    """codes[tokens, m] and scales[ceil(m / 128), tokens] of silu(X Wg^T) * (X Wu^T), the
+    products (operands as in fp8_gemm) rounded to bf16."""
+    tokens, n = X.shape
+    m = Wg.shape[0]
+    d = _on_gpu(X, "X")
+    nb, mb = -(-n // FP8_BLOCK), -(-m // FP8_BLOCK)
+    ldx = _plane(X, "X", tokens, n, "8u", d)
+    ldxs = _plane(xscales, "xscales", nb, tokens, "f", d)
+    ldwg = _plane(Wg, "Wg", m, n, "8u", d)
+    ldgs = _plane(gscales, "gscales", mb, nb, "f", d)
+    ldwu = _plane(Wu, "Wu", m, n, "8u", d)
+    ldus = _plane(uscales, "uscales", mb, nb, "f", d)
+    ldc = _plane(codes, "codes", tokens, m, "8u", d)
+    lds = _plane(scales, "scales", mb, tokens, "f", d)
+    p, nbytes, ws = _space("fp8_gated_gemm_workspace_size", ws, d, stream, tokens, m, n)
+    _launch("fp8_gated_gemm", d, stream, X.data_ptr(), tokens, n, ldx, xscales.data_ptr(), ldxs,
+            Wg.data_ptr(), m, ldwg, gscales.data_ptr(), ldgs, Wu.data_ptr(), ldwu,
+            uscales.data_ptr(), ldus, codes.data_ptr(), ldc, scales.data_ptr(), lds, p, nbytes)
 
 
 def make_kv_cache(codes, scales, zeros, head_dim: int, fmt: str = "int8",

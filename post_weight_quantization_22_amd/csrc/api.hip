@@ -429,6 +429,7 @@ gptq_status fp8_gemm(const uint8_t* X, int64_t tokens, int64_t n, int64_t ldx, c
   if (ldx >= (int64_t(1) << 24)) return GPTQ_ERR_UNSUPPORTED;
   const gptq_status w = check_ws(ws, ws_bytes, fp8_gemm_ws_bytes(tokens, m, n));
   if (w != GPTQ_OK) return w;
+  if ((reinterpret_cast<uintptr_t>(ws) & 15) != 0) return GPTQ_ERR_INVALID_ARG;
   Fp8GemmArgs g{X, ldx, tokens, n, xs, ldxs, W, ldw, m, wscales, ldws, Y, ydt, ldy, R, ldr, ws};
   return hip_status(launch_fp8_gemm(g, stream));
 }
@@ -449,6 +450,38 @@ gptq_status fp8_linear(const void* X, gptq_dtype xdt, int64_t tokens, int64_t n,
   Fp8GemmArgs g{nullptr, 0, tokens, n, nullptr, 0, W, ldw, m, wscales, ldws, Y, ydt, ldy,
                 nullptr, 0, nullptr};
   return hip_status(launch_fp8_linear(X, xdt, ldx, g, ws, stream));
+}
+
+gptq_status fp8_gated_gemm_workspace_size(int64_t tokens, int64_t m, int64_t n, size_t* bytes) {
+  if (!bytes || tokens < 0 || bad_dim(tokens) || m < 0 || bad_dim(m) || n <= 0 || bad_dim(n))
+    return GPTQ_ERR_INVALID_ARG;
+  *bytes = tokens == 0 || m == 0 ? 0 : fp8_gated_ws_bytes(tokens, m, n);
+  return GPTQ_OK;
+}
+
+gptq_status fp8_gated_gemm(const uint8_t* X, int64_t tokens, int64_t n, int64_t ldx,
+                           const float* xs, int64_t ldxs, const uint8_t* Wg, int64_t m,
+                           int64_t ldwg, const float* gscales, int64_t ldgs, const uint8_t* Wu,
+                           int64_t ldwu, const float* uscales, int64_t ldus, uint8_t* codes,
+                           int64_t ldc, float* scales, int64_t lds, void* ws, size_t ws_bytes,
+                           hipStream_t stream) {
+  for (int up = 0; up < 2; ++up) {
+    const gptq_status ok =
+        fp8_operands_ok(tokens, n, up ? Wu : Wg, m, up ? ldwu : ldwg, up ? uscales : gscales,
+                        up ? ldus : ldgs, codes, GPTQ_BF16, m);
+    if (ok != GPTQ_OK) return ok;
+  }
+  if (tokens == 0 || m == 0) return GPTQ_OK;
+  if (!X || !xs || ldx < n || ldx % 16 != 0 || (reinterpret_cast<uintptr_t>(X) & 15) != 0 ||
+      ldxs < tokens || !scales || ldc < m || lds < tokens)
+    return GPTQ_ERR_INVALID_ARG;
+  if (ldx >= (int64_t(1) << 24)) return GPTQ_ERR_UNSUPPORTED;
+  const gptq_status w = check_ws(ws, ws_bytes, fp8_gated_ws_bytes(tokens, m, n));
+  if (w != GPTQ_OK) return w;
+  if ((reinterpret_cast<uintptr_t>(ws) & 15) != 0) return GPTQ_ERR_INVALID_ARG;
+  Fp8GemmArgs g{X,    ldx,     tokens, n,       xs, ldxs, Wg,      ldwg, m, gscales,
+                ldgs, nullptr, GPTQ_BF16, 0, nullptr, 0, ws};
+  return hip_status(launch_fp8_gated(g, Wu, ldwu, uscales, ldus, codes, ldc, scales, lds, stream));
 }
 
 gptq_status kv_cache_write_workspace_size(int64_t tokens, const gptq_kv_cache* cache,

@@ -11,6 +11,8 @@
 // over normal data.  Turned into bf16 first (exact: e4m3 has 4 significant bits)
 // the same operands are summed with fp32 accuracy (1e-8), at half the rate.  So
 // fp32 results and all small batches take the bf16 instruction.
+#include <type_traits>
+
 #include "fp8.hpp"
 
 namespace gptq {
@@ -38,6 +40,16 @@ struct GemmArgs {
   int vec4;  // rows of Y and R start on 4-element borders
   float* part;  // [ks][tokens][m], K splits only
   int64_t nb, ntm, ntt;  // blocks of n, tiles of weight rows and of tokens
+  // gated products only: the up weights (W holds the gate's) and the codes of
+  // silu(gate) * up
+  const uint8_t* W2;
+  int64_t ldw2;
+  const float* sw2;
+  int64_t ldsw2;
+  uint8_t* codes;
+  int64_t ldc;
+  float* scales;  // [ceil(m / 128)][ldso]
+  int64_t ldso;
 };
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -148,8 +160,21 @@ __device__ __forceinline__ float const_load(const float* p) {
   return *(const __attribute__((address_space(4))) float*)(uintptr_t)p;
 }
 
-template <int TM, int TT, int WM, int WT, bool EXACT>
+// silu(g) u of the bf16 values nearest to the two products
+__device__ __forceinline__ float gated(float g, float u) {
+  g = (float)(__bf16)g;
+  u = (float)(__bf16)u;
+  return g / (1.0f + expf(-g)) * u;
+}
+
+// GATED: the tile's first half of rows are gate rows and its second half the up
+// rows of the same 128 columns of h = silu(gate) * up, a whole scale block of h, so
+// the tile quantizes its part of h itself: each pair of waves exchanges halves of
+// their results through LDS, a lane then has 32 of a token's 128 values, and its
+// three neighbours at the same token the others.
+template <int TM, int TT, int WM, int WT, bool EXACT, bool GATED = false>
 __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a) {
+  static_assert(!GATED || (TM == 2 * kFp8Block && WM == 2 && !EXACT), "a gate and an up block");
   constexpr int MI = TM / WM / 16, NJ = TT / WT / 16, NW = WM * WT;
   constexpr int W_BYTES = TM * kRow, X_BYTES = TT * kRow, STAGE = W_BYTES + X_BYTES;
   constexpr int PW = TM / 8 / NW, PX = TT / 8 / NW;  // a wave's DMA instructions, 8 rows each
@@ -168,7 +193,8 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
   const int64_t L = xcd * per + (xcd < rem ? xcd : rem) + idx;
   const int64_t grp = L / (4 * a.ntm), in = L - grp * 4 * a.ntm;
   const int64_t gsz = min((int64_t)4, a.ntt - 4 * grp);
-  const int64_t tok0 = (4 * grp + in % gsz) * TT, row0 = in / gsz * TM;
+  const int64_t tok0 = (4 * grp + in % gsz) * TT;
+  const int64_t row0 = in / gsz * (GATED ? TM / 2 : TM);
   // the split's blocks
   const int nb = (int)a.nb, ks = gridDim.y, z = blockIdx.y;
   const int c0 = (int)((int64_t)nb * z / ks), c1 = (int)((int64_t)nb * (z + 1) / ks);
@@ -178,9 +204,13 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
   const int wm = wv / WT, wt = wv % WT;
   const int q = lane >> 4, l16 = lane & 15;
   const int n = (int)a.n;
-  const int rmax = (int)min((int64_t)TM - 1, a.m - 1 - row0);
+  const int rmax = (int)min((int64_t)(GATED ? TM / 2 : TM) - 1, a.m - 1 - row0);
   const int tmax = (int)min((int64_t)TT - 1, a.tokens - 1 - tok0);
-  const uint8_t* wbase = a.W + row0 * a.ldw;
+  // (gated: the second half of the waves fetches up rows)
+  const bool up = GATED && wv >= NW / 2;
+  const int64_t ldw = up ? a.ldw2 : a.ldw;
+  const uint8_t* wbase = up ? a.W2 + row0 * ldw : a.W + row0 * ldw;
+  const int wp0 = (up ? wv - NW / 2 : wv) * PW;
   const uint8_t* xbase = a.X + tok0 * a.ldx;
   const uint32_t lds0 = lds_addr(smem);
 
@@ -196,7 +226,7 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
     issue(xbase, a.ldx, tmax, wv * PX, j, c, lds0 + buf * STAGE + W_BYTES);
   };
   auto issue_w = [&](int j, int c, int buf) {
-    issue(wbase, a.ldw, rmax, wv * PW, j, c, lds0 + buf * STAGE);
+    issue(wbase, ldw, rmax, wp0, j, c, lds0 + buf * STAGE + 1024 * (wv * PW - wp0));
   };
   // scales of the tile's tokens, 64 by each of the first waves
   const uint32_t so = 4 * (uint32_t)min(64 * wv + lane, tmax);
@@ -205,8 +235,9 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
       lds_dma4(a.sx + tok0 + c * a.lds, so, lds0 + 2 * STAGE + buf * TT * 4 + 256 * wv);
   };
   const float* sxl = reinterpret_cast<const float*>(smem + 2 * STAGE);
-  const int64_t wrow = row0 + wm * (TM / WM);
-  const float* swp = a.sw + (wrow < a.m ? wrow : a.m - 1) / kFp8Block * a.ldsw;
+  const int64_t wrow = row0 + (GATED ? 0 : wm * (TM / WM));
+  const int64_t srow = (wrow < a.m ? wrow : a.m - 1) / kFp8Block;
+  const float* swp = GATED && wm == 1 ? a.sw2 + srow * a.ldsw2 : a.sw + srow * a.ldsw;
 
   const int seg0 = (q ^ swz(l16)) << 4, seg1 = ((4 + q) ^ swz(l16)) << 4;
   auto frag = [&](const uint8_t* st, int row) {
@@ -321,6 +352,65 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[MI - 1][j][e] = fmaf(dp[j][e], sp[j], acc[MI - 1][j][e]);
+  }
+  if constexpr (GATED) {
+    constexpr int NH = NJ / 2;  // column tiles that a wave of a pair quantizes
+    __syncthreads();            // every operand has been read
+    f32x4* mine = reinterpret_cast<f32x4*>(smem) + (wt * 2 + wm) * MI * NH * 64 + lane;
+    const f32x4* theirs = reinterpret_cast<f32x4*>(smem) + (wt * 2 + 1 - wm) * MI * NH * 64 + lane;
+    auto give = [&](auto first) {  // the other wave's column tiles
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NH; ++j) mine[(i * NH + j) * 64] = acc[i][first.value + j];
+    };
+    auto take = [&](auto first, bool gate) {
+#pragma unroll
+      for (int j = 0; j < NH; ++j) {
+        Vals8 h[MI / 2];
+        float am = 0.f;
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+          const f32x4 own = acc[i][first.value + j], other = theirs[(i * NH + j) * 64];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float v = gate ? gated(own[e], other[e]) : gated(other[e], own[e]);
+            h[i / 2].v[4 * (i % 2) + e] = row0 + 16 * i + 4 * q + e < a.m ? v : 0.f;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < MI / 2; ++i) am = fmaxf(am, amax_finite8(h[i]));
+        am = fmaxf(am, __shfl_xor(am, 16));
+        am = fmaxf(am, __shfl_xor(am, 32));
+        const float sc = e4m3_scale(am), rs = 1.0f / sc;
+        const int64_t t = tok0 + 16 * (wt * NJ + first.value + j) + l16;
+        if (t >= a.tokens) continue;
+        if (q == 0) a.scales[row0 / kFp8Block * a.ldso + t] = sc;
+#pragma unroll
+        for (int i = 0; i < MI / 2; ++i) {
+          const uint2 cc = e4m3_codes8(h[i], sc, rs);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t four = k ? cc.y : cc.x;
+            const int64_t col = row0 + 16 * (2 * i + k) + 4 * q;
+            uint8_t* p = a.codes + t * a.ldc + col;
+            if (a.vec4 && col + 4 <= a.m) {
+              *reinterpret_cast<uint32_t*>(p) = four;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (col + e < a.m) p[e] = (uint8_t)(four >> (8 * e));
+            }
+          }
+        }
+      }
+    };
+    if (wm == 0) give(std::integral_constant<int, NH>());
+    else give(std::integral_constant<int, 0>());
+    __syncthreads();
+    if (wm == 0) take(std::integral_constant<int, 0>(), true);
+    else take(std::integral_constant<int, NH>(), false);
+    return;
   }
   if (ks > 1) {
     float* part = a.part + z * a.tokens * a.m;
@@ -586,13 +676,13 @@ Plan plan_of(int64_t tokens, int64_t m, int64_t n, bool exact) {
   return p;
 }
 
-template <int TM, int TT, int WM, int WT, bool EXACT>
+template <int TM, int TT, int WM, int WT, bool EXACT, bool GATED = false>
 void launch_tile(GemmArgs a, int ks, hipStream_t stream) {
-  a.ntm = ceil_div(a.m, (int64_t)TM);
+  a.ntm = ceil_div(a.m, (int64_t)(GATED ? TM / 2 : TM));
   a.ntt = ceil_div(a.tokens, (int64_t)TT);
   const int64_t grid = ceil_div(a.ntm * a.ntt, kXcds) * kXcds;
-  hipLaunchKernelGGL((fp8_gemm_tile_kernel<TM, TT, WM, WT, EXACT>), dim3((unsigned)grid, (unsigned)ks),
-                     dim3(WM * WT * 64), 0, stream, a);
+  hipLaunchKernelGGL((fp8_gemm_tile_kernel<TM, TT, WM, WT, EXACT, GATED>),
+                     dim3((unsigned)grid, (unsigned)ks), dim3(WM * WT * 64), 0, stream, a);
 }
 
 }  // namespace
@@ -635,6 +725,53 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, hipStream_t stream) {
                        stream, a, p.ks);
   }
   return hipGetLastError();
+}
+
+// The gated product in one kernel where its 256 x 256 tiles reach half of the CUs;
+// else the two products into the workspace (bf16 [tokens][m] each) and the
+// quantizer behind them.
+static bool gated_in_one(int64_t tokens, int64_t m) {
+  return tokens > kGemvTokens && ceil_div(tokens, (int64_t)256) * ceil_div(m, (int64_t)128) >= 128;
+}
+
+static int64_t gated_ld(int64_t m) { return (m + 7) / 8 * 8; }
+
+size_t fp8_gated_ws_bytes(int64_t tokens, int64_t m, int64_t n) {
+  if (gated_in_one(tokens, m)) return 0;
+  return 2 * align_up((size_t)tokens * gated_ld(m) * 2, 256) + fp8_gemm_ws_bytes(tokens, m, n);
+}
+
+hipError_t launch_fp8_gated(const Fp8GemmArgs& g, const uint8_t* W2, int64_t ldw2,
+                            const float* sw2, int64_t ldsw2, uint8_t* codes, int64_t ldc,
+                            float* scales, int64_t ldso, hipStream_t stream) {
+  if (gated_in_one(g.tokens, g.m)) {
+    GemmArgs a = gemm_args(g);
+    a.W2 = W2; a.ldw2 = ldw2;
+    a.sw2 = sw2; a.ldsw2 = ldsw2;
+    a.codes = codes; a.ldc = ldc;
+    a.scales = scales; a.ldso = ldso;
+    a.vec4 = reinterpret_cast<uintptr_t>(codes) % 4 == 0 && ldc % 4 == 0;
+    launch_tile<256, 256, 2, 4, false, true>(a, 1, stream);
+    return hipGetLastError();
+  }
+  const int64_t ld = gated_ld(g.m);
+  const size_t one = align_up((size_t)g.tokens * ld * 2, 256);
+  char* ws = static_cast<char*>(g.ws);
+  Fp8GemmArgs p = g;
+  p.ydt = GPTQ_BF16;
+  p.ldy = ld;
+  p.R = nullptr;
+  p.ws = ws + 2 * one;
+  p.Y = ws;
+  hipError_t e = launch_fp8_gemm(p, stream);
+  if (e != hipSuccess) return e;
+  p.W = W2; p.ldw = ldw2;
+  p.sw = sw2; p.ldsw = ldsw2;
+  p.Y = ws + one;
+  e = launch_fp8_gemm(p, stream);
+  if (e != hipSuccess) return e;
+  return launch_fp8_rows(ws, ld, ws + one, ld, GPTQ_BF16, g.tokens, g.m, codes, ldc, scales, ldso,
+                         stream);
 }
 
 // ws: codes [tokens][ld16], scales [nb][tokens], then the product's own

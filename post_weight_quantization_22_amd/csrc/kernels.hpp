@@ -145,6 +145,12 @@ struct Fp8GemmArgs {
 };
 size_t fp8_gemm_ws_bytes(int64_t tokens, int64_t m, int64_t n);
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, hipStream_t stream);
+// e4m3 codes [tokens, ldc] and scales [ceil(m / 128)][ldso] of silu(X W^T) * (X W2^T),
+// both products rounded to bf16 (g's Y, ydt, R are not read)
+size_t fp8_gated_ws_bytes(int64_t tokens, int64_t m, int64_t n);
+hipError_t launch_fp8_gated(const Fp8GemmArgs& g, const uint8_t* W2, int64_t ldw2,
+                            const float* sw2, int64_t ldsw2, uint8_t* codes, int64_t ldc,
+                            float* scales, int64_t ldso, hipStream_t stream);
 // quantizes X into the workspace and multiplies (g's X, ldx, sx, lds are not read)
 size_t fp8_linear_ws_bytes(int64_t tokens, int64_t m, int64_t n);
 hipError_t launch_fp8_linear(const void* X, int xdt, int64_t ldx, const Fp8GemmArgs& g, void* ws,

@@ -196,12 +196,12 @@ def quantize_stack(x0: torch.Tensor, weights: Sequence[Tuple[torch.Tensor, torch
 # calibration data, so a layer's weights are quantized on their own).
 #
 #     x8 = e4m3(x)                     fp8_quantize_rows
-#     g = x8 Wg8^T, u = x8 Wu8^T       fp8_gemm, bf16
-#     h8 = e4m3(silu(g) * u)           fp8_swiglu_quantize
+#     g = x8 Wg8^T, u = x8 Wu8^T       fp8_gated_gemm, g and u bf16
+#     h8 = e4m3(silu(g) * u)
 #     x' = bf16(x + h8 Wd8^T)          fp8_gemm with x as its residual
 #
-# g and u are held in bf16: half a step of 2^-8 relative, before h is rounded to
-# e4m3's 2^-4; the activations between the products then take half the bytes.
+# g and u are rounded to bf16, half a step of 2^-8 relative, before h is rounded to
+# e4m3's 2^-4: where they pass through memory they then take half the bytes.
 # ---------------------------------------------------------------------------
 @dataclasses.dataclass
 class Fp8Layer:
@@ -245,11 +245,9 @@ def forward_block_fp8(x: torch.Tensor, block: Fp8Block, out: Optional[torch.Tens
             out = buf(T, d, torch.bfloat16)
         x8, xs = buf(T, d, torch.float8_e4m3fn), buf(-(-d // _lib.FP8_BLOCK), T, torch.float32)
         _lib.fp8_quantize_rows(x, x8, xs)
-        g, u = buf(T, f, torch.bfloat16), buf(T, f, torch.bfloat16)
-        _lib.fp8_gemm(x8, xs, block.gate.codes, block.gate.scales, g)
-        _lib.fp8_gemm(x8, xs, block.up.codes, block.up.scales, u)
         h8, hs = buf(T, f, torch.float8_e4m3fn), buf(-(-f // _lib.FP8_BLOCK), T, torch.float32)
-        _lib.fp8_swiglu_quantize(g, u, h8, hs)
+        _lib.fp8_gated_gemm(x8, xs, block.gate.codes, block.gate.scales, block.up.codes,
+                            block.up.scales, h8, hs)
         _lib.fp8_gemm(h8, hs, block.down.codes, block.down.scales, out, residual=x)
     return out
 

@@ -220,6 +220,36 @@ def test_product_nan_codes_stay_in_their_row():
         assert np.array_equal(got, want)
 
 
+@pytest.mark.parametrize("T,m,n", [(1, 100, 144), (20, 300, 272), (40, 130, 400), (257, 8200, 272),
+                                   (300, 8192, 512), (4096, 1000, 256), (128, 16384, 144)])
+def test_gated_product(T, m, n):
+    """Integer operands, so g and u are exact and their bf16 roundings too; h is off by
+    2^-20 (the exp, the sum, the quotient and the product), its codes by half a step.
+    Both ways: fused in the tile, and the two products with the quantizer behind."""
+    q = need_gpu()
+    rng = np.random.default_rng(T + m + n)
+    xc, xs, gc, gs = _operands(rng, T, m, n, True)
+    _, _, uc, us = _operands(rng, T, m, n, True)
+    xs, gs, us = xs / 64, gs / 64, us / 64
+    bf = lambda a: torch.from_numpy(a).to(torch.bfloat16).double().numpy()  # noqa: E731
+    g, u = bf(lowp.gemm(xc, xs, gc, gs)[0]), bf(lowp.gemm(xc, xs, uc, us)[0])
+    h = g / (1 + np.exp(-g)) * u
+    codes = torch.full((T, m + 5), 0x55, dtype=torch.uint8, device="cuda")
+    scales = torch.full((-(-m // 128), T + 2), -1.0, device="cuda")
+    say("fp8 gated product", T, m, n)
+    q.fp8_gated_gemm(_up(xc), _up(xs, torch.float32), _up(gc), _up(gs, torch.float32), _up(uc),
+                     _up(us, torch.float32), codes[:, :m], scales[:, :T])
+    s = host(scales)[:, :T].astype(np.float64)
+    for b in range(s.shape[0]):
+        want = np.abs(h[:, b * 128:(b + 1) * 128]).max(1) / 448
+        want = np.where(want == 0, 1.0, want)
+        assert np.all(np.abs(s[b] - want) <= 2.0 ** -19 * want), b
+    sp = np.repeat(s, 128, 0)[:m].T
+    back = lowp.e4m3_decode(host(codes)[:, :m]) * sp
+    assert np.all(np.abs(back - h) <= np.abs(h) * (2.0 ** -4 + 2.0 ** -19) + 2.0 ** -10 * sp)
+    assert np.all(host(codes)[:, m:] == 0x55) and np.all(host(scales)[:, T:] == -1)
+
+
 def test_residual():
     """An integer product plus an integer residual, exact; also in place."""
     q = need_gpu()

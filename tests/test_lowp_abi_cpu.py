@@ -64,6 +64,18 @@ def test_products():
     assert linear(n=40) == UNSUP
     for kw in (dict(X=None), dict(dt=5), dict(ldx=255), dict(ws=FAKE + 4)):
         assert linear(**kw) == BAD, kw
+    def gated(X=FAKE, t=4, n=256, ldx=256, Wg=FAKE, m=8, Wu=FAKE, ldwu=256, us=FAKE, c=FAKE, ldc=8,
+              sc=FAKE, lds=4, ws=FAKE, nbytes=1 << 40):
+        return so.fp8_gated_gemm(X, t, n, ldx, FAKE, 100, Wg, m, 256, FAKE, 2, Wu, ldwu, us, 2, c, ldc,
+                                 sc, lds, ws, nbytes, None)
+
+    assert gated(t=0) == OK and gated(m=0) == OK and gated(n=40) == UNSUP
+    for kw in (dict(X=None), dict(Wg=None), dict(Wu=None), dict(ldwu=250), dict(us=None), dict(c=None),
+               dict(ldc=7), dict(sc=None), dict(lds=3), dict(ldx=200), dict(t=-1), dict(ws=FAKE + 2)):
+        assert gated(**kw) == BAD, kw
+    assert gated(nbytes=16) == WS
+    assert gq.fp8_gated_gemm_workspace_size(4, 8, 256) >= 2 * 4 * 8 * 2
+    assert gq.fp8_gated_gemm_workspace_size(512, 11008, 4096) == 0
     assert linear(t=100, nbytes=16) == WS and linear(t=100, ws=None) == WS
     assert gq.fp8_linear_workspace_size(100, 8, 256) >= 100 * 256
     assert gq.fp8_linear_workspace_size(0, 8, 256) == 0
