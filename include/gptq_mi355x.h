@@ -489,8 +489,10 @@ gptq_status fp8_gated_gemm(const uint8_t* X, int64_t tokens, int64_t n, int64_t 
  * Nothing but the given slots' rows is written.  tokens times the lanes of a
  * token (heads * groups * group lanes of 8 values) must stay below 2^31, else
  * GPTQ_ERR_UNSUPPORTED.  Workspace: kv_cache_write_workspace_size(tokens, kc),
- * 0 for small calls.
+ * 0 for calls of at most GPTQ_KV_SMALL_TOKENS tokens.
  * ---------------------------------------------------------------------- */
+#define GPTQ_KV_SMALL_TOKENS 1024
+
 typedef enum gptq_kv_format { GPTQ_KV_INT4 = 0, GPTQ_KV_INT8 = 1, GPTQ_KV_E4M3 = 2 } gptq_kv_format;
 
 typedef struct gptq_kv_cache {

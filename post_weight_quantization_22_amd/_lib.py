@@ -8,6 +8,7 @@ fails loudly when the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -73,6 +74,7 @@ FP8_BLOCK = 128  # columns (and weight rows) that share a scale
 GPTQ_KV_INT4 = 0
 GPTQ_KV_INT8 = 1
 GPTQ_KV_E4M3 = 2
+GPTQ_KV_SMALL_TOKENS = 1024  # kv_cache_write needs no workspace up to here
 _KV_FORMATS = {"int4": GPTQ_KV_INT4, "int8": GPTQ_KV_INT8, "e4m3": GPTQ_KV_E4M3}
 
 
@@ -672,10 +674,23 @@ def gptq_layer_error(W, codes, scales, zeros, g_idx, S, err, ws=None, stream=Non
 # ---------------------------------------------------------------------------
 # 8-bit floating point, the quantized cache, log probabilities
 # ---------------------------------------------------------------------------
+# torch dtype -> one letter; filled on first use (this module does not import
+# torch before it is needed)
+_KIND = {}
+_FLOAT = {"b": GPTQ_BF16, "f": GPTQ_F32}
+
+
 def _on_gpu(t, name: str):
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} is on {t.device}, expected a GPU tensor")
-    return t.device
+    """The device of an operand, which has to be a GPU."""
+    if not _KIND:
+        import torch
+
+        _KIND.update({torch.bfloat16: "b", torch.float32: "f", torch.float8_e4m3fn: "8",
+                      torch.uint8: "u", torch.int64: "l", torch.int32: "i"})
+    d = t.device
+    if d.type != "cuda":
+        raise ValueError(f"{name} is on {d}, expected a GPU tensor")
+    return d
 
 
 def _plane(t, name: str, rows: int, cols: int, kinds: str, device) -> int:
@@ -683,32 +698,16 @@ def _plane(t, name: str, rows: int, cols: int, kinds: str, device) -> int:
     ``device``, a dtype among ``kinds``) and returns its row stride."""
     if t is None:
         raise ValueError(f"{name} is required")
-    if _KIND.get(t.dtype) is None or _KIND[t.dtype] not in kinds:
+    if _KIND.get(t.dtype, "?") not in kinds:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    shape = t.shape
-    if len(shape) != 2 or shape[0] < rows or shape[1] < cols or (t.stride(1) != 1 and shape[1] > 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] < rows or shape[1] < cols or (stride[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name}: expected a 2-D tensor of at least {rows} x {cols} with unit "
-                         f"column stride, got shape {tuple(shape)} strides {t.stride()}")
+                         f"column stride, got shape {tuple(shape)} strides {stride}")
     # the stride of a single row is not meaningful
-    return t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
-
-
-class _Kinds(dict):
-    """torch dtype -> one letter (filled on first use: this module does not
-    import torch before it is needed)."""
-
-    def get(self, key, default=None):
-        if not self:
-            import torch
-
-            self.update({torch.bfloat16: "b", torch.float32: "f", torch.float8_e4m3fn: "8",
-                         torch.uint8: "u", torch.int64: "l", torch.int32: "i"})
-        return super().get(key, default)
-
-
-_KIND = _Kinds()
+    return stride[0] if shape[0] > 1 else max(stride[0], shape[1])
 
 
 def _launch(name: str, device, stream, *args) -> None:
@@ -716,30 +715,38 @@ def _launch(name: str, device, stream, *args) -> None:
     tensors' device), with that device current."""
     import torch
 
-    fn = getattr(_lib or load(), name)
+    c = torch._C
     index = device.index
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(index)
+        raw = c._cuda_getCurrentRawStream(index)
     else:
         if stream.device != device:
             raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on {device}")
         raw = stream.cuda_stream
-    if index == torch.cuda.current_device():
-        status = fn(*args, raw)
+    if index == c._cuda_getDevice():
+        status = getattr(_lib, name)(*args, raw)
     else:
         with torch.cuda.device(index):
-            status = fn(*args, raw)
-    if status != GPTQ_OK:
+            status = getattr(_lib, name)(*args, raw)
+    if status:
         _check(status, name)
 
 
-def _space(name: str, ws, device, stream, *args):
+@functools.lru_cache(maxsize=1024)
+def _size_of(name: str, *args) -> int:
+    """A workspace query by its arguments (what it answers depends on nothing else)."""
+    out = _sz(0)
+    _check(getattr(load(), name)(*args, ctypes.byref(out)), name)
+    return out.value
+
+
+def _space(need: int, ws, device, stream):
     """(pointer, bytes, tensor) of the caller's workspace, or of one for this call."""
     if ws is None:
-        need = _sz(0)
-        _check(getattr(_lib or load(), name)(*args, ctypes.byref(need)), name)
-        ws = _workspace(need.value, device, stream)
-        return (None, 0, None) if ws is None else (ws.data_ptr(), need.value, ws)
+        if not need:
+            return None, 0, None
+        ws = _workspace(need, device, stream)
+        return ws.data_ptr(), need, ws
     if ws.device != device:
         raise ValueError(f"ws is on {ws.device}, expected {device}")
     if not ws.is_contiguous():
@@ -755,7 +762,7 @@ def fp8_quantize_rows(X, codes, scales, stream=None) -> None:
     ldx = _plane(X, "X", tokens, n, "bf", d)
     ldc = _plane(codes, "codes", tokens, n, "8u", d)
     lds = _plane(scales, "scales", -(-n // FP8_BLOCK), tokens, "f", d)
-    _launch("fp8_quantize_rows", d, stream, X.data_ptr(), _dtype_code(X), tokens, n, ldx,
+    _launch("fp8_quantize_rows", d, stream, X.data_ptr(), _FLOAT[_KIND[X.dtype]], tokens, n, ldx,
             codes.data_ptr(), ldc, scales.data_ptr(), lds)
 
 
@@ -768,7 +775,7 @@ def fp8_swiglu_quantize(gate, up, codes, scales, stream=None) -> None:
     ldc = _plane(codes, "codes", tokens, n, "8u", d)
     lds = _plane(scales, "scales", -(-n // FP8_BLOCK), tokens, "f", d)
     _launch("fp8_swiglu_quantize", d, stream, gate.data_ptr(), ldg, up.data_ptr(), ldu,
-            _dtype_code(gate), tokens, n, codes.data_ptr(), ldc, scales.data_ptr(), lds)
+            _FLOAT[_KIND[gate.dtype]], tokens, n, codes.data_ptr(), ldc, scales.data_ptr(), lds)
 
 
 def fp8_quantize_blocks(W, codes, scales, stream=None) -> None:
@@ -779,22 +786,16 @@ def fp8_quantize_blocks(W, codes, scales, stream=None) -> None:
     ldw = _plane(W, "W", m, n, "bf", d)
     ldc = _plane(codes, "codes", m, n, "8u", d)
     lds = _plane(scales, "scales", -(-m // FP8_BLOCK), -(-n // FP8_BLOCK), "f", d)
-    _launch("fp8_quantize_blocks", d, stream, W.data_ptr(), _dtype_code(W), m, n, ldw,
+    _launch("fp8_quantize_blocks", d, stream, W.data_ptr(), _FLOAT[_KIND[W.dtype]], m, n, ldw,
             codes.data_ptr(), ldc, scales.data_ptr(), lds)
 
 
 def fp8_gemm_workspace_size(tokens: int, m: int, n: int) -> int:
-    out = _sz(0)
-    _check(load().fp8_gemm_workspace_size(tokens, m, n, ctypes.byref(out)),
-           "fp8_gemm_workspace_size")
-    return out.value
+    return _size_of("fp8_gemm_workspace_size", tokens, m, n)
 
 
 def fp8_linear_workspace_size(tokens: int, m: int, n: int) -> int:
-    out = _sz(0)
-    _check(load().fp8_linear_workspace_size(tokens, m, n, ctypes.byref(out)),
-           "fp8_linear_workspace_size")
-    return out.value
+    return _size_of("fp8_linear_workspace_size", tokens, m, n)
 
 
 def fp8_gemm(X, xscales, W, wscales, Y, residual=None, ws=None, stream=None) -> None:
@@ -811,10 +812,10 @@ def fp8_gemm(X, xscales, W, wscales, Y, residual=None, ws=None, stream=None) -> 
     ldws = _plane(wscales, "wscales", -(-m // FP8_BLOCK), nb, "f", d)
     ldy = _plane(Y, "Y", tokens, m, "bf", d)
     ldr = 0 if residual is None else _plane(residual, "residual", tokens, m, _KIND[Y.dtype], d)
-    p, nbytes, ws = _space("fp8_gemm_workspace_size", ws, d, stream, tokens, m, n)
+    p, nbytes, ws = _space(fp8_gemm_workspace_size(tokens, m, n), ws, d, stream)
     _launch("fp8_gemm", d, stream, X.data_ptr(), tokens, n, ldx, xscales.data_ptr(), ldxs,
             W.data_ptr(), m, ldw, wscales.data_ptr(), ldws, _ptr(residual), ldr, Y.data_ptr(),
-            _dtype_code(Y), ldy, p, nbytes)
+            _FLOAT[_KIND[Y.dtype]], ldy, p, nbytes)
 
 
 def fp8_linear(X, W, wscales, Y, ws=None, stream=None) -> None:
@@ -827,16 +828,13 @@ def fp8_linear(X, W, wscales, Y, ws=None, stream=None) -> None:
     ldw = _plane(W, "W", m, n, "8u", d)
     ldws = _plane(wscales, "wscales", -(-m // FP8_BLOCK), -(-n // FP8_BLOCK), "f", d)
     ldy = _plane(Y, "Y", tokens, m, "bf", d)
-    p, nbytes, ws = _space("fp8_linear_workspace_size", ws, d, stream, tokens, m, n)
-    _launch("fp8_linear", d, stream, X.data_ptr(), _dtype_code(X), tokens, n, ldx, W.data_ptr(), m,
-            ldw, wscales.data_ptr(), ldws, Y.data_ptr(), _dtype_code(Y), ldy, p, nbytes)
+    p, nbytes, ws = _space(fp8_linear_workspace_size(tokens, m, n), ws, d, stream)
+    _launch("fp8_linear", d, stream, X.data_ptr(), _FLOAT[_KIND[X.dtype]], tokens, n, ldx,
+            W.data_ptr(), m, ldw, wscales.data_ptr(), ldws, Y.data_ptr(), _FLOAT[_KIND[Y.dtype]], ldy, p, nbytes)
 
 
 def fp8_gated_gemm_workspace_size(tokens: int, m: int, n: int) -> int:
-    out = _sz(0)
-    _check(load().fp8_gated_gemm_workspace_size(tokens, m, n, ctypes.byref(out)),
-           "fp8_gated_gemm_workspace_size")
-    return out.value
+    return _size_of("fp8_gated_gemm_workspace_size", tokens, m, n)
 
 
 def fp8_gated_gemm(X, xscales, Wg, gscales, Wu, uscales, codes, scales, ws=None,
@@ -855,7 +853,7 @@ def fp8_gated_gemm(X, xscales, Wg, gscales, Wu, uscales, codes, scales, ws=None,
     ldus = _plane(uscales, "uscales", mb, nb, "f", d)
     ldc = _plane(codes, "codes", tokens, m, "8u", d)
     lds = _plane(scales, "scales", mb, tokens, "f", d)
-    p, nbytes, ws = _space("fp8_gated_gemm_workspace_size", ws, d, stream, tokens, m, n)
+    p, nbytes, ws = _space(fp8_gated_gemm_workspace_size(tokens, m, n), ws, d, stream)
     _launch("fp8_gated_gemm", d, stream, X.data_ptr(), tokens, n, ldx, xscales.data_ptr(), ldxs,
             Wg.data_ptr(), m, ldwg, gscales.data_ptr(), ldgs, Wu.data_ptr(), ldwu,
             uscales.data_ptr(), ldus, codes.data_ptr(), ldc, scales.data_ptr(), lds, p, nbytes)
@@ -879,32 +877,39 @@ def make_kv_cache(codes, scales, zeros, head_dim: int, fmt: str = "int8",
         raise TypeError(f"codes: unsupported dtype {codes.dtype}")
     if _KIND.get(scales.dtype) != "f":
         raise TypeError(f"scales: dtype {scales.dtype}, expected float32")
-    if codes.dim() != 4 or codes.shape[3] != nbytes or codes.stride(3) != 1:
-        raise ValueError(f"codes: shape {tuple(codes.shape)} strides {codes.stride()}, expected "
+    shape, cs, ps = codes.shape, codes.stride(), scales.stride()
+    if len(shape) != 4 or shape[3] != nbytes or cs[3] != 1:
+        raise ValueError(f"codes: shape {tuple(shape)} strides {cs}, expected "
                          f"[pages, page_size, heads, {nbytes}] with a dense last dimension")
-    pages, page_size, heads = codes.shape[:3]
+    pages, page_size, heads = shape[:3]
     want = (pages, page_size, heads, groups)
-    for t, name in ((scales, "scales"), (zeros, "zeros")):
-        if t is None:
-            continue
-        if t.device != d:
-            raise ValueError(f"{name} is on {t.device}, expected {d}")
-        if tuple(t.shape) != want or (t.stride(3) != 1 and groups > 1):
-            raise ValueError(f"{name}: shape {tuple(t.shape)} strides {t.stride()}, expected "
-                             f"{want} with a dense last dimension")
+    if scales.device != d:
+        raise ValueError(f"scales is on {scales.device}, expected {d}")
+    if scales.shape != want or (ps[3] != 1 and groups > 1):
+        raise ValueError(f"scales: shape {tuple(scales.shape)} strides {ps}, expected {want} with "
+                         "a dense last dimension")
+    z = None
     if zeros is not None:
         if fmt == "e4m3":
             raise ValueError("zeros: e4m3 has none")
         if _KIND.get(zeros.dtype) != "u":
             raise TypeError(f"zeros: dtype {zeros.dtype}, expected uint8")
-        if zeros.stride()[:3] != scales.stride()[:3]:
-            raise ValueError("zeros must have the strides of scales")
-    cs, ps = codes.stride(), scales.stride()
-    c = GPTQKVCache(codes.data_ptr(), scales.data_ptr(),
-                    None if zeros is None else zeros.data_ptr(), pages, cs[0], cs[1], cs[2], ps[0],
+        if zeros.device != d:
+            raise ValueError(f"zeros is on {zeros.device}, expected {d}")
+        if zeros.shape != want or zeros.stride() != ps:
+            raise ValueError("zeros must have the shape and strides of scales")
+        z = zeros.data_ptr()
+    c = GPTQKVCache(codes.data_ptr(), scales.data_ptr(), z, pages, cs[0], cs[1], cs[2], ps[0],
                     ps[1], ps[2], page_size, heads, head_dim, group_size, _KV_FORMATS[fmt])
     c.tensors = (codes, scales, zeros)
+    c.device = d
+    c.row = (heads, head_dim)
+    c.paging = (pages, page_size)
+    c.ref = ctypes.byref(c)
     return c
+
+
+_KV_NONE = (None, 0, 0)
 
 
 def _kv_rows(t, name: str, cache: Optional[GPTQKVCache], tokens: int, device, dtype):
@@ -912,19 +917,19 @@ def _kv_rows(t, name: str, cache: Optional[GPTQKVCache], tokens: int, device, dt
     if cache is None:
         if t is not None:
             raise ValueError(f"{name} is given without its cache")
-        return None, 0, 0
+        return _KV_NONE
     if t is None:
         raise ValueError(f"{name} is required: its cache is given")
-    if cache.tensors[0].device != device or t.device != device:
-        raise ValueError(f"{name}: rows on {t.device}, cache on {cache.tensors[0].device}, "
+    if cache.device != device or t.device != device:
+        raise ValueError(f"{name}: rows on {t.device}, cache on {cache.device}, "
                          f"expected {device}")
-    if t.dtype != dtype or _KIND.get(dtype) not in ("b", "f"):
-        raise TypeError(f"{name}: dtype {t.dtype}, expected bfloat16 or float32 for keys and "
-                        "values alike")
-    if tuple(t.shape) != (tokens, cache.heads, cache.head_dim) or t.stride(2) != 1:
-        raise ValueError(f"{name}: shape {tuple(t.shape)} strides {t.stride()}, expected "
-                         f"{(tokens, cache.heads, cache.head_dim)} with a dense last dimension")
-    return t.data_ptr(), t.stride(0), t.stride(1)
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype} for keys and values alike")
+    shape, stride = t.shape, t.stride()
+    if shape != (tokens, *cache.row) or stride[2] != 1:
+        raise ValueError(f"{name}: shape {tuple(shape)} strides {stride}, expected "
+                         f"{(tokens, *cache.row)} with a dense last dimension")
+    return t.data_ptr(), stride[0], stride[1]
 
 
 def _kv_call(K, V, slots, kc, vc, info):
@@ -934,15 +939,19 @@ def _kv_call(K, V, slots, kc, vc, info):
     d = _on_gpu(slots, "slots")
     if _KIND.get(slots.dtype) != "l" or slots.dim() != 1 or not slots.is_contiguous():
         raise ValueError("slots: expected a contiguous 1-D int64 tensor")
-    _buf(info, "info", (1,), ("int32",), d)
+    if info is not None:
+        _buf(info, "info", (1,), ("int32",), d)
+    dtype = rows.dtype
+    kind = _KIND.get(dtype)
+    if kind not in ("b", "f"):
+        raise TypeError(f"rows: dtype {dtype}, expected bfloat16 or float32")
     tokens = slots.shape[0]
-    k = _kv_rows(K, "K", kc, tokens, d, rows.dtype)
-    v = _kv_rows(V, "V", vc, tokens, d, rows.dtype)
-    if kc is not None and vc is not None and (kc.pages != vc.pages
-                                              or kc.page_size != vc.page_size):
+    k = _kv_rows(K, "K", kc, tokens, d, dtype)
+    v = _kv_rows(V, "V", vc, tokens, d, dtype)
+    if kc is not None and vc is not None and kc.paging != vc.paging:
         raise ValueError("the two caches differ in pages or page_size")
-    return (d, tokens, k, v, _dtype_code(rows), None if kc is None else ctypes.byref(kc),
-            None if vc is None else ctypes.byref(vc))
+    return (d, tokens, k, v, GPTQ_BF16 if kind == "b" else GPTQ_F32,
+            None if kc is None else kc.ref, None if vc is None else vc.ref)
 
 
 def kv_cache_write_workspace_size(tokens: int, cache: GPTQKVCache) -> int:
@@ -955,24 +964,40 @@ def kv_cache_write_workspace_size(tokens: int, cache: GPTQKVCache) -> int:
 def kv_cache_write(K, V, slots, kc, vc, info=None, ws=None, stream=None) -> None:
     """Quantize rows K, V [tokens, heads, head_dim] (bf16 or fp32) into slots[tokens] (int64,
     negative: padding, not written) of the caches kc, vc (either may be None with its rows)."""
-    d, tokens, k, v, dt, pk, pv = _kv_call(K, V, slots, kc, vc, info)
-    p, nbytes, ws = _space("kv_cache_write_workspace_size", ws, d, stream, tokens, pk or pv)
-    _launch("kv_cache_write", d, stream, *k, *v, dt, tokens, slots.data_ptr(), pk, pv, _ptr(info),
-            p, nbytes)
+    d, tokens, (kp, kt, kh), (vp, vt, vh), dt, pk, pv = _kv_call(K, V, slots, kc, vc, info)
+    need = 0
+    if ws is None and tokens > GPTQ_KV_SMALL_TOKENS:
+        need = kv_cache_write_workspace_size(tokens, kc if kc is not None else vc)
+    p, nbytes, ws = _space(need, ws, d, stream)
+    _launch("kv_cache_write", d, stream, kp, kt, kh, vp, vt, vh, dt, tokens, slots.data_ptr(), pk,
+            pv, _ptr(info), p, nbytes)
 
 
 def kv_cache_read(kc, vc, slots, K, V, info=None, stream=None) -> None:
     """Rows K, V [tokens, heads, head_dim] (bf16 or fp32) = the caches' values at slots[tokens]
     (int64, negative: zeros)."""
-    d, tokens, k, v, dt, pk, pv = _kv_call(K, V, slots, kc, vc, info)
-    _launch("kv_cache_read", d, stream, pk, pv, slots.data_ptr(), tokens, *k, *v, dt, _ptr(info))
+    d, tokens, (kp, kt, kh), (vp, vt, vh), dt, pk, pv = _kv_call(K, V, slots, kc, vc, info)
+    _launch("kv_cache_read", d, stream, pk, pv, slots.data_ptr(), tokens, kp, kt, kh, vp, vt, vh,
+            dt, _ptr(info))
 
 
 def token_logprobs_workspace_size(tokens: int, vocab: int, top: int) -> int:
-    out = _sz(0)
-    _check(load().token_logprobs_workspace_size(tokens, vocab, top, ctypes.byref(out)),
-           "token_logprobs_workspace_size")
-    return out.value
+    return _size_of("token_logprobs_workspace_size", tokens, vocab, top)
+
+
+def _vector(t, name: str, count: int, kind: str, device, optional: bool = True) -> None:
+    """A contiguous buffer of at least ``count`` elements."""
+    if t is None:
+        if optional:
+            return
+        raise ValueError(f"{name} is required")
+    if _KIND.get(t.dtype) != kind:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous() or t.numel() < count:
+        raise ValueError(f"{name}: expected {count} contiguous elements, got shape "
+                         f"{tuple(t.shape)} strides {t.stride()}")
 
 
 def token_logprobs(logits, ids, logprob, entropy=None, top_ids=None, top_logprobs=None, ws=None,
@@ -983,17 +1008,19 @@ def token_logprobs(logits, ids, logprob, entropy=None, top_ids=None, top_logprob
     tokens, vocab = logits.shape
     d = _on_gpu(logits, "logits")
     ldl = _plane(logits, "logits", tokens, vocab, "bf", d)
-    _buf(ids, "ids", (tokens,), ("int64",), d, optional=logprob is None)
-    _buf(logprob, "logprob", (tokens,), ("float32",), d, optional=ids is None)
-    _buf(entropy, "entropy", (tokens,), ("float32",), d)
+    _vector(ids, "ids", tokens, "l", d, optional=logprob is None)
+    _vector(logprob, "logprob", tokens, "f", d, optional=ids is None)
+    _vector(entropy, "entropy", tokens, "f", d)
     top = 0
     if top_ids is not None or top_logprobs is not None:
         if top_ids is None or top_ids.dim() != 2:
             raise ValueError("top_ids: expected [tokens, top] together with top_logprobs")
         top = top_ids.shape[1]
-        _buf(top_ids, "top_ids", (tokens, top), ("int32",), d)
-        _buf(top_logprobs, "top_logprobs", (tokens, top), ("float32",), d, optional=False)
-    p, nbytes, ws = _space("token_logprobs_workspace_size", ws, d, stream, tokens, vocab, top)
-    _launch("token_logprobs", d, stream, logits.data_ptr(), _dtype_code(logits), tokens, vocab,
-            ldl, _ptr(ids), _ptr(logprob), _ptr(entropy), top, _ptr(top_ids), _ptr(top_logprobs),
+        if top_logprobs is None or top_logprobs.shape != top_ids.shape:
+            raise ValueError("top_logprobs: expected the shape of top_ids")
+        _vector(top_ids, "top_ids", tokens * top, "i", d)
+        _vector(top_logprobs, "top_logprobs", tokens * top, "f", d)
+    p, nbytes, ws = _space(token_logprobs_workspace_size(tokens, vocab, top), ws, d, stream)
+    _launch("token_logprobs", d, stream, logits.data_ptr(), _FLOAT[_KIND[logits.dtype]], tokens,
+            vocab, ldl, _ptr(ids), _ptr(logprob), _ptr(entropy), top, _ptr(top_ids), _ptr(top_logprobs),
             p, nbytes)

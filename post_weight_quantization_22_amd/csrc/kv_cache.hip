@@ -19,7 +19,7 @@ namespace {
 
 // up to this many tokens a workgroup looks for a later token with the same slot
 // by itself; beyond, two small kernels settle the slots' owners first
-constexpr int64_t kScanTokens = 1024;
+constexpr int64_t kScanTokens = GPTQ_KV_SMALL_TOKENS;
 
 // the most tokens that the 256 lanes of a workgroup touch (one lane a token, and
 // a partial one)

@@ -107,7 +107,9 @@ def test_cache():
     assert write(t=0) == OK and read(t=0) == OK
     assert write(t=4096) == WS  # a large call settles repeated slots in the workspace
     assert gq.kv_cache_write_workspace_size(4096, _cache()) == 4 * 64
-    assert gq.kv_cache_write_workspace_size(8, _cache()) == 0
+    small = _lib.GPTQ_KV_SMALL_TOKENS
+    assert gq.kv_cache_write_workspace_size(small, _cache()) == 0
+    assert gq.kv_cache_write_workspace_size(small + 1, _cache()) > 0
     for f in (write, read):
         for kw in (dict(kc=None), dict(vc=None), dict(kc=None, vc=None, K=None, V=None),
                    dict(K=None), dict(V=None), dict(dt=2), dict(t=-1), dict(slots=None),
@@ -167,6 +169,8 @@ def test_the_binding_refuses_host_tensors_and_wrong_types():
 
 def test_plane_checks():
     d = torch.device("cpu")
+    with pytest.raises(ValueError):
+        _lib._on_gpu(torch.zeros(1), "t")  # (also fills the dtype table)
     assert _lib._plane(torch.zeros(4, 8), "t", 4, 8, "f", d) == 8
     assert _lib._plane(torch.zeros(4, 16)[:, :8], "t", 4, 8, "f", d) == 16
     assert _lib._plane(torch.zeros(1, 8), "t", 1, 8, "f", d) == 8
