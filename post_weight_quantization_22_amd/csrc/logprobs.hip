@@ -18,8 +18,8 @@
 // A lane keeps (m, r, t) of its own logits and the place of its m.  The top
 // alternatives are found among few candidates: with K the k-th best of the 256
 // lanes' best (value, place) pairs, at least k logits are no worse than K, and
-// only the k lanes whose best is no worse than K can hold one; those lanes read
-// their logits once more (from L2) and list them.  Pairs are ordered by value,
+// only the k lanes whose best is no worse than K can hold one; the logits of
+// those lanes are read once more (from L2) and listed.  Pairs are ordered by value,
 // then by the lower index, so all are distinct and the result does not depend
 // on the order in which the list was filled.
 #include "fp8.hpp"
@@ -73,25 +73,88 @@ __device__ __forceinline__ float key_value(uint64_t k) {
 __device__ __forceinline__ uint32_t key_index(uint64_t k) { return ~(uint32_t)k; }
 
 __device__ __forceinline__ uint64_t umax(uint64_t a, uint64_t b) { return a > b ? a : b; }
-__device__ __forceinline__ uint64_t umin(uint64_t a, uint64_t b) { return a < b ? a : b; }
 
-__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int mask) {
-  const uint32_t lo = __shfl_xor((uint32_t)v, mask), hi = __shfl_xor((uint32_t)(v >> 32), mask);
-  return (uint64_t)hi << 32 | lo;
+// The value of lane ^ M within the wave: register moves between lanes (a few
+// cycles each; through LDS one is about 100, and a sort makes 21 in a row).
+template <int M>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t v) {
+  if constexpr (M == 1) return __builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true);  // quad 1 0 3 2
+  else if constexpr (M == 2) return __builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true);  // 2 3 0 1
+  else if constexpr (M == 3) return __builtin_amdgcn_mov_dpp((int)v, 0x1B, 0xF, 0xF, true);  // 3 2 1 0
+  else if constexpr (M == 7) return __builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true);  // mirror of 8
+  else if constexpr (M == 8) return __builtin_amdgcn_mov_dpp((int)v, 0x128, 0xF, 0xF, true);  // rotate 16 by 8
+  else if constexpr (M == 15) return __builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, true);  // mirror of 16
+  else if constexpr (M == 4) return lane_xor<3>(lane_xor<7>(v));
+  else if constexpr (M == 16) {
+    const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return (threadIdx.x & 16) ? p[0] : p[1];
+  } else if constexpr (M == 32) {
+    const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return (threadIdx.x & 32) ? p[0] : p[1];
+  } else if constexpr (M == 31) return lane_xor<16>(lane_xor<15>(v));
+  else {
+    static_assert(M == 63, "masks that the sort uses");
+    return lane_xor<32>(lane_xor<31>(v));
+  }
+}
+template <int M>
+__device__ __forceinline__ uint64_t lane_xor64(uint64_t v) {
+  return (uint64_t)lane_xor<M>((uint32_t)(v >> 32)) << 32 | lane_xor<M>((uint32_t)v);
+}
+template <int M>
+__device__ __forceinline__ float lane_xorf(float v) {
+  return __uint_as_float(lane_xor<M>(__float_as_uint(v)));
 }
 
-// the wave's 64 keys in descending order
-__device__ __forceinline__ uint64_t sort64(uint64_t v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int size = 2; size <= 64; size *= 2)
-#pragma unroll
-    for (int step = size / 2; step > 0; step /= 2) {
-      const uint64_t o = shfl_xor64(v, step);
-      const bool keep_max = ((lane & step) == 0) == ((lane & size) == 0);
-      v = keep_max ? umax(v, o) : umin(v, o);
-    }
+// Of the pair (lane, lane ^ M) the lane without bit LOW keeps the larger key.
+template <int M, int LOW>
+__device__ __forceinline__ uint64_t exchange(uint64_t v) {
+  const uint64_t o = lane_xor64<M>(v);
+  return ((threadIdx.x & LOW) == 0) == (v > o) ? v : o;
+}
+// a bitonic run of 2 LOW lanes into descending order
+template <int LOW>
+__device__ __forceinline__ uint64_t merge_down(uint64_t v) {
+  v = exchange<LOW, LOW>(v);
+  if constexpr (LOW > 1) v = merge_down<LOW / 2>(v);
   return v;
+}
+// the wave's 64 keys in descending order: runs of 2, 4, .. 64, each from its two
+// halves by a mirror exchange and a merge of each half
+template <int SIZE = 2>
+__device__ __forceinline__ uint64_t sort64(uint64_t v) {
+  v = exchange<SIZE - 1, SIZE / 2>(v);
+  if constexpr (SIZE > 2) v = merge_down<SIZE / 4>(v);
+  if constexpr (SIZE < 64) v = sort64<2 * SIZE>(v);
+  return v;
+}
+
+// the wave's parts as one, the same bits in every lane: the largest m, then each
+// lane's sums taken to it, one of the lanes that hold it leaving it out
+__device__ __forceinline__ Part wave_join(Part p) {
+  float m = p.m;
+  m = fmaxf(m, lane_xorf<1>(m));
+  m = fmaxf(m, lane_xorf<2>(m));
+  m = fmaxf(m, lane_xorf<7>(m));
+  m = fmaxf(m, lane_xorf<15>(m));
+  m = fmaxf(m, lane_xorf<16>(m));
+  m = fmaxf(m, lane_xorf<32>(m));
+  const uint64_t holders = __ballot(p.m == m);
+  const bool owner = (int)(threadIdx.x & 63) == __ffsll((unsigned long long)holders) - 1;
+  if (!owner && p.m != kNegInf) {
+    const float d = fmaxf(p.m - m, kFar), w = expf(d);
+    p.t = w * (p.t + d * (1.0f + p.r));
+    p.r = w * (1.0f + p.r);
+  }
+  p.m = m;
+  // (a lane and its mirror hold the same sum by then)
+  p.r += lane_xorf<1>(p.r);   p.t += lane_xorf<1>(p.t);
+  p.r += lane_xorf<2>(p.r);   p.t += lane_xorf<2>(p.t);
+  p.r += lane_xorf<7>(p.r);   p.t += lane_xorf<7>(p.t);
+  p.r += lane_xorf<15>(p.r);  p.t += lane_xorf<15>(p.t);
+  p.r += lane_xorf<16>(p.r);  p.t += lane_xorf<16>(p.t);
+  p.r += lane_xorf<32>(p.r);  p.t += lane_xorf<32>(p.t);
+  return p;
 }
 
 struct Shared {
@@ -114,17 +177,8 @@ __device__ __forceinline__ void best_of_lanes(Shared& sh, uint64_t mine) {
     // of two descending lists of 32, the larger of a[i] and b[31 - i] are the best 32
     const int i = lane & 31, pair = lane >> 5;
     uint64_t k = umax(sh.best[pair * 64 + i], sh.best[pair * 64 + 63 - i]);
-#pragma unroll
-    for (int step = 16; step > 0; step /= 2) {
-      const uint64_t o = shfl_xor64(k, step);
-      k = (lane & step) == 0 ? umax(k, o) : umin(k, o);
-    }
-    k = umax(k, shfl_xor64(k, 63));
-#pragma unroll
-    for (int step = 16; step > 0; step /= 2) {
-      const uint64_t o = shfl_xor64(k, step);
-      k = (lane & step) == 0 ? umax(k, o) : umin(k, o);
-    }
+    k = merge_down<16>(k);
+    k = merge_down<16>(umax(k, lane_xor64<63>(k)));
     if (lane < kTopMax) sh.best[lane] = k;
   }
   __syncthreads();
@@ -158,14 +212,8 @@ __device__ __forceinline__ void best_of_list(Shared& sh, int n, int top) {
     a = sort64(a);
     if (n > 64) {
       b = sort64(b);
-      // a descending, b ascending from the other end: the better half is bitonic
-      a = umax(a, shfl_xor64(b, 63));
-      const int lane = tid;
-#pragma unroll
-      for (int step = 32; step > 0; step /= 2) {
-        const uint64_t o = shfl_xor64(a, step);
-        a = (lane & step) == 0 ? umax(a, o) : umin(a, o);
-      }
+      // both descending: the larger of a[i] and b[63 - i] are the best 64
+      a = merge_down<32>(umax(a, lane_xor64<63>(b)));
     }
     if (tid < kTopMax) sh.best[tid] = a;
   }
@@ -228,8 +276,11 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LpArgs a) {
 
   float m = kNegInf, mr = 0.0f, r = 0.0f, t = 0.0f;  // mr: m, or 0 before the first finite logit
   uint32_t at = 8 * tid;
+  Vals8 next;
+  if (8 * tid < n) next = load_vals8<DT>(x, 8 * tid, n, a.vec);
   for (int64_t c = 8 * tid; c < n; c += 8 * kThreads) {
-    Vals8 v = load_vals8<DT>(x, c, n, a.vec);
+    Vals8 v = next;
+    if (c + 8 * kThreads < n) next = load_vals8<DT>(x, c + 8 * kThreads, n, a.vec);
     if (c + 8 > n) {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
@@ -238,39 +289,33 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LpArgs a) {
     float cm = v.v[0];
 #pragma unroll
     for (int k = 1; k < 8; ++k) cm = fmaxf(cm, v.v[k]);
-    int skip = -1;
     if (cm > m) {  // rescale to the new largest, which the sums below leave out
       if (m != kNegInf) {
         const float d = fmaxf(m - cm, kFar), w = expf(d);
         t = w * (t + d * (1.0f + r));
         r = w * (1.0f + r);
       }
+      int first = 0;
 #pragma unroll
       for (int k = 7; k >= 0; --k)
-        if (v.v[k] == cm) skip = k;
-      at = (uint32_t)c + skip;
+        if (v.v[k] == cm) first = k;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k == first) v.v[k] = kNegInf;
+      at = (uint32_t)c + first;
       m = mr = cm;
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float d = v.v[k] - mr;
-      float e = exp_of(d);
-      if (k == skip) e = 0.0f;
+      const float e = exp_of(d);
       r += e;
       t = fmaf(e, fmaxf(d, kFar), t);
     }
   }
 
-  Part p{m, r, t};
-#pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) {
-    Part o{__shfl_xor(p.m, off), __shfl_xor(p.r, off), __shfl_xor(p.t, off)};
-    // the lower lane's part first on both sides, so that both get the same bits
-    p = (tid & off) ? join(o, p) : join(p, o);
-  }
+  Part p = wave_join(Part{m, r, t});
   if ((tid & 63) == 0) sh.part[tid >> 6] = p;
-  __syncthreads();
-  p = join(join(sh.part[0], sh.part[1]), join(sh.part[2], sh.part[3]));
 
   if (a.top > 0) {
     const uint64_t mine = 8 * tid < n ? key_of(m, at) : 0;
@@ -278,16 +323,20 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LpArgs a) {
     const uint64_t kth = sh.best[a.top - 1];
     if (tid == 0) sh.count = 0;
     __syncthreads();
-    if (mine != 0 && mine >= kth) {
-      for (int64_t c = 8 * tid; c < n; c += 8 * kThreads) {
-        const Vals8 v = load_vals8<DT>(x, c, n, a.vec);
+    // the chunks of the lanes that hold candidates, dealt to all lanes: a key's
+    // index says which lane it came from
+    const int chunks = (int)((n + 8 * kThreads - 1) / (8 * kThreads));
+    for (int u = tid; u < chunks * a.top; u += kThreads) {
+      const uint64_t of = sh.best[u % a.top];
+      const int64_t c = 8 * (((key_index(of) >> 3) & (kThreads - 1)) + (int64_t)(u / a.top) * kThreads);
+      if (of == 0 || c >= n) continue;
+      const Vals8 v = load_vals8<DT>(x, c, n, a.vec);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint64_t key = key_of(v.v[k], (uint32_t)c + k);
-          if (c + k < n && key >= kth) {
-            const int i = atomicAdd(&sh.count, 1);
-            if (i < kList) sh.list[i] = key;
-          }
+      for (int k = 0; k < 8; ++k) {
+        const uint64_t key = key_of(v.v[k], (uint32_t)c + k);
+        if (c + k < n && key >= kth) {
+          const int i = atomicAdd(&sh.count, 1);
+          if (i < kList) sh.list[i] = key;
         }
       }
     }
@@ -310,8 +359,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LpArgs a) {
             if (c + k < n && key < last) b = umax(b, key);
           }
         }
-#pragma unroll
-        for (int off = 1; off < kWave; off <<= 1) b = umax(b, shfl_xor64(b, off));
+        b = sort64(b);
         if ((tid & 63) == 0) sh.list[tid >> 6] = b;
         __syncthreads();
         last = umax(umax(sh.list[0], sh.list[1]), umax(sh.list[2], sh.list[3]));
@@ -319,7 +367,10 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LpArgs a) {
         __syncthreads();
       }
     }
+  } else {
+    __syncthreads();
   }
+  p = join(join(sh.part[0], sh.part[1]), join(sh.part[2], sh.part[3]));
   if (a.nseg == 1) {
     write_row(a, row, p, sh.best, DT);
     return;
@@ -338,11 +389,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_join_kernel(LpArgs a, int d
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x;
   Part p = tid < a.nseg ? a.parts[row * a.nseg + tid] : Part{kNegInf, 0.0f, 0.0f};
-#pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) {
-    Part o{__shfl_xor(p.m, off), __shfl_xor(p.r, off), __shfl_xor(p.t, off)};
-    p = (tid & off) ? join(o, p) : join(p, o);
-  }
+  p = wave_join(p);
   if (tid == 0) sh.part[0] = p;  // at most 64 segments
   if (a.top > 0) {
     // nseg lists in descending order: a lane takes the j-th of 256 / nseg of them in turn
