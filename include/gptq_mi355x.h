@@ -468,14 +468,14 @@ gptq_status fp8_gated_gemm(const uint8_t* X, int64_t tokens, int64_t n, int64_t 
  *   GPTQ_KV_E4M3: fp8_quantize_rows' grid with the group as its block; zeros is
  *     not used.
  * The cache is paged: a token's place is a flat slot, page * page_size + offset
- * with 0 <= slot < pages * page_size.  The slots' codes lie at
+ * with 0 <= slot < pages * page_size < 2^31.  The slots' codes lie at
  *   codes + page * page_stride + offset * slot_stride + head * head_stride (bytes),
  * scales and zeros at
  *   page * param_page_stride + offset * param_slot_stride + head * param_head_stride
  *   + group (elements), any order of pages, slots and heads.
  * head_dim: a multiple of 8, at most 1024.  group_size: a power of two in
  * 16 .. 512 (the last group of a head may be shorter) or -1 = the whole head
- * (head_dim <= 512).  codes 8-byte aligned (4-byte: INT4) and strides multiples
+ * (head_dim <= 512).  heads * head_dim <= 2^23.  codes 8-byte aligned (4-byte: INT4) and strides multiples
  * of 8 (4) bytes.
  *
  * kv_cache_write: rows K and V [tokens][heads][head_dim] (strides in elements,

@@ -43,14 +43,16 @@ gptq_status fp8_operands_ok(int64_t tokens, int64_t n, const void* W, int64_t m,
 
 gptq_status kv_cache_ok(const gptq_kv_cache* c, int64_t tokens) {
   if (!c || !c->codes || !c->scales || c->pages <= 0 || c->page_size <= 0 || c->heads <= 0 ||
-      c->head_dim <= 0 || c->pages > (int64_t(1) << 40) / c->page_size)
+      c->head_dim <= 0)
     return GPTQ_ERR_INVALID_ARG;
   if (c->format != GPTQ_KV_INT4 && c->format != GPTQ_KV_INT8 && c->format != GPTQ_KV_E4M3)
     return GPTQ_ERR_INVALID_ARG;
   const int32_t g = c->group_size;
   if (g != -1 && (g < 16 || g > 512 || (g & (g - 1)) != 0)) return GPTQ_ERR_INVALID_ARG;
+  // (the lanes of a token are counted in 22 bits, slots in 31)
   if (c->head_dim % 8 != 0 || c->head_dim > 1024 || (g == -1 && c->head_dim > 512) ||
-      c->heads > 65536)
+      int64_t(c->heads) * (c->head_dim / 8) > (int64_t(1) << 20) ||
+      c->pages > INT32_MAX / c->page_size)
     return GPTQ_ERR_UNSUPPORTED;
   const int a = c->format == GPTQ_KV_INT4 ? 4 : 8;
   if ((reinterpret_cast<uintptr_t>(c->codes) % a) != 0 || c->page_stride % a != 0 ||

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "kernels.hpp"
+#include "lanes.hpp"
 
 namespace gptq {
 
@@ -77,8 +78,11 @@ __device__ __forceinline__ uint32_t e4m3_decide(float x, float s, uint32_t lo, u
   return r > 0.0f ? hi : r < 0.0f ? lo : ((lo & 1) ? hi : lo);
 }
 
-// 8 codes of x / s.  x * (1 / s) is within 2^-22 |x / s| of the quotient, so the
-// hardware's rounding of that product lowered and raised by 2^-21 brackets the
+// 1 / s to within 2^-23 of itself, for a normal s and 1 / s
+__device__ __forceinline__ float approx_recip(float s) { return __builtin_amdgcn_rcpf(s); }
+
+// 8 codes of x / s, rs = approx_recip(s).  x * rs is within 2^-22 |x / s| of the
+// quotient, so the hardware's rounding of that product lowered and raised by 2^-21 brackets the
 // code; where the two differ (a border of the format is that close: about one
 // value in 10^5) e4m3_decide takes the real quotient.  A non-finite value
 // becomes the NaN code (the instruction's own result for it).

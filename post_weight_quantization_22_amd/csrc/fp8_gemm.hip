@@ -134,7 +134,7 @@ __device__ __forceinline__ void store_part(float* p, int64_t left, int64_t m, f3
 //  - no branch comes between matrix instructions: past the last block the last
 //    one is fetched again into buffers that nothing reads.
 constexpr int kRow = 128;  // bytes of a row of a block
-constexpr int64_t kXcds = 8;
+constexpr uint32_t kXcds = 8;
 
 __device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
 
@@ -186,18 +186,19 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
 
   // tiles in runs per XCD; within a run, groups of 4 token tiles walked before the
   // next row tile, so that the workgroups of an XCD share both operands in its L2
-  const int64_t ntiles = a.ntm * a.ntt, b = blockIdx.x;
-  const int64_t xcd = b % kXcds, idx = b / kXcds;
-  const int64_t per = ntiles / kXcds, rem = ntiles % kXcds;
+  // (in 32 bits: a 64-bit division is a long sequence)
+  const uint32_t ntm = (uint32_t)a.ntm, ntt = (uint32_t)a.ntt, ntiles = ntm * ntt;
+  const uint32_t xcd = blockIdx.x % kXcds, idx = blockIdx.x / kXcds;
+  const uint32_t per = ntiles / kXcds, rem = ntiles % kXcds;
   if (idx >= per + (xcd < rem ? 1 : 0)) return;
-  const int64_t L = xcd * per + (xcd < rem ? xcd : rem) + idx;
-  const int64_t grp = L / (4 * a.ntm), in = L - grp * 4 * a.ntm;
-  const int64_t gsz = min((int64_t)4, a.ntt - 4 * grp);
-  const int64_t tok0 = (4 * grp + in % gsz) * TT;
-  const int64_t row0 = in / gsz * (GATED ? TM / 2 : TM);
+  const uint32_t L = xcd * per + min(xcd, rem) + idx;
+  const uint32_t grp = L / (4 * ntm), in = L - grp * 4 * ntm;
+  const uint32_t gsz = min(4u, ntt - 4 * grp), rt = in / gsz;
+  const int64_t tok0 = (int64_t)(4 * grp + (in - rt * gsz)) * TT;
+  const int64_t row0 = (int64_t)rt * (GATED ? TM / 2 : TM);
   // the split's blocks
   const int nb = (int)a.nb, ks = gridDim.y, z = blockIdx.y;
-  const int c0 = (int)((int64_t)nb * z / ks), c1 = (int)((int64_t)nb * (z + 1) / ks);
+  const int c0 = nb * z / ks, c1 = nb * (z + 1) / ks;  // at most 2^17 blocks, 16 splits
 
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -380,9 +381,9 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
         }
 #pragma unroll
         for (int i = 0; i < MI / 2; ++i) am = fmaxf(am, amax_finite8(h[i]));
-        am = fmaxf(am, __shfl_xor(am, 16));
-        am = fmaxf(am, __shfl_xor(am, 32));
-        const float sc = e4m3_scale(am), rs = 1.0f / sc;
+        am = fmaxf(am, lane_xorf<16>(am));
+        am = fmaxf(am, lane_xorf<32>(am));
+        const float sc = e4m3_scale(am), rs = approx_recip(sc);
         const int64_t t = tok0 + 16 * (wt * NJ + first.value + j) + l16;
         if (t >= a.tokens) continue;
         if (q == 0) a.scales[row0 / kFp8Block * a.ldso + t] = sc;
@@ -513,11 +514,8 @@ __global__ __launch_bounds__(kGemvWaves * 64) void fp8_gemv_kernel(GemvArgs v) {
       const int t = u / nb, b = u - t * nb, c0 = b * kRow + 8 * l16;
       const Vals8 x =
           load_vals8<DT>(reinterpret_cast<const char*>(v.src) + t * v.ldsrc * esz, c0, n, v.vec);
-      float am = amax_finite8(x);
-#pragma unroll
-      for (int off = 1; off < 16; off <<= 1) am = fmaxf(am, __shfl_xor(am, off, 16));
-      const float s = e4m3_scale(am);
-      *reinterpret_cast<uint2*>(dyn + t * xrow + c0) = e4m3_codes8(x, s, 1.0f / s);
+      const float s = e4m3_scale(lanes_max<16>(amax_finite8(x)));
+      *reinterpret_cast<uint2*>(dyn + t * xrow + c0) = e4m3_codes8(x, s, approx_recip(s));
       if (l16 == 0) xs[t * nb + b] = s;
     }
     __syncthreads();

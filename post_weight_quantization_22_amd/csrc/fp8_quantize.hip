@@ -18,12 +18,6 @@ namespace {
 
 constexpr int kLanes = kFp8Block / 8;  // lanes that share a row's block
 
-__device__ __forceinline__ float amax_over_block(float a) {
-#pragma unroll
-  for (int off = 1; off < kLanes; off <<= 1) a = fmaxf(a, __shfl_xor(a, off, kLanes));
-  return a;
-}
-
 // codes c0 .. c0 + 7 of a row of n
 __device__ __forceinline__ void store_codes8(uint8_t* row, int64_t c0, int64_t n, bool vec,
                                              uint2 c) {
@@ -65,8 +59,8 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(RowsArgs a) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) x.v[k] = silu_times(x.v[k], u.v[k]);
   }
-  const float s = e4m3_scale(amax_over_block(amax_finite8(x)));
-  const uint2 c = e4m3_codes8(x, s, 1.0f / s);
+  const float s = e4m3_scale(lanes_max<kLanes>(amax_finite8(x)));
+  const uint2 c = e4m3_codes8(x, s, approx_recip(s));
   store_codes8(a.codes + t * a.ldc, c0, a.n, a.vecc, c);
   if ((threadIdx.x & 15) == 0) a.scales[b * a.lds + t] = s;
 }
@@ -97,12 +91,11 @@ __global__ __launch_bounds__(256) void fp8_blocks_kernel(const void* __restrict_
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) am = fmaxf(am, amax_finite8(x[i]));
-#pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) am = fmaxf(am, __shfl_xor(am, off));
+  am = lanes_max<kWave>(am);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = am;
   __syncthreads();
   am = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-  const float s = e4m3_scale(am), rs = 1.0f / s;
+  const float s = e4m3_scale(am), rs = approx_recip(s);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t r = r0 + 16 * i;

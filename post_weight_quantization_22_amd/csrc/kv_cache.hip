@@ -17,13 +17,14 @@ namespace gptq {
 
 namespace {
 
-// up to this many tokens a workgroup looks for a later token with the same slot
-// by itself; beyond, two small kernels settle the slots' owners first
+// Up to this many tokens a workgroup looks for a later token with the same slot by
+// itself, T reads of 8 bytes from L2 and a compare for each of its tokens; beyond,
+// two small kernels settle the slots' owners first (4.4 us; at 8192 tokens of 8
+// heads of 128 the search would cost 11 to 20 us).
 constexpr int64_t kScanTokens = GPTQ_KV_SMALL_TOKENS;
+constexpr int kSeen = 16;  // slots that a lane compares at a time
 
-// the most tokens that the 256 lanes of a workgroup touch (one lane a token, and
-// a partial one)
-constexpr int kMaxTokensPerGroup = 257;
+constexpr int kThreads = 256;
 
 struct Side {  // one of the two caches and its rows
   char* rows;
@@ -33,9 +34,10 @@ struct Side {  // one of the two caches and its rows
   uint8_t* zeros;
   int64_t cpage, cslot, chead;  // codes, bytes
   int64_t ppage, pslot, phead;  // scales and zeros, elements
-  int32_t heads, dim, glanes;   // glanes: 8-value chunks per group
-  int32_t upt;                  // units (lanes) per token: heads * ng * glanes
-  int32_t ng;
+  int32_t dim, ng;
+  int32_t upt;       // units (lanes) per token: heads * ng << lg
+  int32_t lg;        // log2 of the 8-value chunks per group
+  float per_token, per_head;  // 1 / upt, 1 / (ng << lg)
   int32_t fmt, vec;
 };
 
@@ -43,124 +45,207 @@ struct KvArgs {
   Side s[2];
   const int64_t* slots;
   int64_t tokens, nslots;
-  int32_t page_size;
+  int32_t page_size, page_shift;  // page_shift: log2 of page_size, -1 if it is no power of two
+  int32_t flat;                   // a page's end is the next one's start, in all arrays
   int32_t* info;
-  const int32_t* owner;  // writes: the token that each slot keeps, or null (scan)
+  const int32_t* owner;  // writes: the token that each slot keeps, or null (search)
 };
 
-__device__ __forceinline__ void unit_of(const KvArgs& a, const Side& s, int64_t& t, int& h, int& g,
-                                        int& l, bool& live) {
-  const int64_t base = (int64_t)blockIdx.x * 256;
-  const int64_t t0 = base / s.upt;
-  const uint32_t u = (uint32_t)(base - t0 * s.upt) + threadIdx.x;
-  const uint32_t dt = u / (uint32_t)s.upt, r = u - dt * (uint32_t)s.upt;
-  t = t0 + dt;
-  live = t < a.tokens;
-  const uint32_t per_head = (uint32_t)(s.ng * s.glanes);
-  h = (int)(r / per_head);
-  const uint32_t w = r - (uint32_t)h * per_head;
-  g = (int)(w / (uint32_t)s.glanes);
-  l = (int)(w - (uint32_t)g * s.glanes);
+// x / d for 0 <= x < 2^22 by the reciprocal: (x + 1/2) / d is at least 1 / (2 d)
+// away from an integer, 2^-22 of the quotient or more, and rounds to it by less
+__device__ __forceinline__ int small_div(int x, float recip) {
+  return (int)(((float)x + 0.5f) * recip);
+}
+
+struct Unit {
+  int64_t t;
+  int h, g, l, c0;
+};
+
+// Unit k * 256 + tid of a workgroup that starts at unit `rest` of token t0.
+__device__ __forceinline__ Unit unit_of(const Side& s, int64_t t0, int rest, int k) {
+  const int u = rest + k * kThreads + (int)threadIdx.x;
+  const int dt = small_div(u, s.per_token), r = u - dt * s.upt;
+  Unit o;
+  o.t = t0 + dt;
+  o.h = small_div(r, s.per_head);
+  const int w = r - o.h * (s.ng << s.lg);
+  o.g = w >> s.lg;
+  o.l = w & ((1 << s.lg) - 1);
+  o.c0 = 8 * w;
+  return o;
+}
+
+struct Place {
+  int64_t code, param;  // of the slot's first head
+};
+
+__device__ __forceinline__ Place place_of(const KvArgs& a, const Side& s, int64_t slot) {
+  Place p;
+  if (a.flat) {
+    p.code = slot * s.cslot;
+    p.param = slot * s.pslot;
+    return p;
+  }
+  const int64_t page = a.page_shift >= 0 ? slot >> a.page_shift : slot / a.page_size;
+  const int64_t off = slot - page * a.page_size;
+  p.code = page * s.cpage + off * s.cslot;
+  p.param = page * s.ppage + off * s.pslot;
+  return p;
 }
 
 // Of two tokens of a call with the same slot the later one stays, as it would
 // if they were written one after another: stale[i] says that the i-th token of
 // this workgroup has a later namesake.
-__device__ __forceinline__ void find_stale(const KvArgs& a, int64_t t0, int nt, int64_t* sl,
+__device__ __forceinline__ void find_stale(const KvArgs& a, int64_t t0, int nt, int* sl,
                                            int* stale) {
-  for (int i = threadIdx.x; i < nt; i += 256) {
-    sl[i] = t0 + i < a.tokens ? a.slots[t0 + i] : -1;
+  auto slot_at = [&](int64_t t) -> int {
+    if (t >= a.tokens) return -1;
+    const int64_t v = a.slots[t];
+    return v < 0 || v >= a.nslots ? -1 : (int)v;
+  };
+  for (int i = threadIdx.x; i < nt; i += kThreads) {
+    sl[i] = slot_at(t0 + i);
     stale[i] = 0;
   }
   __syncthreads();
-  for (int64_t u = t0 + 1 + threadIdx.x; u < a.tokens; u += 256) {
-    const int64_t v = a.slots[u];
-    for (int i = 0; i < nt; ++i)
-      if (sl[i] == v && u > t0 + i) stale[i] = 1;
+  // among its own tokens, then all that come behind them
+  for (int i = threadIdx.x; i < nt; i += kThreads)
+    for (int j = i + 1; j < nt; ++j)
+      if (sl[j] == sl[i]) stale[i] = 1;
+  for (int64_t u0 = t0 + nt; u0 < a.tokens; u0 += kSeen * kThreads) {
+    int seen[kSeen];
+#pragma unroll
+    for (int k = 0; k < kSeen; ++k) seen[k] = slot_at(u0 + threadIdx.x + k * kThreads);
+    for (int i = 0; i < nt; ++i) {
+      const int v = sl[i];
+      bool hit = false;
+#pragma unroll
+      for (int k = 0; k < kSeen; ++k) hit |= seen[k] == v;
+      if (hit) stale[i] = 1;  // (padding has no namesake that matters)
+    }
   }
   __syncthreads();
 }
 
-template <int LPG>
-__device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-  for (int off = 1; off < LPG; off <<= 1) v = fmaxf(v, __shfl_xor(v, off, LPG));
-  return v;
+// Group parameters of rtn_minmax's grid from the group's range, bit for bit
+// minmax_params': the zero-point's quotient by the reciprocal of span (within
+// 2^-21 of it, 255 at most: 1.3e-4), the IEEE division where a half-integer is near.
+__device__ __forceinline__ void minmax_params_fast(float lo, float hi, float maxq, float& scale,
+                                                   float& zero) {
+  if (lo == hi) {
+    lo = -1.0f;
+    hi = 1.0f;
+  }
+  const float span = hi - lo, num = __fmul_rn(-lo, maxq);
+  scale = __fdiv_rn(span, maxq);
+  const float z = num * approx_recip(span);
+  zero = rintf(z);
+  // (false for a number only: a span whose reciprocal is no normal number divides)
+  if (!(fabsf(z - zero) < 0.4998f) || !(span > 0x1p-120f && span < 0x1p120f))
+    zero = rintf(__fdiv_rn(num, span));
 }
 
-template <int DT, int LPG>
-__global__ __launch_bounds__(256) void kv_write_kernel(KvArgs a) {
+// The 8 integer codes of quant_code(x, scale, zero, maxq).  A quotient is at most
+// 255 and its form by the reciprocal within 2^-22 of it, 6.1e-5: the integers
+// agree unless a half-integer is that near, and then the division decides.
+__device__ __forceinline__ void int_codes8(const Vals8& x, float scale, float zero, float maxq,
+                                           uint32_t* q) {
+  const float rs = approx_recip(scale);
+  float c[8], far = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float t = x.v[e] * rs;
+    c[e] = rintf(t);
+    far = fmaxf(far, fabsf(t - c[e]));  // (a NaN has code 0 either way)
+  }
+  if (!(far < 0.4999f) || !(scale > 0x1p-120f && scale < 0x1p120f)) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c[e] = rintf(__fdiv_rn(x.v[e], scale));
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) q[e] = (uint32_t)fminf(fmaxf(c[e] + zero, 0.0f), maxq);
+}
+
+// K units a lane, their loads in flight together.
+template <int DT, int LPG, int K>
+__global__ __launch_bounds__(kThreads) void kv_write_kernel(KvArgs a) {
   const Side& s = a.s[blockIdx.y];
   if (s.codes == nullptr) return;
-  const int64_t first = (int64_t)blockIdx.x * 256 / s.upt;
-  if (first >= a.tokens) return;
-  __shared__ int64_t sl[kMaxTokensPerGroup];
-  __shared__ int stale[kMaxTokensPerGroup];
-  int64_t t;
-  int h, g, l;
-  bool live;
-  unit_of(a, s, t, h, g, l, live);
-  if (a.owner == nullptr) {
-    const int nt = (int)(((int64_t)blockIdx.x * 256 + 255) / s.upt - first) + 1;
-    find_stale(a, first, nt, sl, stale);
-  }
-  const int64_t slot = live ? a.slots[t] : -1;
-  if (slot >= a.nslots) {
-    if (a.info) *a.info = 1;
-    live = false;
-  }
-  if (slot < 0) live = false;
-  if (live) {
-    if (a.owner) live = a.owner[slot] == (int32_t)t;
-    else live = stale[t - first] == 0;
-  }
-  const int c0 = (g * s.glanes + l) * 8;
-  const bool here = live && c0 < s.dim;
-  Vals8 x;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) x.v[k] = 0.0f;
+  const uint32_t base = blockIdx.x * (kThreads * K);  // fewer than 2^31 units in all
+  const int64_t t0 = base / (uint32_t)s.upt;
+  if (t0 >= a.tokens) return;
+  const int rest = (int)(base - (uint32_t)t0 * s.upt);
+  // one lane a token at most, and a partial one in front
+  __shared__ int sl[kThreads * K + 1], stale[kThreads * K + 1];
+  Unit un[K];
+  Vals8 x[K];
+  bool live[K];
+  int64_t slot[K];
   constexpr int esz = DT == GPTQ_BF16 ? 2 : 4;
-  if (here)
-    x = load_vals8<DT>(s.rows + (t * s.tstride + h * s.hstride) * esz, c0, s.dim, s.vec);
-  float scale, zero = 0.0f;
-  uint2 code;
-  if (s.fmt == GPTQ_KV_E4M3) {
-    scale = e4m3_scale(group_max<LPG>(amax_finite8(x)));
-    code = e4m3_codes8(x, scale, 1.0f / scale);
-  } else {
-    const float maxq = s.fmt == GPTQ_KV_INT4 ? 15.0f : 255.0f;
-    float lo = 0.0f, hi = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      lo = fminf(lo, x.v[k]);
-      hi = fmaxf(hi, x.v[k]);
-    }
-    lo = -group_max<LPG>(-lo);
-    hi = group_max<LPG>(hi);
-    if (s.zeros) minmax_params(lo, hi, maxq, scale, zero);
-    else sym_params(fmaxf(-lo, hi), maxq, scale, zero);
-    const float rs = 1.0f / scale;
-    uint32_t q[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) q[k] = (uint32_t)quant_code_fast(x.v[k], scale, rs, zero, maxq);
-    if (s.fmt == GPTQ_KV_INT4) {
-      code.x = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) code.x |= q[k] << (4 * k);
-    } else {
-      code.x = q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24;
-      code.y = q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24;
-    }
+  for (int k = 0; k < K; ++k) {
+    un[k] = unit_of(s, t0, rest, k);
+    live[k] = un[k].t < a.tokens;
+    slot[k] = live[k] ? a.slots[un[k].t] : -1;
   }
-  if (!here) return;
-  const int64_t page = slot / a.page_size, off = slot - page * a.page_size;
-  uint8_t* row = s.codes + page * s.cpage + off * s.cslot + h * s.chead;
-  if (s.fmt == GPTQ_KV_INT4) *reinterpret_cast<uint32_t*>(row + c0 / 2) = code.x;
-  else *reinterpret_cast<uint2*>(row + c0) = code;
-  if (l == 0) {
-    const int64_t p = page * s.ppage + off * s.pslot + h * s.phead + g;
-    s.scales[p] = scale;
-    if (s.zeros) s.zeros[p] = (uint8_t)zero;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[k].v[e] = 0.0f;
+    if (live[k] && un[k].c0 < s.dim)
+      x[k] = load_vals8<DT>(s.rows + (un[k].t * s.tstride + un[k].h * s.hstride) * esz, un[k].c0,
+                            s.dim, s.vec);
+  }
+  if (a.owner == nullptr)
+    find_stale(a, t0, small_div(rest + kThreads * K - 1, s.per_token) + 1, sl, stale);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (slot[k] >= a.nslots) {
+      if (a.info) *a.info = 1;
+      live[k] = false;
+    }
+    if (slot[k] < 0) live[k] = false;
+    if (live[k])
+      live[k] = a.owner ? a.owner[slot[k]] == (int32_t)un[k].t : stale[un[k].t - t0] == 0;
+    float scale, zero = 0.0f;
+    uint2 code;
+    if (s.fmt == GPTQ_KV_E4M3) {
+      scale = e4m3_scale(lanes_max<LPG>(amax_finite8(x[k])));
+      code = e4m3_codes8(x[k], scale, approx_recip(scale));
+    } else {
+      const float maxq = s.fmt == GPTQ_KV_INT4 ? 15.0f : 255.0f;
+      float lo = 0.0f, hi = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        lo = fminf(lo, x[k].v[e]);
+        hi = fmaxf(hi, x[k].v[e]);
+      }
+      lo = -lanes_max<LPG>(-lo);
+      hi = lanes_max<LPG>(hi);
+      if (s.zeros) minmax_params_fast(lo, hi, maxq, scale, zero);
+      else sym_params(fmaxf(-lo, hi), maxq, scale, zero);
+      uint32_t q[8];
+      int_codes8(x[k], scale, zero, maxq, q);
+      if (s.fmt == GPTQ_KV_INT4) {
+        code.x = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) code.x |= q[e] << (4 * e);
+      } else {
+        code.x = q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24;
+        code.y = q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24;
+      }
+    }
+    if (!live[k] || un[k].c0 >= s.dim) continue;
+    const Place p = place_of(a, s, slot[k]);
+    uint8_t* row = s.codes + p.code + un[k].h * s.chead;
+    if (s.fmt == GPTQ_KV_INT4) *reinterpret_cast<uint32_t*>(row + un[k].c0 / 2) = code.x;
+    else *reinterpret_cast<uint2*>(row + un[k].c0) = code;
+    if (un[k].l == 0) {
+      const int64_t i = p.param + un[k].h * s.phead + un[k].g;
+      s.scales[i] = scale;
+      if (s.zeros) s.zeros[i] = (uint8_t)zero;
+    }
   }
 }
 
@@ -208,61 +293,73 @@ __device__ __forceinline__ void store_vals8(char* row, int c0, bool vec, const f
   }
 }
 
-template <int DT>
-__global__ __launch_bounds__(256) void kv_read_kernel(KvArgs a) {
+// K units a lane, their loads in flight together.
+template <int DT, int K>
+__global__ __launch_bounds__(kThreads) void kv_read_kernel(KvArgs a) {
   const Side& s = a.s[blockIdx.y];
   if (s.codes == nullptr) return;
-  int64_t t;
-  int h, g, l;
-  bool live;
-  unit_of(a, s, t, h, g, l, live);
-  const int c0 = (g * s.glanes + l) * 8;
-  if (!live || c0 >= s.dim) return;
+  const uint32_t base = blockIdx.x * (kThreads * K);
+  const int64_t t0 = base / (uint32_t)s.upt;
+  const int rest = (int)(base - (uint32_t)t0 * s.upt);
   constexpr int esz = DT == GPTQ_BF16 ? 2 : 4;
-  char* out = s.rows + (t * s.tstride + h * s.hstride) * esz;
-  float v[8];
-  const int64_t slot = a.slots[t];
-  if (slot < 0 || slot >= a.nslots) {  // padding reads as zeros
-    if (slot >= 0 && a.info) *a.info = 1;
+  const float mid = s.fmt == GPTQ_KV_INT4 ? 8.0f : 128.0f;
+  Unit un[K];
+  bool live[K];
+  int64_t slot[K];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = 0.0f;
-    store_vals8<DT>(out, c0, s.vec, v);
-    return;
+  for (int k = 0; k < K; ++k) {
+    un[k] = unit_of(s, t0, rest, k);
+    live[k] = un[k].t < a.tokens && un[k].c0 < s.dim;
+    slot[k] = live[k] ? a.slots[un[k].t] : -1;
   }
-  const int64_t page = slot / a.page_size, off = slot - page * a.page_size;
-  const uint8_t* row = s.codes + page * s.cpage + off * s.cslot + h * s.chead;
-  const int64_t p = page * s.ppage + off * s.pslot + h * s.phead + g;
-  const float scale = s.scales[p];
-  if (s.fmt == GPTQ_KV_E4M3) {
-    const uint2 c = *reinterpret_cast<const uint2*>(row + c0);
-    v[0] = __builtin_amdgcn_cvt_f32_fp8((int)c.x, 0);
-    v[1] = __builtin_amdgcn_cvt_f32_fp8((int)c.x, 1);
-    v[2] = __builtin_amdgcn_cvt_f32_fp8((int)c.x, 2);
-    v[3] = __builtin_amdgcn_cvt_f32_fp8((int)c.x, 3);
-    v[4] = __builtin_amdgcn_cvt_f32_fp8((int)c.y, 0);
-    v[5] = __builtin_amdgcn_cvt_f32_fp8((int)c.y, 1);
-    v[6] = __builtin_amdgcn_cvt_f32_fp8((int)c.y, 2);
-    v[7] = __builtin_amdgcn_cvt_f32_fp8((int)c.y, 3);
+  uint2 code[K];
+  float scale[K], zero[K];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] *= scale;
-  } else if (s.fmt == GPTQ_KV_INT4) {
-    const uint32_t c = *reinterpret_cast<const uint32_t*>(row + c0 / 2);
-    const float z = s.zeros ? (float)s.zeros[p] : 8.0f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = ((float)((c >> (4 * k)) & 15u) - z) * scale;
-  } else {
-    const uint2 c = *reinterpret_cast<const uint2*>(row + c0);
-    const float z = s.zeros ? (float)s.zeros[p] : 128.0f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      v[k] = ((float)(((k < 4 ? c.x : c.y) >> (8 * (k & 3))) & 255u) - z) * scale;
+  for (int k = 0; k < K; ++k) {
+    // padding reads as zeros: code and zero 0, scale 0
+    code[k] = make_uint2(0, 0);
+    scale[k] = zero[k] = 0.0f;
+    if (slot[k] >= a.nslots && a.info) *a.info = 1;
+    if (slot[k] < 0 || slot[k] >= a.nslots) continue;
+    const Place p = place_of(a, s, slot[k]);
+    const uint8_t* row = s.codes + p.code + un[k].h * s.chead;
+    const int64_t i = p.param + un[k].h * s.phead + un[k].g;
+    if (s.fmt == GPTQ_KV_INT4) code[k].x = *reinterpret_cast<const uint32_t*>(row + un[k].c0 / 2);
+    else code[k] = *reinterpret_cast<const uint2*>(row + un[k].c0);
+    scale[k] = s.scales[i];
+    zero[k] = s.zeros ? (float)s.zeros[i] : mid;
   }
-  store_vals8<DT>(out, c0, s.vec, v);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (!live[k]) continue;
+    const uint2 c = code[k];
+    float v[8];
+    if (s.fmt == GPTQ_KV_E4M3) {
+      v[0] = __builtin_amdgcn_cvt_f32_fp8((int)c.x, 0);
+      v[1] = __builtin_amdgcn_cvt_f32_fp8((int)c.x, 1);
+      v[2] = __builtin_amdgcn_cvt_f32_fp8((int)c.x, 2);
+      v[3] = __builtin_amdgcn_cvt_f32_fp8((int)c.x, 3);
+      v[4] = __builtin_amdgcn_cvt_f32_fp8((int)c.y, 0);
+      v[5] = __builtin_amdgcn_cvt_f32_fp8((int)c.y, 1);
+      v[6] = __builtin_amdgcn_cvt_f32_fp8((int)c.y, 2);
+      v[7] = __builtin_amdgcn_cvt_f32_fp8((int)c.y, 3);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= scale[k];
+    } else if (s.fmt == GPTQ_KV_INT4) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = ((float)((c.x >> (4 * e)) & 15u) - zero[k]) * scale[k];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        v[e] = ((float)(((e < 4 ? c.x : c.y) >> (8 * (e & 3))) & 255u) - zero[k]) * scale[k];
+    }
+    store_vals8<DT>(s.rows + (un[k].t * s.tstride + un[k].h * s.hstride) * esz, un[k].c0, s.vec, v);
+  }
 }
 
-inline int pow2_at_least(int v) {
-  int p = 1;
-  while (p < v) p *= 2;
+inline int log2_at_least(int v) {
+  int p = 0;
+  while ((1 << p) < v) ++p;
   return p;
 }
 
@@ -277,18 +374,24 @@ Side side_of(const gptq_kv_cache* c, const KvRows& r, int dt) {
   s.zeros = c->format == GPTQ_KV_E4M3 ? nullptr : c->zeros;
   s.cpage = c->page_stride; s.cslot = c->slot_stride; s.chead = c->head_stride;
   s.ppage = c->param_page_stride; s.pslot = c->param_slot_stride; s.phead = c->param_head_stride;
-  s.heads = c->heads;
   s.dim = c->head_dim;
   // a group as long as the head or longer is the whole head
   const int g = c->group_size > 0 && c->group_size < c->head_dim ? c->group_size : c->head_dim;
-  s.glanes = pow2_at_least((g + 7) / 8);
+  s.lg = log2_at_least((g + 7) / 8);
   s.ng = (int)ceil_div(c->head_dim, g);
-  s.upt = s.heads * s.ng * s.glanes;
+  s.upt = c->heads * (s.ng << s.lg);
+  s.per_token = 1.0f / (float)s.upt;
+  s.per_head = 1.0f / (float)(s.ng << s.lg);
   s.fmt = c->format;
   const int per16 = dt == GPTQ_BF16 ? 8 : 4;
   s.vec = (reinterpret_cast<uintptr_t>(r.p) & 15) == 0 && r.token_stride % per16 == 0 &&
           r.head_stride % per16 == 0;
   return s;
+}
+
+bool flat(const gptq_kv_cache* c) {
+  return !c || (c->page_stride == c->page_size * c->slot_stride &&
+                c->param_page_stride == c->page_size * c->param_slot_stride);
 }
 
 KvArgs args_of(const gptq_kv_cache* kc, const gptq_kv_cache* vc, const int64_t* slots,
@@ -301,9 +404,14 @@ KvArgs args_of(const gptq_kv_cache* kc, const gptq_kv_cache* vc, const int64_t* 
   a.tokens = tokens;
   a.nslots = c->pages * c->page_size;
   a.page_size = c->page_size;
+  a.page_shift = (1 << log2_at_least(c->page_size)) == c->page_size ? log2_at_least(c->page_size) : -1;
+  a.flat = flat(kc) && flat(vc);
   a.info = info;
   return a;
 }
+
+// four units a lane where that still gives every CU four workgroups
+int units_a_lane(int64_t units) { return units >= int64_t(1) << 20 ? 4 : 1; }
 
 }  // namespace
 
@@ -323,25 +431,23 @@ hipError_t launch_kv_write(const KvRows& k, const KvRows& v, int dt, int64_t tok
     a.owner = owner;
   }
   // one launch for both caches where their groups span the same lanes
-  for (int pass = 0; pass < 2; ++pass) {
+  const int la = a.s[0].codes ? 1 << a.s[0].lg : 0, lb = a.s[1].codes ? 1 << a.s[1].lg : 0;
+  const bool together = la == lb || la == 0 || lb == 0;
+  for (int pass = 0; pass < (together ? 1 : 2); ++pass) {
     KvArgs p = a;
-    const int la = a.s[0].codes ? a.s[0].glanes : 0, lb = a.s[1].codes ? a.s[1].glanes : 0;
-    int lpg;
-    if (la == lb || la == 0 || lb == 0) {
-      if (pass == 1) break;
-      lpg = la ? la : lb;
-    } else {
+    int lpg = la ? la : lb;
+    if (!together) {
       p.s[1 - pass] = Side{};
       lpg = pass == 0 ? la : lb;
     }
-    const int64_t upt = hmax(p.s[0].upt, p.s[1].upt);
-    const dim3 grid((unsigned)ceil_div(tokens * upt, 256), 2);
-#define GPTQ_KV(L)                                                                               \
-  case L:                                                                                        \
-    if (dt == GPTQ_BF16)                                                                         \
-      hipLaunchKernelGGL((kv_write_kernel<GPTQ_BF16, L>), grid, dim3(256), 0, stream, p);        \
-    else                                                                                         \
-      hipLaunchKernelGGL((kv_write_kernel<GPTQ_F32, L>), grid, dim3(256), 0, stream, p);         \
+    const int64_t units = tokens * hmax(p.s[0].upt, p.s[1].upt);
+    const dim3 grid((unsigned)ceil_div(units, (int64_t)kThreads), 2), block(kThreads);
+#define GPTQ_KV(L)                                                                             \
+  case L:                                                                                      \
+    if (dt == GPTQ_BF16)                                                                       \
+      hipLaunchKernelGGL((kv_write_kernel<GPTQ_BF16, L, 1>), grid, block, 0, stream, p);       \
+    else                                                                                       \
+      hipLaunchKernelGGL((kv_write_kernel<GPTQ_F32, L, 1>), grid, block, 0, stream, p);        \
     break;
     switch (lpg) {
       GPTQ_KV(1)
@@ -362,10 +468,16 @@ hipError_t launch_kv_read(const gptq_kv_cache* kc, const gptq_kv_cache* vc, cons
                           int64_t tokens, const KvRows& k, const KvRows& v, int dt, int32_t* info,
                           hipStream_t stream) {
   const KvArgs a = args_of(kc, vc, slots, tokens, k, v, dt, info);
-  const int64_t upt = hmax(a.s[0].upt, a.s[1].upt);
-  const dim3 grid((unsigned)ceil_div(tokens * upt, 256), 2);
-  if (dt == GPTQ_BF16) hipLaunchKernelGGL(kv_read_kernel<GPTQ_BF16>, grid, dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL(kv_read_kernel<GPTQ_F32>, grid, dim3(256), 0, stream, a);
+  const int64_t units = tokens * hmax(a.s[0].upt, a.s[1].upt);
+  const int per = units_a_lane(units);
+  const dim3 grid((unsigned)ceil_div(units, (int64_t)kThreads * per), 2), block(kThreads);
+  if (per == 4) {
+    if (dt == GPTQ_BF16) hipLaunchKernelGGL((kv_read_kernel<GPTQ_BF16, 4>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((kv_read_kernel<GPTQ_F32, 4>), grid, block, 0, stream, a);
+  } else {
+    if (dt == GPTQ_BF16) hipLaunchKernelGGL((kv_read_kernel<GPTQ_BF16, 1>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((kv_read_kernel<GPTQ_F32, 1>), grid, block, 0, stream, a);
+  }
   return hipGetLastError();
 }
 

@@ -113,6 +113,36 @@ def test_write_and_read(fmt, asym, T, H, D, group, page, order, xdt, ydt):
     assert torch.all(Ko[..., D:] == 3) and torch.all(Vo[..., D:] == 3)
 
 
+@pytest.mark.parametrize("page,order", [(16, "phd"), (16, "hpd"), (24, "hpd")])
+@pytest.mark.parametrize("fmt,asym", FORMS)
+def test_long_calls(fmt, asym, page, order):
+    """Enough rows for several units a lane, heads that fill no wave: every row's codes
+    against rtn_minmax's form of the oracle, whole arrays at once."""
+    q = need_gpu()
+    rng = np.random.default_rng(page)
+    T, H, D, G = 6001, 3, 160, 64
+    pages = -(-6100 // page)
+    kc, vc = (Cache(q, pages, page, H, D, fmt, G, asym, order) for _ in range(2))
+    K, V = (torch.from_numpy(rng.normal(size=(T, H, D))).to(torch.bfloat16) for _ in range(2))
+    slots = rng.permutation(pages * page)[:T]
+    sd = torch.from_numpy(slots).cuda()
+    say("kv long", fmt, asym, page, order)
+    q.kv_cache_write(K.cuda(), V.cuda(), sd, kc.h, vc.h)
+    Ko, Vo = (torch.empty((T, H, D), device="cuda") for _ in range(2))
+    q.kv_cache_read(kc.h, vc.h, sd, Ko, Vo)
+    for c, x, o in ((kc, K, Ko), (vc, V, Vo)):
+        codes, scales, zeros = c.flat()
+        qc, qs, qz = lowp.kv_quantize(x.double().numpy().reshape(T * H, D), fmt, G, asym)
+        assert np.array_equal(codes[slots], lowp.kv_pack(qc, fmt).reshape(T, H, -1))
+        assert np.array_equal(scales[slots], qs.astype(np.float32).reshape(T, H, -1))
+        if asym:
+            assert np.array_equal(zeros[slots], qz.astype(np.uint8).reshape(T, H, -1))
+        rest = np.setdiff1d(np.arange(codes.shape[0]), slots)
+        assert np.all(codes[rest] == 0x55) and np.all(scales[rest] == -1)
+        want = lowp.kv_dequantize(qc, qs, qz, fmt, G).reshape(T, H, D)
+        assert np.all(np.abs(host(o) - want) <= 2.0 ** -23 * np.abs(want))
+
+
 @pytest.mark.parametrize("fmt,asym", FORMS)
 def test_integers_equal_rtn_minmax(fmt, asym):
     """The integer formats' grid is rtn_minmax's: the same codes, scales and zeros."""
@@ -137,7 +167,7 @@ def test_integers_equal_rtn_minmax(fmt, asym):
         assert torch.equal(c.zeros.view(T, -1).float(), z)
 
 
-@pytest.mark.parametrize("T", [6, 700, 1024, 1025, 3000])
+@pytest.mark.parametrize("T", [6, 700, 1024, 1025, 3000, 9000])
 def test_repeated_slots_keep_the_last_row(T):
     q = need_gpu()
     rng = np.random.default_rng(T)
@@ -225,8 +255,8 @@ def test_codes_past_32_bits():
 
 def test_cache_captured_and_replayed():
     q = need_gpu()
-    T, H, D = 1500, 2, 64
-    c, e = (Cache(q, 100, 16, H, D, "int4", 32, True) for _ in range(2))
+    T, H, D = 9500, 2, 64
+    c, e = (Cache(q, 600, 16, H, D, "int4", 32, True) for _ in range(2))
     x = torch.zeros((T, H, D), device="cuda")
     slots = torch.zeros(T, dtype=torch.int64, device="cuda")
     out, want = torch.empty_like(x), torch.empty_like(x)
@@ -235,7 +265,7 @@ def test_cache_captured_and_replayed():
         q.kv_cache_write(x, None, slots, cache.h, None)
         q.kv_cache_read(cache.h, None, slots, o, None)
 
-    slots.copy_(torch.randperm(1600)[:T])
+    slots.copy_(torch.randperm(9600)[:T])
     step(e, want)
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
@@ -243,7 +273,7 @@ def test_cache_captured_and_replayed():
         step(c, out)
     for turn in range(4):
         x.copy_(torch.randn(x.shape))
-        slots.copy_(torch.randint(0, 1600, (T,)))
+        slots.copy_(torch.randint(0, 9600, (T,)))
         g.replay()
         torch.cuda.synchronize()
         step(e, want)

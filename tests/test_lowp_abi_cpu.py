@@ -105,8 +105,8 @@ def test_cache():
                                 slots, t, K, 128, 64, V, 128, 64, dt, None, None)
 
     assert write(t=0) == OK and read(t=0) == OK
-    assert write(t=4096) == WS  # a large call settles repeated slots in the workspace
-    assert gq.kv_cache_write_workspace_size(4096, _cache()) == 4 * 64
+    assert write(t=10000) == WS  # a large call settles repeated slots in the workspace
+    assert gq.kv_cache_write_workspace_size(10000, _cache()) == 4 * 64
     small = _lib.GPTQ_KV_SMALL_TOKENS
     assert gq.kv_cache_write_workspace_size(small, _cache()) == 0
     assert gq.kv_cache_write_workspace_size(small + 1, _cache()) > 0
@@ -121,7 +121,8 @@ def test_cache():
                    dict(kc=_cache(heads=0)), dict(kc=_cache(pages=0))):
             assert f(**kw) == BAD, kw
         for kw in (dict(kc=_cache(head_dim=60)), dict(kc=_cache(head_dim=1032)),
-                   dict(kc=_cache(head_dim=520, group_size=-1)), dict(t=1 << 24, kc=_cache(heads=512))):
+                   dict(kc=_cache(head_dim=520, group_size=-1)),
+                   dict(kc=_cache(heads=1 << 18)), dict(kc=_cache(pages=1 << 28)), dict(t=1 << 24, kc=_cache(heads=512))):
             assert f(**kw) == UNSUP, kw
     # two values to a byte: 4-byte codes
     assert read(t=0, kc=_cache(format=0, codes=FAKE + 4, slot_stride=132)) == OK
