@@ -219,7 +219,7 @@ def load() -> ctypes.CDLL:
     lib.fp8_gated_gemm.restype = _i32
     lib.fp8_gated_gemm.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64,
                                    _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _sz, _vp]
-    _kvp = ctypes.POINTER(GPTQKVCache)
+    _kvp = _vp  # the address of a GPTQKVCache
     lib.kv_cache_write_workspace_size.restype = _i32
     lib.kv_cache_write_workspace_size.argtypes = [_i64, _kvp, ctypes.POINTER(_sz)]
     lib.kv_cache_write.restype = _i32
@@ -905,7 +905,7 @@ def make_kv_cache(codes, scales, zeros, head_dim: int, fmt: str = "int8",
     c.device = d
     c.row = (heads, head_dim)
     c.paging = (pages, page_size)
-    c.ref = ctypes.byref(c)
+    c.ref = ctypes.addressof(c)
     return c
 
 
@@ -914,27 +914,25 @@ _KV_NONE = (None, 0, 0)
 
 def _kv_rows(t, name: str, cache: Optional[GPTQKVCache], tokens: int, device, dtype):
     """(pointer, token stride, head stride) of rows [tokens, heads, head_dim]."""
-    if cache is None:
-        if t is not None:
-            raise ValueError(f"{name} is given without its cache")
-        return _KV_NONE
-    if t is None:
-        raise ValueError(f"{name} is required: its cache is given")
+    if cache is None or t is None:
+        if cache is None and t is None:
+            return _KV_NONE
+        raise ValueError(f"{name}: rows and their cache come together")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype} for keys and values alike")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or stride[2] != 1 or shape[0] != tokens or shape[1:] != cache.row:
+        raise ValueError(f"{name}: shape {tuple(shape)} strides {stride}, expected "
+                         f"{(tokens, *cache.row)} with a dense last dimension")
     if cache.device != device or t.device != device:
         raise ValueError(f"{name}: rows on {t.device}, cache on {cache.device}, "
                          f"expected {device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype} for keys and values alike")
-    shape, stride = t.shape, t.stride()
-    if shape != (tokens, *cache.row) or stride[2] != 1:
-        raise ValueError(f"{name}: shape {tuple(shape)} strides {stride}, expected "
-                         f"{(tokens, *cache.row)} with a dense last dimension")
     return t.data_ptr(), stride[0], stride[1]
 
 
 def _kv_call(K, V, slots, kc, vc, info):
     rows = K if K is not None else V
-    if rows is None or (kc is None and vc is None):
+    if rows is None:
         raise ValueError("keys with their cache or values with theirs are required")
     d = _on_gpu(slots, "slots")
     if _KIND.get(slots.dtype) != "l" or slots.dim() != 1 or not slots.is_contiguous():
@@ -942,16 +940,15 @@ def _kv_call(K, V, slots, kc, vc, info):
     if info is not None:
         _buf(info, "info", (1,), ("int32",), d)
     dtype = rows.dtype
-    kind = _KIND.get(dtype)
-    if kind not in ("b", "f"):
+    dt = _FLOAT.get(_KIND.get(dtype))
+    if dt is None:
         raise TypeError(f"rows: dtype {dtype}, expected bfloat16 or float32")
     tokens = slots.shape[0]
     k = _kv_rows(K, "K", kc, tokens, d, dtype)
     v = _kv_rows(V, "V", vc, tokens, d, dtype)
     if kc is not None and vc is not None and kc.paging != vc.paging:
         raise ValueError("the two caches differ in pages or page_size")
-    return (d, tokens, k, v, GPTQ_BF16 if kind == "b" else GPTQ_F32,
-            None if kc is None else kc.ref, None if vc is None else vc.ref)
+    return d, tokens, k, v, dt, None if kc is None else kc.ref, None if vc is None else vc.ref
 
 
 def kv_cache_write_workspace_size(tokens: int, cache: GPTQKVCache) -> int:
