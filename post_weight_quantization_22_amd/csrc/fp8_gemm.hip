@@ -172,7 +172,12 @@ __device__ __forceinline__ float gated(float g, float u) {
 // the tile quantizes its part of h itself: each pair of waves exchanges halves of
 // their results through LDS, a lane then has 32 of a token's 128 values, and its
 // three neighbours at the same token the others.
-template <int TM, int TT, int WM, int WT, bool EXACT, bool GATED = false>
+template <int N>
+__device__ __forceinline__ void wait_vm() {  // at most N vector loads outstanding
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
+}
+
+template <int TM, int TT, int WM, int WT, int STAGES, bool EXACT, bool GATED = false>
 __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a) {
   static_assert(!GATED || (TM == 2 * kFp8Block && WM == 2 && !EXACT), "a gate and an up block");
   constexpr int MI = TM / WM / 16, NJ = TT / WT / 16, NW = WM * WT;
@@ -182,7 +187,11 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
   static_assert(PX % 2 == 0 || PX == 1, "the swizzle of a piece goes by its parity");
   static_assert(TM / WM <= kFp8Block && kFp8Block % (TM / WM) == 0, "a wave's rows share a scale");
   static_assert(TT % 64 == 0 && TT / 64 <= NW, "a wave fetches the scales of 64 tokens");
-  __shared__ __align__(16) uint8_t smem[2 * STAGE + 2 * TT * 4];
+  constexpr int NS = TT / 64, LAG = STAGES - 1;  // waves that fetch scales; blocks in flight
+  // with three buffers or more the next block is there while one is multiplied, and
+  // its first operands are read behind this one's last matrix instructions
+  constexpr bool AHEAD = STAGES >= 3;
+  __shared__ __align__(16) uint8_t smem[STAGES * STAGE + STAGES * TT * 4];
 
   // tiles in runs per XCD; within a run, groups of 4 token tiles walked before the
   // next row tile, so that the workgroups of an XCD share both operands in its L2
@@ -232,10 +241,10 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
   // scales of the tile's tokens, 64 by each of the first waves
   const uint32_t so = 4 * (uint32_t)min(64 * wv + lane, tmax);
   auto issue_s = [&](int c, int buf) {
-    if (wv < TT / 64)
-      lds_dma4(a.sx + tok0 + c * a.lds, so, lds0 + 2 * STAGE + buf * TT * 4 + 256 * wv);
+    if (wv < NS)
+      lds_dma4(a.sx + tok0 + c * a.lds, so, lds0 + STAGES * STAGE + buf * TT * 4 + 256 * wv);
   };
-  const float* sxl = reinterpret_cast<const float*>(smem + 2 * STAGE);
+  const float* sxl = reinterpret_cast<const float*>(smem + STAGES * STAGE);
   const int64_t wrow = row0 + (GATED ? 0 : wm * (TM / WM));
   const int64_t srow = (wrow < a.m ? wrow : a.m - 1) / kFp8Block;
   const float* swp = GATED && wm == 1 ? a.sw2 + srow * a.ldsw2 : a.sw + srow * a.ldsw;
@@ -256,40 +265,75 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
     dp[j] = f32x4{0.f, 0.f, 0.f, 0.f};
     sp[j] = 0.f;
   }
-  issue_s(c0, 0);
 #pragma unroll
-  for (int j = 0; j < PX; ++j) issue_x(j, c0, 0);
+  for (int p = 0; p < LAG; ++p) {
+    const int c = min(c0 + p, c1 - 1);
+    issue_s(c, p);
 #pragma unroll
-  for (int j = 0; j < PW; ++j) issue_w(j, c0, 0);
+    for (int j = 0; j < PX; ++j) issue_x(j, c, p);
+#pragma unroll
+    for (int j = 0; j < PW; ++j) issue_w(j, c, p);
+  }
+  // this wave's DMA is there but for that of the LATER last blocks issued
+  auto landed = [&](auto later) {
+    constexpr int N = decltype(later)::value;
+    if (N > 0 && wv < NS) wait_vm<N * (PX + PW + 1)>();
+    else wait_vm<N * (PX + PW)>();
+  };
+  // the row's end: zeros in X past it
+  auto zero_tail = [&](int c, uint8_t* xst) {
+    for (int i = threadIdx.x; i < TT * 8; i += NW * 64) {
+      const int row = i >> 3, sg = i & 7;
+      if (c * kRow + 16 * sg >= n)
+        *reinterpret_cast<i32x4*>(xst + row * kRow + ((sg ^ swz(row)) << 4)) = i32x4{0, 0, 0, 0};
+    }
+    __syncthreads();
+  };
   float sw = const_load(swp + c0);
   int buf = 0;
+  i32x8 x[NJ], w;
+  if constexpr (AHEAD) {
+    landed(std::integral_constant<int, LAG - 1>());
+    __syncthreads();
+    if ((c0 + 1) * kRow > n) zero_tail(c0, smem + W_BYTES);
+    w = frag(smem, wm * (TM / WM) + l16);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) x[j] = frag(smem + W_BYTES, 16 * (wt * NJ + j) + l16);
+  }
   for (int c = c0; c < c1; ++c) {
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's share of block c is there
-    __syncthreads();                     // everyone's, and block c - 1 has been read
+    // this wave's share of block c (AHEAD: of block c + 1) is there, then everyone's,
+    // and block c - 1 has been read
+    landed(std::integral_constant<int, AHEAD ? LAG - 2 : LAG - 1>());
+    __syncthreads();
+    const int after = buf == STAGES - 1 ? 0 : buf + 1;  // the next block's buffer
     const uint8_t* wst = smem + buf * STAGE;
-    uint8_t* xst = smem + buf * STAGE + W_BYTES;
-    if ((c + 1) * kRow > n) {  // the row's end: zeros in X past it
-      for (int i = threadIdx.x; i < TT * 8; i += NW * 64) {
-        const int row = i >> 3, sg = i & 7;
-        if (c * kRow + 16 * sg >= n)
-          *reinterpret_cast<i32x4*>(xst + row * kRow + ((sg ^ swz(row)) << 4)) =
-              i32x4{0, 0, 0, 0};
-      }
-      __syncthreads();
-    }
-    const int cn = min(c + 1, c1 - 1), nbuf = buf ^ 1;
+    const uint8_t* xst = smem + buf * STAGE + W_BYTES;
+    const uint8_t* wnx = smem + after * STAGE;
+    const uint8_t* xnx = smem + after * STAGE + W_BYTES;
+    const int ct = AHEAD ? c + 1 : c;
+    if (ct < c1 && (ct + 1) * kRow > n)
+      zero_tail(ct, smem + (AHEAD ? after : buf) * STAGE + W_BYTES);
+    // the block to fetch, and the buffer that block c - 1 has left
+    const int cn = min(c + LAG, c1 - 1), nbuf = buf == 0 ? STAGES - 1 : buf - 1;
+    const int c2 = min(c + 1, c1 - 1);
     float s[NJ];
     if (EXACT) {
       issue_s(cn, nbuf);
 #pragma unroll
       for (int j = 0; j < NJ; ++j) s[j] = sxl[buf * TT + 16 * (wt * NJ + j) + l16] * sw;
-      sw = const_load(swp + cn);
-      Bf32 x[NJ];
+      sw = const_load(swp + c2);
+      Bf32 xw[NJ];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) x[j] = widen(frag(xst, 16 * (wt * NJ + j) + l16));
+      for (int j = 0; j < NJ; ++j) {
+        xw[j] = widen(AHEAD ? x[j] : frag(xst, 16 * (wt * NJ + j) + l16));
+        if (AHEAD) x[j] = frag(xnx, 16 * (wt * NJ + j) + l16);
+      }
+      if (!AHEAD) w = frag(wst, wm * (TM / WM) + l16);
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
-        const Bf32 w = widen(frag(wst, wm * (TM / WM) + 16 * i + l16));
+        const Bf32 ww = widen(w);
+        if (i + 1 < MI) w = frag(wst, wm * (TM / WM) + 16 * (i + 1) + l16);
+        else if (AHEAD) w = frag(wnx, wm * (TM / WM) + l16);
 #pragma unroll
         for (int j = i * PX / MI; j < (i + 1) * PX / MI; ++j) issue_x(j, cn, nbuf);
 #pragma unroll
@@ -301,53 +345,58 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
         for (int k = 0; k < 4; ++k)
 #pragma unroll
           for (int j = 0; j < NJ; ++j)
-            d[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.k[k], x[j].k[k], d[j], 0, 0, 0);
+            d[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ww.k[k], xw[j].k[k], d[j], 0, 0, 0);
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[j][e], s[j], acc[i][j][e]);
       }
     } else {
-      i32x8 x[NJ];
-      i32x8 w = frag(wst, wm * (TM / WM) + l16);
+      if constexpr (!AHEAD) {
+        w = frag(wst, wm * (TM / WM) + l16);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) x[j] = frag(xst, 16 * (wt * NJ + j) + l16);
+        for (int j = 0; j < NJ; ++j) x[j] = frag(xst, 16 * (wt * NJ + j) + l16);
+      }
 #pragma unroll
       for (int j = 0; j < NJ; ++j) s[j] = sxl[buf * TT + 16 * (wt * NJ + j) + l16] * sw;
-      sw = const_load(swp + cn);
+      sw = const_load(swp + c2);
       __builtin_amdgcn_sched_barrier(0);
       issue_s(cn, nbuf);
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
         i32x8 wn = w;
         if (i + 1 < MI) wn = frag(wst, wm * (TM / WM) + 16 * (i + 1) + l16);
+        else if (AHEAD) wn = frag(wnx, wm * (TM / WM) + l16);
         f32x4 d[NJ];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
           d[j] = block_fast(w, x[j]);
+          if (AHEAD && i + 1 == MI) x[j] = frag(xnx, 16 * (wt * NJ + j) + l16);
           const int ip = i > 0 ? i - 1 : MI - 1;
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             acc[ip][j][e] = fmaf(dp[j][e], i > 0 ? s[j] : sp[j], acc[ip][j][e]);
-          // one DMA instruction after every second matrix instruction, X's first
-          if (j & 1) {
-            const int k = (i * NJ + j) / 2;
-            if (k < PX) issue_x(k, cn, nbuf);
-            else if (k < PX + PW) issue_w(k - PX, cn, nbuf);
-          }
+          // the DMA, X's first, after every second matrix instruction where there are
+          // enough of them
+          constexpr int P = PX + PW, SPAN = MI * NJ < 2 * P ? MI * NJ : 2 * P;
+#pragma unroll
+          for (int k = 0; k < P; ++k)
+            if ((k + 1) * SPAN / P - 1 == i * NJ + j) {
+              if (k < PX) issue_x(k, cn, nbuf);
+              else issue_w(k - PX, cn, nbuf);
+            }
           __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int j = 0; j < NJ; ++j) dp[j] = d[j];
         w = wn;
       }
-      static_assert(EXACT || PX + PW <= MI * NJ / 2, "the block has room for its DMA");
 #pragma unroll
       for (int j = 0; j < NJ; ++j) sp[j] = s[j];
     }
-    buf = nbuf;
+    buf = after;
   }
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // no DMA into this LDS outlives the workgroup
+  wait_vm<0>();  // no DMA into this LDS outlives the workgroup
   if (!EXACT) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
@@ -627,8 +676,13 @@ __global__ __launch_bounds__(256) void fp8_gemm_reduce_kernel(GemmArgs a, int ks
   store4(a, t, r, v);
 }
 
-// Decode batches go through fp8_gemv_kernel.
-constexpr int64_t kGemvTokens = 32;
+// Batches that go through fp8_gemv_kernel: 16 tokens, and 32 over weights that a
+// few microseconds read (32 x 4096 x 4096: 8 us, in narrow tiles 11.5; but
+// 32 x 11008 x 4096: 20 and 15, 32 x 8192 x 28672: 66 and 49, where the tiles'
+// deeper DMA counts).
+bool by_gemv(int64_t tokens, int64_t m, int64_t n) {
+  return tokens <= 16 || (tokens <= 32 && m * n <= int64_t(1) << 25);
+}
 
 // 32 weight rows a workgroup (the activations' codes read half as often) where
 // that still gives one to every CU
@@ -655,38 +709,45 @@ bool quantizes_itself(int64_t tokens, int64_t n) {
   return tokens <= 16 && tokens * (ceil_div(n, (int64_t)kFp8Block) * (kRow + 4) + 32) <= 32768;
 }
 
-// How a product is cut: tile, and K splits where the tiles do not fill the chip.
+// How a product is cut: tile, and K splits where the tiles do not reach every CU.
+// Measured for bf16 results (us):             256x256  256x128  128x128 (split)
+//   2048 x 8192 x 28672 (256 tiles of 256x256)    420        -        -
+//   512 x 11008 x 4096  (86 of 256x256)            46       43       50
+//   2048 x 4096 x 4096  (128)                      54       45       52
+//   1024 x 4096 x 4096  (256 of 128x128)           43       35       26
+//   512 x 4096 x 11008  (128, 2 splits)            52       42       41
+enum Tile { T256x256, T256x128, T128x128, T128x64 };
 struct Plan {
-  int tile;  // 256, 128 or 64 tokens
+  Tile tile;
   int ks;
 };
 
 Plan plan_of(int64_t tokens, int64_t m, int64_t n, bool exact) {
   const int64_t nb = ceil_div(n, (int64_t)kFp8Block);
-  Plan p;
-  const int64_t t256 = ceil_div(tokens, (int64_t)256) * ceil_div(m, (int64_t)256);
-  p.tile = !exact && t256 >= 160 ? 256 : 128;
-  p.ks = 1;
-  if (p.tile == 128) {
-    const int64_t tiles = ceil_div(tokens, (int64_t)128) * ceil_div(m, (int64_t)128);
-    p.ks = (int)hmax(1, hmin(hmin(512 / tiles, nb / 4), 16));
-  }
-  return p;
+  auto tiles = [&](int64_t tm, int64_t tt) { return ceil_div(m, tm) * ceil_div(tokens, tt); };
+  if (!exact && tiles(256, 256) >= 160) return {T256x256, 1};
+  if (tiles(128, 128) > 256) return {T256x128, 1};
+  // the narrow tile for narrow batches, and where there is little work for each CU
+  // (333 x 1000 x 4112: 16.4 -> 14.4 us, 128 x 4096 x 4096: 17.8 -> 14.9; but
+  // 128 x 8192 x 28672: 62 -> 72)
+  const Tile tile = tokens <= 64 || tiles(128, 128) * nb < 8 * 256 ? T128x64 : T128x128;
+  const int64_t t = tiles(128, tile == T128x64 ? 64 : 128);
+  return {tile, (int)hmax(1, hmin(hmin(256 / t, nb / 4), 16))};
 }
 
-template <int TM, int TT, int WM, int WT, bool EXACT, bool GATED = false>
+template <int TM, int TT, int WM, int WT, int STAGES, bool EXACT, bool GATED = false>
 void launch_tile(GemmArgs a, int ks, hipStream_t stream) {
   a.ntm = ceil_div(a.m, (int64_t)(GATED ? TM / 2 : TM));
   a.ntt = ceil_div(a.tokens, (int64_t)TT);
   const int64_t grid = ceil_div(a.ntm * a.ntt, kXcds) * kXcds;
-  hipLaunchKernelGGL((fp8_gemm_tile_kernel<TM, TT, WM, WT, EXACT, GATED>),
+  hipLaunchKernelGGL((fp8_gemm_tile_kernel<TM, TT, WM, WT, STAGES, EXACT, GATED>),
                      dim3((unsigned)grid, (unsigned)ks), dim3(WM * WT * 64), 0, stream, a);
 }
 
 }  // namespace
 
 size_t fp8_gemm_ws_bytes(int64_t tokens, int64_t m, int64_t n) {
-  if (tokens <= kGemvTokens) return 0;
+  if (by_gemv(tokens, m, n)) return 0;
   // either type of Y
   const Plan e = plan_of(tokens, m, n, true), f = plan_of(tokens, m, n, false);
   const int ks = e.ks > f.ks ? e.ks : f.ks;
@@ -711,12 +772,24 @@ static GemmArgs gemm_args(const Fp8GemmArgs& g) {
 
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, hipStream_t stream) {
   const GemmArgs a = gemm_args(g);
-  if (g.tokens <= kGemvTokens) return launch_gemv<SRC_CODES>(GemvArgs{a, nullptr, 0, 0}, 0, stream);
+  if (by_gemv(g.tokens, g.m, g.n)) return launch_gemv<SRC_CODES>(GemvArgs{a, nullptr, 0, 0}, 0, stream);
   const bool exact = !a.ybf16;
   const Plan p = plan_of(g.tokens, g.m, g.n, exact);
-  if (p.tile == 256) launch_tile<256, 256, 2, 4, false>(a, 1, stream);
-  else if (exact) launch_tile<128, 128, 2, 2, true>(a, p.ks, stream);
-  else launch_tile<128, 128, 2, 2, false>(a, p.ks, stream);
+  switch (p.tile) {
+    case T256x256: launch_tile<256, 256, 2, 4, 2, false>(a, 1, stream); break;
+    case T256x128:
+      if (exact) launch_tile<256, 128, 2, 4, 3, true>(a, 1, stream);
+      else launch_tile<256, 128, 2, 4, 3, false>(a, 1, stream);
+      break;
+    case T128x128:
+      if (exact) launch_tile<128, 128, 2, 4, 4, true>(a, p.ks, stream);
+      else launch_tile<128, 128, 2, 4, 4, false>(a, p.ks, stream);
+      break;
+    case T128x64:
+      if (exact) launch_tile<128, 64, 4, 2, 6, true>(a, p.ks, stream);
+      else launch_tile<128, 64, 4, 2, 6, false>(a, p.ks, stream);
+      break;
+  }
   if (p.ks > 1) {
     const int64_t total = g.tokens * ceil_div(g.m, (int64_t)4);
     hipLaunchKernelGGL(fp8_gemm_reduce_kernel, dim3((unsigned)ceil_div(total, (int64_t)256)), dim3(256), 0,
@@ -729,7 +802,7 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, hipStream_t stream) {
 // else the two products into the workspace (bf16 [tokens][m] each) and the
 // quantizer behind them.
 static bool gated_in_one(int64_t tokens, int64_t m) {
-  return tokens > kGemvTokens && ceil_div(tokens, (int64_t)256) * ceil_div(m, (int64_t)128) >= 128;
+  return tokens > 32 && ceil_div(tokens, (int64_t)256) * ceil_div(m, (int64_t)128) >= 128;
 }
 
 static int64_t gated_ld(int64_t m) { return (m + 7) / 8 * 8; }
@@ -749,7 +822,7 @@ hipError_t launch_fp8_gated(const Fp8GemmArgs& g, const uint8_t* W2, int64_t ldw
     a.codes = codes; a.ldc = ldc;
     a.scales = scales; a.ldso = ldso;
     a.vec4 = reinterpret_cast<uintptr_t>(codes) % 4 == 0 && ldc % 4 == 0;
-    launch_tile<256, 256, 2, 4, false, true>(a, 1, stream);
+    launch_tile<256, 256, 2, 4, 2, false, true>(a, 1, stream);
     return hipGetLastError();
   }
   const int64_t ld = gated_ld(g.m);
