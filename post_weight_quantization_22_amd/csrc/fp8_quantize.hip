@@ -43,26 +43,36 @@ struct RowsArgs {
 
 __device__ __forceinline__ float silu_times(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
-// 16 lanes per token and block, a workgroup 16 tokens of one block: the scales
-// of a block are stored for 16 tokens together.
-template <int DT, bool SWIGLU>
+// 16 lanes per token and block; a workgroup takes 16 tokens of B neighbouring
+// blocks, its loads all in flight at once: rows are read in pieces of B * 256
+// bytes, and a block's scales are stored for 16 tokens together.
+template <int DT, bool SWIGLU, int B>
 __global__ __launch_bounds__(256) void fp8_rows_kernel(RowsArgs a) {
-  const int64_t t = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-  const int64_t b = blockIdx.y;
+  const int64_t t = (int64_t)blockIdx.y * 16 + (threadIdx.x >> 4);
+  const int64_t b0 = (int64_t)blockIdx.x * B;
   if (t >= a.tokens) return;
-  const int64_t c0 = b * kFp8Block + 8 * (threadIdx.x & 15);
+  const int64_t c0 = b0 * kFp8Block + 8 * (threadIdx.x & 15);
   constexpr int esz = DT == GPTQ_BF16 ? 2 : 4;
-  Vals8 x = load_vals8<DT>(reinterpret_cast<const char*>(a.X) + t * a.ldx * esz, c0, a.n, a.vec);
-  if (SWIGLU) {
-    const Vals8 u =
-        load_vals8<DT>(reinterpret_cast<const char*>(a.X2) + t * a.ldx2 * esz, c0, a.n, a.vec);
+  const char* row = reinterpret_cast<const char*>(a.X) + t * a.ldx * esz;
+  const char* row2 = SWIGLU ? reinterpret_cast<const char*>(a.X2) + t * a.ldx2 * esz : nullptr;
+  Vals8 x[B], u[SWIGLU ? B : 1];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x.v[k] = silu_times(x.v[k], u.v[k]);
+  for (int i = 0; i < B; ++i) {
+    x[i] = load_vals8<DT>(row, c0 + i * kFp8Block, a.n, a.vec);
+    if (SWIGLU) u[i] = load_vals8<DT>(row2, c0 + i * kFp8Block, a.n, a.vec);
   }
-  const float s = e4m3_scale(lanes_max<kLanes>(amax_finite8(x)));
-  const uint2 c = e4m3_codes8(x, s, approx_recip(s));
-  store_codes8(a.codes + t * a.ldc, c0, a.n, a.vecc, c);
-  if ((threadIdx.x & 15) == 0) a.scales[b * a.lds + t] = s;
+#pragma unroll
+  for (int i = 0; i < B; ++i) {
+    if ((b0 + i) * kFp8Block >= a.n) break;
+    if (SWIGLU) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[i].v[k] = silu_times(x[i].v[k], u[i].v[k]);
+    }
+    const float s = e4m3_scale(lanes_max<kLanes>(amax_finite8(x[i])));
+    const uint2 c = e4m3_codes8(x[i], s, approx_recip(s));
+    store_codes8(a.codes + t * a.ldc, c0 + i * kFp8Block, a.n, a.vecc, c);
+    if ((threadIdx.x & 15) == 0) a.scales[(b0 + i) * a.lds + t] = s;
+  }
 }
 
 // A workgroup per 128 x 128 block: 16 rows a step, the block's values held in
@@ -119,26 +129,32 @@ hipError_t launch_fp8_rows(const void* X, int64_t ldx, const void* X2, int64_t l
   const int per16 = dt == GPTQ_BF16 ? 8 : 4;
   a.vec = aligned(X, 16) && ldx % per16 == 0 && (!X2 || (aligned(X2, 16) && ldx2 % per16 == 0));
   a.vecc = aligned(codes, 8) && ldc % 8 == 0;
-  // tokens <= 2^24 and n <= 2^24: at most 2^20 x 2^17 workgroups, blocks in y up to 65535 a launch
+  // four blocks a workgroup where that still gives each CU eight of them
   const int64_t nb = ceil_div(n, (int64_t)kFp8Block);
-  const dim3 block(256);
-  for (int64_t b0 = 0; b0 < nb; b0 += 65535) {
+  const int per = ceil_div(nb, (int64_t)4) * ceil_div(tokens, (int64_t)16) >= 2048 ? 4 : 1;
+  // 16-token rows of workgroups in y, up to 65535 a launch
+  constexpr int64_t kRows = int64_t(65535) * 16;
+  for (int64_t t0 = 0; t0 < tokens; t0 += kRows) {
     RowsArgs p = a;
-    const int64_t nbl = hmin(nb - b0, (int64_t)65535);
-    const int64_t skip = b0 * kFp8Block;
-    p.X = reinterpret_cast<const char*>(X) + skip * (dt == GPTQ_BF16 ? 2 : 4);
-    if (X2) p.X2 = reinterpret_cast<const char*>(X2) + skip * (dt == GPTQ_BF16 ? 2 : 4);
-    p.codes = codes + skip;
-    p.scales = scales + b0 * lds;
-    p.n = n - skip;
-    const dim3 grid((unsigned)ceil_div(tokens, 16), (unsigned)nbl);
+    const int64_t esz = dt == GPTQ_BF16 ? 2 : 4;
+    p.tokens = hmin(tokens - t0, kRows);
+    p.X = reinterpret_cast<const char*>(X) + t0 * ldx * esz;
+    if (X2) p.X2 = reinterpret_cast<const char*>(X2) + t0 * ldx2 * esz;
+    p.codes = codes + t0 * ldc;
+    p.scales = scales + t0;
+    const dim3 grid((unsigned)ceil_div(nb, (int64_t)per), (unsigned)ceil_div(p.tokens, (int64_t)16));
+    const dim3 block(256);
+#define GPTQ_ROWS(DT, SW)                                                                   \
+  if (per == 4) hipLaunchKernelGGL((fp8_rows_kernel<DT, SW, 4>), grid, block, 0, stream, p); \
+  else hipLaunchKernelGGL((fp8_rows_kernel<DT, SW, 1>), grid, block, 0, stream, p);
     if (X2) {
-      if (dt == GPTQ_BF16) hipLaunchKernelGGL((fp8_rows_kernel<GPTQ_BF16, true>), grid, block, 0, stream, p);
-      else hipLaunchKernelGGL((fp8_rows_kernel<GPTQ_F32, true>), grid, block, 0, stream, p);
+      if (dt == GPTQ_BF16) { GPTQ_ROWS(GPTQ_BF16, true) }
+      else { GPTQ_ROWS(GPTQ_F32, true) }
     } else {
-      if (dt == GPTQ_BF16) hipLaunchKernelGGL((fp8_rows_kernel<GPTQ_BF16, false>), grid, block, 0, stream, p);
-      else hipLaunchKernelGGL((fp8_rows_kernel<GPTQ_F32, false>), grid, block, 0, stream, p);
+      if (dt == GPTQ_BF16) { GPTQ_ROWS(GPTQ_BF16, false) }
+      else { GPTQ_ROWS(GPTQ_F32, false) }
     }
+#undef GPTQ_ROWS
   }
   return hipGetLastError();
 }
