@@ -427,9 +427,9 @@ gptq_status fp8_quantize_blocks(const void* W, gptq_dtype wdt, int64_t m, int64_
  * at 2^-13 of the largest of them (1.5e-5 relative over normal data, against the
  * 2^-8 of Y's rounding).
  * n a multiple of 16 (else GPTQ_ERR_UNSUPPORTED); X and W 16-byte aligned with
- * row strides that are multiples of 16 and below 2^24.
+ * row strides that are multiples of 16 and at most 2^24 - 128.
  * fp8_linear: Y = X W^T from 16- or 32-bit activations: fp8_quantize_rows into
- * the workspace, then the product.  X as in fp8_quantize_rows.
+ * the workspace, then the product.  X as in fp8_quantize_rows; Y apart from X.
  * fp8_gated_gemm: the codes and scales (as fp8_swiglu_quantize writes them) of
  * h = silu(X Wg^T) * (X Wu^T), both products rounded to bf16: the first half of a
  * gated MLP block without its two products in memory.
@@ -483,12 +483,15 @@ gptq_status fp8_gated_gemm(const uint8_t* X, int64_t tokens, int64_t n, int64_t 
  * and is not written.  Where a slot occurs twice the later token's row stays.
  * kv_cache_read: the rows of slots[tokens] as K and V; a negative slot gives
  * zeros, a slot may occur any number of times.  Either cache may be NULL (with
- * its rows); two caches of a call have the same pages and page_size.
+ * its rows); two caches of a call have the same pages and page_size and share no
+ * memory.  Strides of dimensions longer than 1 are not 0, but for the rows that
+ * kv_cache_write reads (one head's row for several heads).
  * A slot past the last is not accessed (write: skipped, read: zeros), and *info
  * (a device int32 that the caller has cleared, may be NULL) becomes 1.
  * Nothing but the given slots' rows is written.  tokens times the lanes of a
  * token (heads * groups * group lanes of 8 values) must stay below 2^31, else
- * GPTQ_ERR_UNSUPPORTED.  Workspace: kv_cache_write_workspace_size(tokens, kc),
+ * GPTQ_ERR_UNSUPPORTED.  Workspace (4-byte aligned):
+ * kv_cache_write_workspace_size(tokens, kc), 4 bytes for each of the cache's slots,
  * 0 for calls of at most GPTQ_KV_SMALL_TOKENS tokens.
  * ---------------------------------------------------------------------- */
 #define GPTQ_KV_SMALL_TOKENS 1024

@@ -26,6 +26,10 @@ gptq_status check_ws(void* ws, size_t ws_bytes, size_t need) {
   return GPTQ_OK;
 }
 
+// a tile's rows are addressed by a 24-bit product with the row stride, which for
+// fp8_linear's own codes is n rounded up to 128
+constexpr int64_t kFp8MaxStride = (int64_t(1) << 24) - 128;
+
 // what fp8_gemm and fp8_linear share; GPTQ_OK also where there is nothing to do
 gptq_status fp8_operands_ok(int64_t tokens, int64_t n, const void* W, int64_t m, int64_t ldw,
                             const float* wscales, int64_t ldws, const void* Y, int ydt,
@@ -37,8 +41,7 @@ gptq_status fp8_operands_ok(int64_t tokens, int64_t n, const void* W, int64_t m,
   if (!W || !wscales || !Y || ldw < n || ldw % 16 != 0 || ldy < m ||
       (reinterpret_cast<uintptr_t>(W) & 15) != 0 || ldws < ceil_div(n, int64_t(128)))
     return GPTQ_ERR_INVALID_ARG;
-  // offsets within a tile are 32-bit
-  return ldw >= (int64_t(1) << 24) ? GPTQ_ERR_UNSUPPORTED : GPTQ_OK;
+  return ldw > kFp8MaxStride ? GPTQ_ERR_UNSUPPORTED : GPTQ_OK;
 }
 
 gptq_status kv_cache_ok(const gptq_kv_cache* c, int64_t tokens) {
@@ -54,6 +57,11 @@ gptq_status kv_cache_ok(const gptq_kv_cache* c, int64_t tokens) {
       int64_t(c->heads) * (c->head_dim / 8) > (int64_t(1) << 20) ||
       c->pages > INT32_MAX / c->page_size)
     return GPTQ_ERR_UNSUPPORTED;
+  // an expanded dimension would have two places share their bytes
+  if ((c->pages > 1 && (c->page_stride == 0 || c->param_page_stride == 0)) ||
+      (c->page_size > 1 && (c->slot_stride == 0 || c->param_slot_stride == 0)) ||
+      (c->heads > 1 && (c->head_stride == 0 || c->param_head_stride == 0)))
+    return GPTQ_ERR_INVALID_ARG;
   const int a = c->format == GPTQ_KV_INT4 ? 4 : 8;
   if ((reinterpret_cast<uintptr_t>(c->codes) % a) != 0 || c->page_stride % a != 0 ||
       c->slot_stride % a != 0 || c->head_stride % a != 0)
@@ -428,7 +436,7 @@ gptq_status fp8_gemm(const uint8_t* X, int64_t tokens, int64_t n, int64_t ldx, c
   if (!X || !xs || ldx < n || ldx % 16 != 0 || (reinterpret_cast<uintptr_t>(X) & 15) != 0 ||
       ldxs < tokens || (R && ldr < m) || (R == Y && ldr != ldy))
     return GPTQ_ERR_INVALID_ARG;
-  if (ldx >= (int64_t(1) << 24)) return GPTQ_ERR_UNSUPPORTED;
+  if (ldx > kFp8MaxStride) return GPTQ_ERR_UNSUPPORTED;
   const gptq_status w = check_ws(ws, ws_bytes, fp8_gemm_ws_bytes(tokens, m, n));
   if (w != GPTQ_OK) return w;
   if ((reinterpret_cast<uintptr_t>(ws) & 15) != 0) return GPTQ_ERR_INVALID_ARG;
@@ -447,8 +455,9 @@ gptq_status fp8_linear(const void* X, gptq_dtype xdt, int64_t tokens, int64_t n,
   if (!X || ldx < n) return GPTQ_ERR_INVALID_ARG;
   const gptq_status w = check_ws(ws, ws_bytes, fp8_linear_ws_bytes(tokens, m, n));
   if (w != GPTQ_OK) return w;
-  // the codes lie at the workspace's start and are read 16 bytes at a time
-  if ((reinterpret_cast<uintptr_t>(ws) & 15) != 0) return GPTQ_ERR_INVALID_ARG;
+  // the codes lie at the workspace's start and are read 16 bytes at a time; a small
+  // batch's workgroups read X while others write Y
+  if ((reinterpret_cast<uintptr_t>(ws) & 15) != 0 || X == Y) return GPTQ_ERR_INVALID_ARG;
   Fp8GemmArgs g{nullptr, 0, tokens, n, nullptr, 0, W, ldw, m, wscales, ldws, Y, ydt, ldy,
                 nullptr, 0, nullptr};
   return hip_status(launch_fp8_linear(X, xdt, ldx, g, ws, stream));
@@ -477,7 +486,7 @@ gptq_status fp8_gated_gemm(const uint8_t* X, int64_t tokens, int64_t n, int64_t 
   if (!X || !xs || ldx < n || ldx % 16 != 0 || (reinterpret_cast<uintptr_t>(X) & 15) != 0 ||
       ldxs < tokens || !scales || ldc < m || lds < tokens)
     return GPTQ_ERR_INVALID_ARG;
-  if (ldx >= (int64_t(1) << 24)) return GPTQ_ERR_UNSUPPORTED;
+  if (ldx > kFp8MaxStride) return GPTQ_ERR_UNSUPPORTED;
   const gptq_status w = check_ws(ws, ws_bytes, fp8_gated_ws_bytes(tokens, m, n));
   if (w != GPTQ_OK) return w;
   if ((reinterpret_cast<uintptr_t>(ws) & 15) != 0) return GPTQ_ERR_INVALID_ARG;
@@ -505,6 +514,7 @@ gptq_status kv_cache_write(const void* K, int64_t k_token_stride, int64_t k_head
   const gptq_kv_cache* c = kc ? kc : vc;
   const gptq_status w = check_ws(ws, ws_bytes, kv_write_ws_bytes(tokens, c->pages * c->page_size));
   if (w != GPTQ_OK) return w;
+  if ((reinterpret_cast<uintptr_t>(ws) & 3) != 0) return GPTQ_ERR_INVALID_ARG;
   const KvRows k{const_cast<void*>(K), k_token_stride, k_head_stride};
   const KvRows v{const_cast<void*>(V), v_token_stride, v_head_stride};
   return hip_status(launch_kv_write(k, v, dt, tokens, slots, kc, vc, info, ws, stream));
@@ -516,6 +526,10 @@ gptq_status kv_cache_read(const gptq_kv_cache* kc, const gptq_kv_cache* vc, cons
                           int32_t* info, hipStream_t stream) {
   const gptq_status ok = kv_call_ok(K, V, dt, tokens, slots, kc, vc);
   if (ok != GPTQ_OK || tokens == 0) return ok;
+  // rows that are written share no place
+  if ((kc && ((tokens > 1 && k_token_stride == 0) || (kc->heads > 1 && k_head_stride == 0))) ||
+      (vc && ((tokens > 1 && v_token_stride == 0) || (vc->heads > 1 && v_head_stride == 0))))
+    return GPTQ_ERR_INVALID_ARG;
   const KvRows k{K, k_token_stride, k_head_stride}, v{V, v_token_stride, v_head_stride};
   return hip_status(launch_kv_read(kc, vc, slots, tokens, k, v, dt, info, stream));
 }

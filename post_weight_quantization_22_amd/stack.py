@@ -233,6 +233,8 @@ def forward_block_fp8(x: torch.Tensor, block: Fp8Block, out: Optional[torch.Tens
     Enqueued on ``stream`` (default: the current stream of x's device)."""
     if stream is None:
         stream = torch.cuda.current_stream(x.device)
+    if stream.device != x.device:
+        raise ValueError(f"the stream is on {stream.device}, x on {x.device}")
     if x.dtype != torch.bfloat16:
         raise TypeError(f"x: dtype {x.dtype}, expected bfloat16")
     T, d = x.shape

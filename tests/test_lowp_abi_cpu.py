@@ -182,3 +182,39 @@ def test_plane_checks():
         _lib._plane(torch.zeros(4, 8, dtype=torch.float16), "t", 4, 8, "bf", d)
     with pytest.raises(ValueError):
         _lib._plane(None, "t", 4, 8, "f", d)
+
+
+def test_calls_whose_addresses_would_not_hold():
+    """The widest row strides, outputs that share memory, workspaces off their border."""
+    so = _lib.load()
+    top = 1 << 24
+
+    def linear(n, ldw, X=FAKE, Y=FAKE + 4096, t=40, ws=FAKE, nbytes=0):
+        return so.fp8_linear(X, 1, t, n, n, FAKE, 8, ldw, FAKE, top // 128, Y, 0, 8, ws, nbytes, None)
+
+    # fp8_linear rounds n up to 128 for its own codes, whose stride must stay below 2^24
+    assert linear(top - 112, top - 112) == UNSUP and linear(top - 16, top - 16) == UNSUP
+    assert linear(top - 128, top - 112) == UNSUP
+    assert linear(top - 128, top - 128) == WS  # a stride that holds, no workspace given
+    assert linear(256, 256, Y=FAKE, nbytes=1 << 40) == BAD  # Y is X
+    for ldx, ldw in ((top - 112, 256), (256, top - 112)):
+        assert so.fp8_gemm(FAKE, 4, 256, ldx, FAKE, 4, FAKE, 8, ldw, FAKE, 2, None, 0, FAKE, 0, 8,
+                           FAKE, 1 << 40, None) == UNSUP
+
+    def write(kc, t=2000, ws=FAKE, nbytes=1 << 20):
+        return so.kv_cache_write(FAKE, 128, 64, None, 0, 0, 1, t, FAKE, ctypes.byref(kc), None, None,
+                                 ws, nbytes, None)
+
+    assert write(_cache(), ws=FAKE + 2) == BAD
+    for kw in (dict(page_stride=0), dict(slot_stride=0), dict(head_stride=0),
+               dict(param_page_stride=0), dict(param_slot_stride=0), dict(param_head_stride=0)):
+        assert write(_cache(**kw)) == BAD, kw
+
+    def read(kt=128, kh=64, vt=128, vh=64, t=4, c=_cache()):
+        return so.kv_cache_read(ctypes.byref(c), ctypes.byref(c), FAKE, t, FAKE, kt, kh, FAKE, vt, vh,
+                                1, None, None)
+
+    for kw in (dict(kt=0), dict(kh=0), dict(vt=0), dict(vh=0)):
+        assert read(**kw) == BAD, kw
+    # dimensions of length 1 may have any stride
+    assert read(t=0, c=_cache(pages=1, page_stride=0, param_page_stride=0)) == OK
