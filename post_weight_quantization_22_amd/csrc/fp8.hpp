@@ -14,32 +14,58 @@ struct Vals8 {
   float v[8];
 };
 
-// Values c0 .. c0 + 7 of a row (bf16 or fp32) as fp32, 0 past n.  `vec`: the
-// row's address and c0 allow 16-byte loads (uniform over the grid).
+// Values c0 .. c0 + 7 of a row (bf16 or fp32) as they lie in memory, 0 past n.
+// `vec`: the row's address and c0 allow 16-byte loads (uniform over the grid).  Kept
+// apart from their conversion: converted inside the branch below, each load would be
+// waited for there, and several could not be in flight.
 template <int DT>
-__device__ __forceinline__ Vals8 load_vals8(const void* row, int64_t c0, int64_t n, bool vec) {
-  Vals8 o;
+struct Raw8 {
+  uint32_t w[DT == GPTQ_BF16 ? 4 : 8];
+};
+
+template <int DT>
+__device__ __forceinline__ Raw8<DT> load_raw8(const void* row, int64_t c0, int64_t n, bool vec) {
+  Raw8<DT> o;
+  const char* p = reinterpret_cast<const char*>(row) + c0 * (DT == GPTQ_BF16 ? 2 : 4);
   if (vec && c0 + 8 <= n) {
-    if (DT == GPTQ_BF16) {
-      const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(row) + c0);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        o.v[2 * k] = __uint_as_float(w[k] << 16);
-        o.v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-      }
-    } else {
-      const float* p = reinterpret_cast<const float*>(row) + c0;
-      const float4 a = *reinterpret_cast<const float4*>(p);
-      const float4 b = *reinterpret_cast<const float4*>(p + 4);
-      o.v[0] = a.x; o.v[1] = a.y; o.v[2] = a.z; o.v[3] = a.w;
-      o.v[4] = b.x; o.v[5] = b.y; o.v[6] = b.z; o.v[7] = b.w;
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    o.w[0] = a.x; o.w[1] = a.y; o.w[2] = a.z; o.w[3] = a.w;
+    if constexpr (DT != GPTQ_BF16) {
+      const uint4 b = *reinterpret_cast<const uint4*>(p + 16);
+      o.w[4] = b.x; o.w[5] = b.y; o.w[6] = b.z; o.w[7] = b.w;
     }
     return o;
   }
+  if constexpr (DT == GPTQ_BF16) {
+    const uint16_t* e = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) o.v[k] = c0 + k < n ? load_elem(row, DT, c0 + k) : 0.0f;
+    for (int k = 0; k < 4; ++k) {
+      o.w[k] = c0 + 2 * k < n ? e[2 * k] : 0;
+      if (c0 + 2 * k + 1 < n) o.w[k] |= (uint32_t)e[2 * k + 1] << 16;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o.w[k] = c0 + k < n ? reinterpret_cast<const uint32_t*>(p)[k] : 0;
+  }
   return o;
+}
+
+template <int DT>
+__device__ __forceinline__ Vals8 vals_of(const Raw8<DT>& r) {
+  Vals8 o;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if constexpr (DT == GPTQ_BF16)
+      o.v[k] = __uint_as_float(k % 2 ? r.w[k / 2] & 0xFFFF0000u : r.w[k / 2] << 16);
+    else
+      o.v[k] = __uint_as_float(r.w[k]);
+  }
+  return o;
+}
+
+template <int DT>
+__device__ __forceinline__ Vals8 load_vals8(const void* row, int64_t c0, int64_t n, bool vec) {
+  return vals_of(load_raw8<DT>(row, c0, n, vec));
 }
 
 // The largest finite magnitude of 8 values.
@@ -62,57 +88,70 @@ __device__ __forceinline__ float e4m3_scale(float amax) {
   return amax == 0.0f ? 1.0f : fmaxf(__fdiv_rn(amax, kE4m3Max), 0x1p-126f);
 }
 
-// The e4m3 code nearest to the real quotient x / s, ties to even, where its two
-// candidates lo and hi = lo + 1 (magnitudes) are known: the sign of
-// |x| - h s with h the border between them, which one fma gives exactly (small
-// scales are lifted first, so that no partial result is below the subnormals).
-__device__ __forceinline__ uint32_t e4m3_decide(float x, float s, uint32_t lo, uint32_t hi) {
-  float a = fabsf(x);
-  if (s < 0x1p-60f) {
-    a *= 0x1p64f;
-    s *= 0x1p64f;
-  }
-  const float vl = __builtin_amdgcn_cvt_f32_fp8((int)lo, 0), vh = __builtin_amdgcn_cvt_f32_fp8((int)hi, 0);
-  const float h = 0.5f * (vl + vh);  // exact: 5 significant bits
-  const float r = fmaf(-h, s, a);
-  return r > 0.0f ? hi : r < 0.0f ? lo : ((lo & 1) ? hi : lo);
-}
-
 // 1 / s to within 2^-23 of itself, for a normal s and 1 / s
 __device__ __forceinline__ float approx_recip(float s) { return __builtin_amdgcn_rcpf(s); }
 
-// 8 codes of x / s, rs = approx_recip(s).  x * rs is within 2^-22 |x / s| of the
-// quotient, so the hardware's rounding of that product lowered and raised by 2^-21 brackets the
-// code; where the two differ (a border of the format is that close: about one
-// value in 10^5) e4m3_decide takes the real quotient.  A non-finite value
-// becomes the NaN code (the instruction's own result for it).
-__device__ __forceinline__ uint2 e4m3_codes8(const Vals8& x, float s, float rs) {
-  uint32_t lo[2], hi[2];
+// |x| / s so that the instruction's rounding of it (to nearest, ties to even)
+// is the rounding of the real quotient: q = q0 + (x - q0 s) rs is a neighbour of the
+// quotient, r = x - q s, which one fma gives exactly, says on which side; where it is
+// not 0 the last bit is set on that side of q, whose neighbours on a border of the
+// format end in 0.
+__device__ __forceinline__ float sticky_quotient(float x, float s, float rs) {
+  x = fabsf(x);
+  const float q0 = x * rs, q = fmaf(fmaf(-q0, s, x), rs, q0), r = fmaf(-q, s, x);
+  const uint32_t u = __float_as_uint(q) + (uint32_t)(__float_as_int(r) >> 31);
+  return __uint_as_float(r != 0.0f ? u | 1u : u);
+}
+
+// 8 codes of x / s, rs = approx_recip(s).  A non-finite value becomes the NaN code
+// (the instruction's own result for it).
+// Of fp32 values about one in 10^5 lies near a border of the format: x * rs is within
+// 2^-22 |x / s| of the quotient, the hardware's rounding of that product lowered and
+// raised by 2^-21 brackets the code, and only where the two differ the sticky quotient
+// is worked out.  Of bf16 values one in a few hundred lies on a border (a scale
+// amax / 448 of 8 significant bits), one or more in nearly every wave: BF16 works it
+// out at once.
+template <bool BF16>
+__device__ __forceinline__ uint2 e4m3_codes8(Vals8 x, float s, float rs) {
+  uint32_t c[2];
+  bool near = BF16;
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
     float q[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) q[k] = x.v[4 * p + k] * rs;
     int a = 0, b = 0;
-    a = __builtin_amdgcn_cvt_pk_fp8_f32(q[0] * 0.99999952f, q[1] * 0.99999952f, a, false);
-    a = __builtin_amdgcn_cvt_pk_fp8_f32(q[2] * 0.99999952f, q[3] * 0.99999952f, a, true);
-    b = __builtin_amdgcn_cvt_pk_fp8_f32(q[0] * 1.00000048f, q[1] * 1.00000048f, b, false);
-    b = __builtin_amdgcn_cvt_pk_fp8_f32(q[2] * 1.00000048f, q[3] * 1.00000048f, b, true);
-    lo[p] = (uint32_t)a;
-    hi[p] = (uint32_t)b;
+    if (!BF16) {
+      a = __builtin_amdgcn_cvt_pk_fp8_f32(q[0] * 0.99999952f, q[1] * 0.99999952f, a, false);
+      a = __builtin_amdgcn_cvt_pk_fp8_f32(q[2] * 0.99999952f, q[3] * 0.99999952f, a, true);
+      b = __builtin_amdgcn_cvt_pk_fp8_f32(q[0] * 1.00000048f, q[1] * 1.00000048f, b, false);
+      b = __builtin_amdgcn_cvt_pk_fp8_f32(q[2] * 1.00000048f, q[3] * 1.00000048f, b, true);
+      near |= a != b;
+    }
+    c[p] = (uint32_t)a;
   }
-  if (lo[0] != hi[0] || lo[1] != hi[1]) {
+  if (near) {
+    if (s < 0x1p-60f) {  // lifted, so that no remainder is below the subnormals
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int sh = 8 * (k & 3);
-      const uint32_t cl = (lo[k >> 2] >> sh) & 0x7F, ch = (hi[k >> 2] >> sh) & 0x7F;
-      if (cl != ch && is_finite(x.v[k])) {
-        const uint32_t c = e4m3_decide(x.v[k], s, cl, ch);
-        lo[k >> 2] = (lo[k >> 2] & ~(0x7Fu << sh)) | (c << sh);
+      for (int k = 0; k < 8; ++k) x.v[k] *= 0x1p64f;
+      s *= 0x1p64f;
+      rs *= 0x1p-64f;
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      float q[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        q[k] = sticky_quotient(x.v[4 * p + k], s, rs);
+        if (BF16) q[k] = copysignf(q[k], x.v[4 * p + k]);
       }
+      int a = 0;
+      a = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], a, false);
+      a = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], a, true);
+      c[p] = BF16 ? (uint32_t)a : (c[p] & 0x80808080u) | ((uint32_t)a & 0x7F7F7F7Fu);
     }
   }
-  return make_uint2(lo[0], lo[1]);
+  return make_uint2(c[0], c[1]);
 }
 
 }  // namespace gptq

@@ -438,7 +438,7 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
         if (q == 0) a.scales[row0 / kFp8Block * a.ldso + t] = sc;
 #pragma unroll
         for (int i = 0; i < MI / 2; ++i) {
-          const uint2 cc = e4m3_codes8(h[i], sc, rs);
+          const uint2 cc = e4m3_codes8<false>(h[i], sc, rs);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const uint32_t four = k ? cc.y : cc.x;
@@ -559,13 +559,15 @@ __global__ __launch_bounds__(kGemvWaves * 64) void fp8_gemv_kernel(GemvArgs v) {
   if (SRC != SRC_CODES) {
     constexpr int DT = SRC == GPTQ_BF16 ? GPTQ_BF16 : GPTQ_F32;
     constexpr int esz = DT == GPTQ_BF16 ? 2 : 4;
-    for (int u = threadIdx.x >> 4; u < T * nb; u += kGemvWaves * 4) {
-      const int t = u / nb, b = u - t * nb, c0 = b * kRow + 8 * l16;
-      const Vals8 x =
-          load_vals8<DT>(reinterpret_cast<const char*>(v.src) + t * v.ldsrc * esz, c0, n, v.vec);
-      const float s = e4m3_scale(lanes_max<16>(amax_finite8(x)));
-      *reinterpret_cast<uint2*>(dyn + t * xrow + c0) = e4m3_codes8(x, s, approx_recip(s));
-      if (l16 == 0) xs[t * nb + b] = s;
+    for (int t = 0; t < T; ++t) {
+      const char* row = reinterpret_cast<const char*>(v.src) + t * v.ldsrc * esz;
+      for (int b = threadIdx.x >> 4; b < nb; b += kGemvWaves * 4) {  // 16 lanes a block
+        const Vals8 x = load_vals8<DT>(row, b * kRow + 8 * l16, n, v.vec);
+        const float s = e4m3_scale(lanes_max<16>(amax_finite8(x)));
+        *reinterpret_cast<uint2*>(dyn + t * xrow + b * kRow + 8 * l16) =
+            e4m3_codes8<DT == GPTQ_BF16>(x, s, approx_recip(s));
+        if (l16 == 0) xs[t * nb + b] = s;
+      }
     }
     __syncthreads();
   }
@@ -684,12 +686,14 @@ bool by_gemv(int64_t tokens, int64_t m, int64_t n) {
   return tokens <= 16 || (tokens <= 32 && m * n <= int64_t(1) << 25);
 }
 
-// 32 weight rows a workgroup (the activations' codes read half as often) where
-// that still gives one to every CU
+// 32 weight rows a workgroup (the activations are read, or quantized, half as often)
+// where that still gives one to every CU and there are more than 2 tokens (us, 16 and
+// 32 rows: 8 x 28672 x 8192 64 and 60, 16 x 8192 x 28672 73 and 54; but
+// 1 x 28672 x 8192 57 and 59, quantizing itself 48 and 53)
 template <int SRC>
 hipError_t launch_gemv(const GemvArgs& v, size_t lds, hipStream_t stream) {
   constexpr bool codes = SRC == SRC_CODES;  // only these come with more than 16 tokens
-  const int nt = codes && v.g.tokens > 16 ? 2 : 1, rt = v.g.m >= 8192 ? 2 : 1;
+  const int nt = codes && v.g.tokens > 16 ? 2 : 1, rt = v.g.m >= 8192 && v.g.tokens > 2 ? 2 : 1;
   lds = lds > (size_t)kGemvWaves * rt * nt * 1024 ? lds : (size_t)kGemvWaves * rt * nt * 1024;
   const dim3 grid((unsigned)ceil_div(v.g.m, (int64_t)16 * rt)), block(kGemvWaves * 64);
   if (nt == 1 && rt == 1)
@@ -703,10 +707,12 @@ hipError_t launch_gemv(const GemvArgs& v, size_t lds, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Few enough activations that every workgroup quantizes them itself (and their
-// codes fit its LDS): no kernel before the product.
+// Few enough activations that every workgroup quantizes them itself, in at most 4
+// rounds of 32 blocks: no kernel before the product, whose launch costs about 2 us
+// (us, in one and in two kernels: 1 x 4096 x 4096 7.3 and 9.0, 4 x 4096 x 4096 9.7 and
+// 9.5, 7 x 4096 x 4096 12.0 and 9.9, 1 x 28672 x 8192 48 and 62).
 bool quantizes_itself(int64_t tokens, int64_t n) {
-  return tokens <= 16 && tokens * (ceil_div(n, (int64_t)kFp8Block) * (kRow + 4) + 32) <= 32768;
+  return tokens <= 16 && tokens * ceil_div(n, (int64_t)kFp8Block) <= 128;
 }
 
 // How a product is cut: tile, and K splits where the tiles do not reach every CU.
@@ -798,11 +804,14 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// The gated product in one kernel where its 256 x 256 tiles reach half of the CUs;
-// else the two products into the workspace (bf16 [tokens][m] each) and the
-// quantizer behind them.
+// The gated product in one kernel where more than one row of its 256 x 256 tiles is
+// needed and they reach half of the CUs; else the two products into the workspace
+// (bf16 [tokens][m] each) and the quantizer behind them.  In one and in three (us):
+// 512 x 11008 x 4096 71 and 112, 300 x 11008 x 4096 78 and 105, 512 x 8192 x 4096 (128
+// tiles) 60 and 62; but 512 x 4096 x 4096 (64) 57 and 51, 256 x 11008 x 4096 70 and
+// 61, 64 x 28672 x 8192 160 and 118.
 static bool gated_in_one(int64_t tokens, int64_t m) {
-  return tokens > 32 && ceil_div(tokens, (int64_t)256) * ceil_div(m, (int64_t)128) >= 128;
+  return tokens > 256 && ceil_div(tokens, (int64_t)256) * ceil_div(m, (int64_t)128) >= 128;
 }
 
 static int64_t gated_ld(int64_t m) { return (m + 7) / 8 * 8; }

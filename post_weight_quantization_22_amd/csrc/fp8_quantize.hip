@@ -55,21 +55,23 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(RowsArgs a) {
   constexpr int esz = DT == GPTQ_BF16 ? 2 : 4;
   const char* row = reinterpret_cast<const char*>(a.X) + t * a.ldx * esz;
   const char* row2 = SWIGLU ? reinterpret_cast<const char*>(a.X2) + t * a.ldx2 * esz : nullptr;
-  Vals8 x[B], u[SWIGLU ? B : 1];
+  Raw8<DT> xr[B], ur[SWIGLU ? B : 1];
 #pragma unroll
   for (int i = 0; i < B; ++i) {
-    x[i] = load_vals8<DT>(row, c0 + i * kFp8Block, a.n, a.vec);
-    if (SWIGLU) u[i] = load_vals8<DT>(row2, c0 + i * kFp8Block, a.n, a.vec);
+    xr[i] = load_raw8<DT>(row, c0 + i * kFp8Block, a.n, a.vec);
+    if (SWIGLU) ur[i] = load_raw8<DT>(row2, c0 + i * kFp8Block, a.n, a.vec);
   }
 #pragma unroll
   for (int i = 0; i < B; ++i) {
     if ((b0 + i) * kFp8Block >= a.n) break;
+    Vals8 x = vals_of(xr[i]);
     if (SWIGLU) {
+      const Vals8 u = vals_of(ur[i]);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[i].v[k] = silu_times(x[i].v[k], u[i].v[k]);
+      for (int k = 0; k < 8; ++k) x.v[k] = silu_times(x.v[k], u.v[k]);
     }
-    const float s = e4m3_scale(lanes_max<kLanes>(amax_finite8(x[i])));
-    const uint2 c = e4m3_codes8(x[i], s, approx_recip(s));
+    const float s = e4m3_scale(lanes_max<kLanes>(amax_finite8(x)));
+    const uint2 c = e4m3_codes8<DT == GPTQ_BF16 && !SWIGLU>(x, s, approx_recip(s));
     store_codes8(a.codes + t * a.ldc, c0 + i * kFp8Block, a.n, a.vecc, c);
     if ((threadIdx.x & 15) == 0) a.scales[(b0 + i) * a.lds + t] = s;
   }
@@ -87,20 +89,21 @@ __global__ __launch_bounds__(256) void fp8_blocks_kernel(const void* __restrict_
   const int64_t r0 = (int64_t)blockIdx.y * kFp8Block + (threadIdx.x >> 4);
   const int64_t c0 = (int64_t)blockIdx.x * kFp8Block + 8 * (threadIdx.x & 15);
   constexpr int esz = DT == GPTQ_BF16 ? 2 : 4;
-  Vals8 x[8];
+  Raw8<DT> x[8];
   float am = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = r0 + 16 * i;
-    if (r < m) {
-      x[i] = load_vals8<DT>(reinterpret_cast<const char*>(W) + r * ldw * esz, c0, n, vec);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[i].v[k] = 0.0f;
-    }
+  for (int i = 0; i < 8; ++i) {  // rows past the end: the last one again, the same maximum
+    const int64_t r = min(r0 + 16 * i, m - 1);
+    x[i] = load_raw8<DT>(reinterpret_cast<const char*>(W) + r * ldw * esz, c0, n, vec);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) am = fmaxf(am, amax_finite8(x[i]));
+  for (int i = 0; i < 8; ++i) am = fmaxf(am, amax_finite8(vals_of(x[i])));
+  // (the packed values are kept and widened again below: kept wide they would take
+  // twice the registers)
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (uint32_t& w : x[i].w) asm("" : "+v"(w));
   am = lanes_max<kWave>(am);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = am;
   __syncthreads();
@@ -109,7 +112,7 @@ __global__ __launch_bounds__(256) void fp8_blocks_kernel(const void* __restrict_
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t r = r0 + 16 * i;
-    if (r < m) store_codes8(codes + r * ldc, c0, n, vecc, e4m3_codes8(x[i], s, rs));
+    if (r < m) store_codes8(codes + r * ldc, c0, n, vecc, e4m3_codes8<DT == GPTQ_BF16>(vals_of(x[i]), s, rs));
   }
   if (threadIdx.x == 0) scales[blockIdx.y * lds + blockIdx.x] = s;
 }
@@ -129,9 +132,10 @@ hipError_t launch_fp8_rows(const void* X, int64_t ldx, const void* X2, int64_t l
   const int per16 = dt == GPTQ_BF16 ? 8 : 4;
   a.vec = aligned(X, 16) && ldx % per16 == 0 && (!X2 || (aligned(X2, 16) && ldx2 % per16 == 0));
   a.vecc = aligned(codes, 8) && ldc % 8 == 0;
-  // four blocks a workgroup where that still gives each CU eight of them
+  // two blocks a workgroup where that still gives each CU eight of them (us, one / two
+  // / four blocks: 512 x 8192 5.6 / 5.7, 1024 x 8192 8.6 / 8.4, 2048 x 28672 44 / 36 / 38)
   const int64_t nb = ceil_div(n, (int64_t)kFp8Block);
-  const int per = ceil_div(nb, (int64_t)4) * ceil_div(tokens, (int64_t)16) >= 2048 ? 4 : 1;
+  const int per = ceil_div(nb, (int64_t)2) * ceil_div(tokens, (int64_t)16) >= 2048 ? 2 : 1;
   // 16-token rows of workgroups in y, up to 65535 a launch
   constexpr int64_t kRows = int64_t(65535) * 16;
   for (int64_t t0 = 0; t0 < tokens; t0 += kRows) {
@@ -145,7 +149,7 @@ hipError_t launch_fp8_rows(const void* X, int64_t ldx, const void* X2, int64_t l
     const dim3 grid((unsigned)ceil_div(nb, (int64_t)per), (unsigned)ceil_div(p.tokens, (int64_t)16));
     const dim3 block(256);
 #define GPTQ_ROWS(DT, SW)                                                                   \
-  if (per == 4) hipLaunchKernelGGL((fp8_rows_kernel<DT, SW, 4>), grid, block, 0, stream, p); \
+  if (per == 2) hipLaunchKernelGGL((fp8_rows_kernel<DT, SW, 2>), grid, block, 0, stream, p); \
   else hipLaunchKernelGGL((fp8_rows_kernel<DT, SW, 1>), grid, block, 0, stream, p);
     if (X2) {
       if (dt == GPTQ_BF16) { GPTQ_ROWS(GPTQ_BF16, true) }

@@ -188,15 +188,12 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvArgs a) {
   const Unit un = unit_of<V>(s, t0, rest, 0);
   bool live = un.t < a.tokens;
   const int64_t slot = live ? a.slots[un.t] : -1;
-  Vals8 x[V];
+  Raw8<DT> xr[V] = {};
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[v].v[e] = 0.0f;
+  for (int v = 0; v < V; ++v)
     if (live && un.c0 + 8 * v < s.dim)
-      x[v] = load_vals8<DT>(s.rows + (un.t * s.tstride + un.h * s.hstride) * esz, un.c0 + 8 * v,
+      xr[v] = load_raw8<DT>(s.rows + (un.t * s.tstride + un.h * s.hstride) * esz, un.c0 + 8 * v,
                             s.dim, s.vec);
-  }
   if (a.owner == nullptr)
     find_stale(a, t0, small_div(rest + kThreads - 1, s.per_token) + 1, sl, stale);
   if (slot >= a.nslots) {
@@ -205,6 +202,9 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvArgs a) {
   }
   if (slot < 0) live = false;
   if (live) live = a.owner ? a.owner[slot] == (int32_t)un.t : stale[un.t - t0] == 0;
+  Vals8 x[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) x[v] = vals_of(xr[v]);
   float scale, zero = 0.0f;
   uint2 code[V];
   if (s.fmt == GPTQ_KV_E4M3) {
@@ -213,7 +213,7 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvArgs a) {
     scale = e4m3_scale(lanes_max<LPG>(am));
     const float rs = approx_recip(scale);
 #pragma unroll
-    for (int v = 0; v < V; ++v) code[v] = e4m3_codes8(x[v], scale, rs);
+    for (int v = 0; v < V; ++v) code[v] = e4m3_codes8<DT == GPTQ_BF16>(x[v], scale, rs);
   } else {
     const float maxq = s.fmt == GPTQ_KV_INT4 ? 15.0f : 255.0f;
     float lo = 0.0f, hi = 0.0f;

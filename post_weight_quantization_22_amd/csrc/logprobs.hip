@@ -245,11 +245,11 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LpArgs a) {
 
   float m = kNegInf, mr = 0.0f, r = 0.0f, t = 0.0f;  // mr: m, or 0 before the first finite logit
   uint32_t at = 8 * tid;
-  Vals8 next;
-  if (8 * tid < n) next = load_vals8<DT>(x, 8 * tid, n, a.vec);
+  Raw8<DT> next;
+  if (8 * tid < n) next = load_raw8<DT>(x, 8 * tid, n, a.vec);
   for (int64_t c = 8 * tid; c < n; c += 8 * kThreads) {
-    Vals8 v = next;
-    if (c + 8 * kThreads < n) next = load_vals8<DT>(x, c + 8 * kThreads, n, a.vec);
+    Vals8 v = vals_of(next);
+    if (c + 8 * kThreads < n) next = load_raw8<DT>(x, c + 8 * kThreads, n, a.vec);
     if (c + 8 > n) {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
