@@ -68,6 +68,16 @@ __device__ __forceinline__ Vals8 load_vals8(const void* row, int64_t c0, int64_t
   return vals_of(load_raw8<DT>(row, c0, n, vec));
 }
 
+// Stores that do not stay in the caches (8- and 16-byte aligned).
+__device__ __forceinline__ void stream_store(void* p, uint2 v) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  __builtin_nontemporal_store(u32x2{v.x, v.y}, reinterpret_cast<u32x2*>(p));
+}
+__device__ __forceinline__ void stream_store(void* p, uint4 v) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4*>(p));
+}
+
 // The largest finite magnitude of 8 values.
 __device__ __forceinline__ float amax_finite8(const Vals8& x) {
   float a = 0.0f;

@@ -246,11 +246,11 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvArgs a) {
   const Place p = place_of(a, s, slot);
   uint8_t* row = s.codes + p.code + un.h * s.chead;
   if (s.fmt == GPTQ_KV_INT4) {
-    if (V == 2) *reinterpret_cast<uint2*>(row + un.c0 / 2) = make_uint2(code[0].x, code[V - 1].x);
+    if (V == 2) stream_store(row + un.c0 / 2, make_uint2(code[0].x, code[V - 1].x));
     else *reinterpret_cast<uint32_t*>(row + un.c0 / 2) = code[0].x;
   } else {
 #pragma unroll
-    for (int v = 0; v < V; ++v) *reinterpret_cast<uint2*>(row + un.c0 + 8 * v) = code[v];
+    for (int v = 0; v < V; ++v) stream_store(row + un.c0 + 8 * v, code[v]);
   }
   if (un.l == 0) {
     const int64_t i = p.param + un.h * s.phead + un.g;
@@ -286,7 +286,7 @@ __device__ __forceinline__ void store_vals8(char* row, int c0, bool vec, const f
              (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[2 * k + 1]) << 16;
     uint16_t* p = reinterpret_cast<uint16_t*>(row) + c0;
     if (vec) {
-      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+      stream_store(p, make_uint4(w[0], w[1], w[2], w[3]));
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) p[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
@@ -294,8 +294,11 @@ __device__ __forceinline__ void store_vals8(char* row, int c0, bool vec, const f
   } else {
     float* p = reinterpret_cast<float*>(row) + c0;
     if (vec) {
-      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+      uint32_t w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(v[k]);
+      stream_store(p, make_uint4(w[0], w[1], w[2], w[3]));
+      stream_store(p + 4, make_uint4(w[4], w[5], w[6], w[7]));
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) p[k] = v[k];
