@@ -10,7 +10,10 @@
 //
 // Both directions are bound by HBM (2 + 1 or 2 + 1/2 bytes a value).  A lane
 // owns 8 consecutive values of a row, a group spans LPG lanes of a wave and its
-// range is a butterfly over them.
+// range is a butterfly over them.  Keys and values of 8 heads of 128: 131072 tokens read
+// from e4m3 in 156 us (5.2 TB/s), 8192 tokens written in 4 bits in 15 us (2.8 TB/s: the
+// index arithmetic and the codes' rounding fill the issue slots), 5 tokens in 5 us (the
+// launch and three dependent round trips: slots, rows, codes).
 #include "fp8.hpp"
 
 namespace gptq {
@@ -436,7 +439,9 @@ KvArgs args_of(const gptq_kv_cache* kc, const gptq_kv_cache* vc, const int64_t* 
   return a;
 }
 
-// four units a lane where that still gives every CU four workgroups
+// four units a lane where that still gives every CU four workgroups (8 heads of 128, us,
+// one and four units: 4096 tokens 7.7 and 8.5, 8192 tokens 12.0 and 11.3, 131072 tokens
+// 204 and 168)
 int units_a_lane(int64_t units) { return units >= int64_t(1) << 20 ? 4 : 1; }
 
 }  // namespace
