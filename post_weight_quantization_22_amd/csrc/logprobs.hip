@@ -201,7 +201,7 @@ struct LpArgs {
   int32_t* top_ids;
   float* top_logprobs;
   int64_t seg;  // logits of a segment, a multiple of 2048 (or the whole row)
-  int nseg, vec;
+  int nseg;
   Part* parts;      // [tokens][nseg], segments only
   uint64_t* keys;   // [tokens][nseg][top], segments only
 };
@@ -234,7 +234,31 @@ __device__ __forceinline__ void write_row(const LpArgs& a, int64_t row, const Pa
   }
 }
 
-// A workgroup per row and segment.
+// Logits col .. col + 7 of n (col may lie up to 7 in front), 16-byte aligned where all
+// of them are inside; 0 outside.
+template <int DT>
+__device__ __forceinline__ Raw8<DT> load_chunk(const char* x, int64_t col, int64_t n) {
+  Raw8<DT> o;
+  if (col >= 0 && col + 8 <= n) return load_raw8<DT>(x, col, n, true);
+  if constexpr (DT == GPTQ_BF16) {
+    const uint16_t* e = reinterpret_cast<const uint16_t*>(x);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t i = col + 2 * k;
+      o.w[k] = i >= 0 && i < n ? e[i] : 0;
+      if (i + 1 >= 0 && i + 1 < n) o.w[k] |= (uint32_t)e[i + 1] << 16;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      o.w[k] = col + k >= 0 && col + k < n ? reinterpret_cast<const uint32_t*>(x)[col + k] : 0;
+  }
+  return o;
+}
+
+// A workgroup per row and segment.  Its chunks of 8 logits lie on 16-byte borders, the
+// first one beginning `off` places in front of the row (2048 x 50257 bf16, rows that start
+// on any border: 68 us; by loads of single logits 157).
 template <int DT>
 __global__ __launch_bounds__(kThreads) void logprobs_kernel(LpArgs a) {
   __shared__ Shared sh;
@@ -245,17 +269,21 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LpArgs a) {
   constexpr int esz = DT == GPTQ_BF16 ? 2 : 4;
   const char* x = reinterpret_cast<const char*>(a.X) + (row * a.ldx + c0) * esz;
 
+  const int off = (int)(reinterpret_cast<uintptr_t>(x) / esz % (16 / esz));
+  const int64_t end = n + off;  // chunks are counted from 8 c - off on
+
   float m = kNegInf, mr = 0.0f, r = 0.0f, t = 0.0f;  // mr: m, or 0 before the first finite logit
-  uint32_t at = 8 * tid;
+  uint32_t at = max(8 * tid - off, 0);
   Raw8<DT> next;
-  if (8 * tid < n) next = load_raw8<DT>(x, 8 * tid, n, a.vec);
-  for (int64_t c = 8 * tid; c < n; c += 8 * kThreads) {
+  if (8 * tid < end) next = load_chunk<DT>(x, 8 * tid - off, n);
+  for (int64_t p = 8 * tid; p < end; p += 8 * kThreads) {
+    const int64_t c = p - off;
     Vals8 v = vals_of(next);
-    if (c + 8 * kThreads < n) next = load_raw8<DT>(x, c + 8 * kThreads, n, a.vec);
-    if (c + 8 > n) {
+    if (p + 8 * kThreads < end) next = load_chunk<DT>(x, c + 8 * kThreads, n);
+    if (c < 0 || c + 8 > n) {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (c + k >= n) v.v[k] = kNegInf;
+        if (c + k < 0 || c + k >= n) v.v[k] = kNegInf;
     }
     float cm = v.v[0];
 #pragma unroll
@@ -289,23 +317,24 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LpArgs a) {
   if ((tid & 63) == 0) sh.part[tid >> 6] = p;
 
   if (a.top > 0) {
-    const uint64_t mine = 8 * tid < n ? key_of(m, at) : 0;
+    const uint64_t mine = 8 * tid < end ? key_of(m, at) : 0;
     best_of_lanes(sh, mine);
     const uint64_t kth = sh.best[a.top - 1];
     if (tid == 0) sh.count = 0;
     __syncthreads();
     // the chunks of the lanes that hold candidates, dealt to all lanes: a key's
     // index says which lane it came from
-    const int chunks = (int)((n + 8 * kThreads - 1) / (8 * kThreads));
+    const int chunks = (int)((end + 8 * kThreads - 1) / (8 * kThreads));
     for (int u = tid; u < chunks * a.top; u += kThreads) {
       const uint64_t of = sh.best[u % a.top];
-      const int64_t c = 8 * (((key_index(of) >> 3) & (kThreads - 1)) + (int64_t)(u / a.top) * kThreads);
+      const uint32_t lane = ((key_index(of) + off) >> 3) & (kThreads - 1);
+      const int64_t c = 8 * (lane + (int64_t)(u / a.top) * kThreads) - off;
       if (of == 0 || c >= n) continue;
-      const Vals8 v = load_vals8<DT>(x, c, n, a.vec);
+      const Vals8 v = vals_of(load_chunk<DT>(x, c, n));
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const uint64_t key = key_of(v.v[k], (uint32_t)c + k);
-        if (c + k < n && key >= kth) {
+        if (c + k >= 0 && c + k < n && key >= kth) {
           const int i = atomicAdd(&sh.count, 1);
           if (i < kList) sh.list[i] = key;
         }
@@ -322,12 +351,12 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LpArgs a) {
       uint64_t last = ~0ull;
       for (int i = 0; i < a.top; ++i) {
         uint64_t b = 0;
-        for (int64_t c = 8 * tid; c < n; c += 8 * kThreads) {
-          const Vals8 v = load_vals8<DT>(x, c, n, a.vec);
+        for (int64_t c = 8 * tid - off; c < n; c += 8 * kThreads) {
+          const Vals8 v = vals_of(load_chunk<DT>(x, c, n));
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const uint64_t key = key_of(v.v[k], (uint32_t)c + k);
-            if (c + k < n && key < last) b = umax(b, key);
+            if (c + k >= 0 && c + k < n && key < last) b = umax(b, key);
           }
         }
         b = sort64(b);
@@ -384,11 +413,12 @@ __global__ __launch_bounds__(kThreads) void logprobs_join_kernel(LpArgs a, int d
   write_row(a, row, sh.part[0], sh.best, dt);
 }
 
-// Segments of a row: none from 256 rows on, else as many as give 512 workgroups; at
-// least 2048 logits each, at most 64 of them (us, whole rows and segments:
-// 4 x 128000 40 and 12.6, 128 x 32000 17 and 14.7; twice as many segments: the same).
+// Segments of a row: none from 256 rows on and for short rows, else as many as give 512
+// workgroups; at least 2048 logits each, at most 64 of them (us, whole rows and
+// segments: 1 x 16384 9.5 and 10.8, 1 x 24576 11.4 and 10.8, 4 x 128000 35 and 12.4,
+// 200 x 128000 37 and 29; twice as many segments: the same).
 int segments(int64_t tokens, int64_t vocab) {
-  if (tokens >= 256) return 1;
+  if (tokens >= 256 || vocab < 24576) return 1;
   const int64_t want = ceil_div(512, tokens);
   return (int)hmax(1, hmin(hmin(want, 64), vocab / 2048));
 }
@@ -409,8 +439,6 @@ hipError_t launch_logprobs(const void* X, int dt, int64_t tokens, int64_t vocab,
   a.vocab = vocab; a.ldx = ldx; a.top = top;
   a.seg = ns == 1 ? vocab : (ceil_div(vocab, ns) + 2047) / 2048 * 2048;
   a.nseg = (int)ceil_div(vocab, a.seg);
-  const int per16 = dt == GPTQ_BF16 ? 8 : 4;
-  a.vec = (reinterpret_cast<uintptr_t>(X) & 15) == 0 && ldx % per16 == 0;
   a.parts = static_cast<Part*>(ws);
   a.keys = reinterpret_cast<uint64_t*>(static_cast<char*>(ws) +
                                        align_up((size_t)tokens * ns * sizeof(Part), 16));

@@ -303,3 +303,49 @@ def test_a_heads_row_for_several_heads():
     with pytest.raises(q.GPTQError):
         x = torch.zeros((4, 128), device="cuda")
         q.fp8_linear(x, torch.zeros((128, 128), dtype=U8, device="cuda"), torch.ones((1, 1), device="cuda"), x)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V,top", [(1, 1), (2, 2), (6, 3), (9, 9), (2045, 4), (4100, 32), (25001, 20)])
+def test_logits_on_any_border(V, top, dtype):
+    """Rows that start on each border of a 16-byte piece, what lies in front of and behind
+    them larger than any logit; fewer rows than segments need, and many."""
+    q = need_gpu()
+    for T in (3, 300):
+        g = torch.Generator().manual_seed(V + T)
+        for off in (0, 1, 3, 5, 7):
+            base = torch.full((T, V + 9), 1e4).to(dtype)
+            base[:, off:off + V] = (torch.randn((T, V), generator=g) * 3).to(dtype)
+            base[1, off:off + V] = float("-inf")
+            base[2, off:off + V] = 7  # ties
+            x = base.cuda()[:, off:off + V]
+            ids = torch.randint(0, V, (T,), generator=g)
+            lp, ent = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+            ti, tl = torch.empty((T, top), dtype=torch.int32, device="cuda"), torch.empty((T, top), device="cuda")
+            say("logprobs on a border", T, V, off, dtype)
+            q.token_logprobs(x, ids.cuda(), lp, ent, ti, tl)
+            n = min(T, 12)
+            a, b, c, d = lowp.logprobs(base[:n, off:off + V].double().numpy(), ids[:n].numpy(), top)
+            assert np.array_equal(host(ti)[:n], c)
+            for got, want in ((lp, a), (ent, b), (tl, d)):
+                got, inf = host(got)[:n], np.isinf(want)
+                assert np.array_equal(np.isinf(got), inf) and np.all(got[inf] == want[inf])
+                assert np.all(np.abs(got[~inf] - want[~inf]) <= 2.0 ** -18 * (1 + np.abs(want[~inf])))
+
+
+@pytest.mark.parametrize("off", [0, 1, 3])
+def test_candidates_beyond_the_list_on_any_border(off):
+    q = need_gpu()
+    T, V = 260, 100000
+    g = torch.Generator().manual_seed(off)
+    x = torch.full((T, V + 4), -20.0)
+    col = torch.arange(V)
+    lanes = (col + off) // 8 % 256 < 9
+    x[:, off:off + V][:, lanes] = torch.randn(int(lanes.sum()), generator=g) + 5.0
+    ti, tl = torch.empty((T, 32), dtype=torch.int32, device="cuda"), torch.empty((T, 32), device="cuda")
+    say("logprobs, few lanes, border", off)
+    q.token_logprobs(x.cuda()[:, off:off + V], None, None, None, ti, tl)
+    rows = [0, 1, T - 1]
+    _, _, c, d = lowp.logprobs(x[rows, off:off + V].double().numpy(), None, 32)
+    assert np.array_equal(host(ti)[rows], c)
+    assert np.all(np.abs(host(tl)[rows] - d) <= 2.0 ** -18 * (1 + np.abs(d)))
