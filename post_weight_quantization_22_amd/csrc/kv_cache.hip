@@ -11,7 +11,7 @@
 // Both directions are bound by HBM (2 + 1 or 2 + 1/2 bytes a value).  A lane
 // owns 8 consecutive values of a row, a group spans LPG lanes of a wave and its
 // range is a butterfly over them.  Keys and values of 8 heads of 128: 131072 tokens read
-// from e4m3 in 156 us (5.2 TB/s), 8192 tokens written in 4 bits in 15 us (2.8 TB/s: the
+// from e4m3 in 156 us (5.2 TB/s), 8192 tokens written in 4 bits in 14 us (3.0 TB/s: the
 // index arithmetic and the codes' rounding fill the issue slots), 5 tokens in 5 us (the
 // launch and three dependent round trips: slots, rows, codes).
 #include "fp8.hpp"

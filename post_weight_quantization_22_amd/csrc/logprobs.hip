@@ -13,7 +13,7 @@
 // (m, r, t) of two parts join: with m1 >= m2, d = m2 - m1, w = e^d
 //   r = r1 + w (1 + r2),  t = t1 + w (t2 + d (1 + r2)).
 //
-// Bound by HBM: each logit is read once (2048 x 32000 fp32 in 56 us, 4.7 TB/s; few rows by
+// Bound by HBM: each logit is read once (2048 x 32000 fp32 in 57 us, 4.6 TB/s; few rows by
 // latency: 4 x 128000 7.8 us and 5.2 us to join the segments).
 // A workgroup of 256 takes a row (or a segment of it, where there are few rows; a
 // second kernel joins the segments).
