@@ -431,8 +431,8 @@ gptq_status fp8_quantize_blocks(const void* W, gptq_dtype wdt, int64_t m, int64_
  * fp8_linear: Y = X W^T from 16- or 32-bit activations: fp8_quantize_rows into
  * the workspace, then the product.  X as in fp8_quantize_rows; Y apart from X.
  * fp8_gated_gemm: the codes and scales (as fp8_swiglu_quantize writes them) of
- * h = silu(X Wg^T) * (X Wu^T), both products rounded to bf16: the first half of a
- * gated MLP block without its two products in memory.
+ * h = silu(X Wg^T) * (X Wu^T), both products summed as for bf16 Y and rounded to bf16:
+ * the first half of a gated MLP block without its two products in memory.
  * Workspace (16-byte aligned): fp8_gemm_workspace_size,
  * fp8_linear_workspace_size, fp8_gated_gemm_workspace_size(tokens, m, n).
  * ---------------------------------------------------------------------- */

@@ -201,6 +201,7 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
   // with three buffers or more the next block is there while one is multiplied, and
   // its first operands are read behind this one's last matrix instructions
   constexpr bool AHEAD = STAGES >= 3;
+  static_assert(AHEAD || !EXACT, "the bf16 form reads ahead");
   __shared__ __align__(16) uint8_t smem[STAGES * STAGE + STAGES * TT * 4];
 
   // tiles in runs per XCD; within a run, groups of 4 token tiles walked before the
@@ -335,15 +336,14 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
       Bf32 xw[NJ];
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        xw[j] = widen(AHEAD ? x[j] : frag(xst, 16 * (wt * NJ + j) + l16));
-        if (AHEAD) x[j] = frag(xnx, 16 * (wt * NJ + j) + l16);
+        xw[j] = widen(x[j]);
+        x[j] = frag(xnx, 16 * (wt * NJ + j) + l16);
       }
-      if (!AHEAD) w = frag(wst, wm * (TM / WM) + l16);
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
         const Bf32 ww = widen(w);
-        if (i + 1 < MI) w = frag(wst, wm * (TM / WM) + 16 * (i + 1) + l16);
-        else if (AHEAD) w = frag(wnx, wm * (TM / WM) + l16);
+        w = i + 1 < MI ? frag(wst, wm * (TM / WM) + 16 * (i + 1) + l16)
+                       : frag(wnx, wm * (TM / WM) + l16);
 #pragma unroll
         for (int j = i * PX / MI; j < (i + 1) * PX / MI; ++j) issue_x(j, cn, nbuf);
 #pragma unroll
