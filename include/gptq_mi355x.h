@@ -421,17 +421,15 @@ gptq_status fp8_quantize_blocks(const void* W, gptq_dtype wdt, int64_t m, int64_
  * wscales[ceil(m / 128)][ldws] as fp8_quantize_blocks writes them; Y[tokens, m]
  * (row stride ldy, fp32 or bf16).  R[tokens, m] (row stride ldr, Y's type), where
  * it is not NULL, is added before the rounding to Y's type; it may be Y itself.
- * Sums are fp32 in a fixed order and NaN codes give NaN.  For fp32 Y a block's
- * products are summed with fp32 accuracy; for bf16 Y and large batches by the
- * 8-bit matrix instructions, which cut the products of 8 neighbouring columns
- * at 2^-13 of the largest of them (1.5e-5 relative over normal data, against the
- * 2^-8 of Y's rounding).
+ * Sums are fp32, in an order that the sizes fix, and NaN codes give NaN: a
+ * token's row is the same in calls of other sizes but for the order of its fp32
+ * sums.
  * n a multiple of 16 (else GPTQ_ERR_UNSUPPORTED); X and W 16-byte aligned with
  * row strides that are multiples of 16 and at most 2^24 - 128.
  * fp8_linear: Y = X W^T from 16- or 32-bit activations: fp8_quantize_rows into
  * the workspace, then the product.  X as in fp8_quantize_rows; Y apart from X.
  * fp8_gated_gemm: the codes and scales (as fp8_swiglu_quantize writes them) of
- * h = silu(X Wg^T) * (X Wu^T), both products summed as for bf16 Y and rounded to bf16:
+ * h = silu(X Wg^T) * (X Wu^T), both products summed as in fp8_gemm and rounded to bf16:
  * the first half of a gated MLP block without its two products in memory.
  * Workspace (16-byte aligned): fp8_gemm_workspace_size,
  * fp8_linear_workspace_size, fp8_gated_gemm_workspace_size(tokens, m, n).

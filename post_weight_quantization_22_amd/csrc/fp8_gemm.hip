@@ -7,15 +7,13 @@
 //
 // Precision of the inner sum.  The e4m3 matrix instructions add their products in
 // groups of 8 that are cut, toward zero, at 2^-13 of the group's largest product
-// (measured: beside a product of 2^16 a product below 8 is lost): 1.5e-5 relative
-// over normal data.  Turned into bf16 first (exact: e4m3 has 4 significant bits)
-// the same operands are summed with fp32 accuracy (1e-8), at half the rate.  So
-// fp32 results and all small batches take the bf16 instruction.  The gated product
-// takes the 8-bit one: its two products are rounded to bf16 (2^-9 each) and their
-// gated product to e4m3 (2^-4), and where the cut moves one of them over a border of
-// those formats the code moves too.  Over normal data that gives the block's output a
-// relative error of 0.003 where exact sums would leave 0.0017; with the bf16
-// instruction the gate-and-up product of 512 x 11008 x 4096 takes 143 us, not 74.
+// (measured: beside a product of 2^16 a product below 8 is lost).  That is a bias, not
+// a rounding, and largest beside an outlier channel: over normal data 1.5e-5 of a
+// result, and a gated MLP block's output, whose codes move where the cut moves a
+// value over a border of their format, ends 0.003 from exact sums' instead of 0.0017.
+// So every product here widens its codes to bf16 (exact: e4m3 has 4 significant bits)
+// and takes the bf16 instruction, which sums them with fp32 accuracy (1e-8), at half
+// the rate.
 #include <type_traits>
 
 #include "fp8.hpp"
@@ -130,29 +128,24 @@ __device__ __forceinline__ void store_part(float* p, int64_t left, int64_t m, f3
 // Rows past the end are re-read from the last one and their results dropped; past
 // n the last block's segments re-read the row's last ones and meet zeros in X.
 //
-// What bounds the 256 x 256 tile is LDS: a block is 2048 matrix cycles, 192 KB of
-// operand reads and 64 KB of DMA.  So that the three run beside each other
-//  - a wave issues its DMA one instruction at a time between matrix instructions
-//    (all at once they hold it behind the CU's address unit);
-//  - the fmas of a row tile stand between the next one's matrix instructions, and
-//    the last one's between the first of the next block;
-//  - no branch comes between matrix instructions: past the last block the last
-//    one is fetched again into buffers that nothing reads.
-// Measured: 2048 x 8192 x 28672 in 256 x 256 tiles 418 us, 2.3 PFLOP/s (a library's
-// product with one scale for all: 2.55); gated 512 x 11008 x 4096 74 us, 1.25 PFLOP/s (172
-// tiles for 256 CUs); 512 x 4096 x 11008 in 128 x 128 tiles, two splits, 37 us, 1.25;
-// 333 x 1000 x 4112, fp32, in 128 x 64 tiles, five splits, 13 us: a few blocks a
+// What bounds the 256 x 256 tile are the matrix cores and the widening beside them: a
+// block is 4096 matrix cycles of a SIMD and 384 conversions, about 7 cycles each.  So
+// that they, 192 KB of operand reads and 64 KB of DMA run beside each other
+//  - a wave issues its DMA in pieces between the row tiles (all at once they hold it
+//    behind the CU's address unit);
+//  - a row tile's column tiles are summed two at a time: with all four sums open the
+//    256 registers do not suffice;
+//  - no branch comes between a matrix instruction and the reader of its result: past
+//    the last block the last one is fetched again into buffers that nothing reads.
+// Measured: 2048 x 8192 x 28672 in 256 x 256 tiles 755 us, 1.27 PFLOP/s (a library's
+// bf16 product: 1.36 to 1.47); gated 512 x 11008 x 4096 111 us, 0.83 PFLOP/s (172
+// tiles for 256 CUs); 512 x 4096 x 11008 in 128 x 128 tiles, two splits, 59 us, 0.78;
+// 333 x 1000 x 4112 in 128 x 64 tiles, five splits, 13 us: a few blocks a
 // workgroup, most of it the first blocks' latency.
 constexpr int kRow = 128;  // bytes of a row of a block
 constexpr uint32_t kXcds = 8;
 
 __device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
-
-// the 8-bit instruction: k = 128, the block, from a zero accumulator
-__device__ __forceinline__ f32x4 block_fast(i32x8 w, i32x8 x) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0,
-                                                          0, 0, 0);
-}
 
 struct Bf32 {
   bf16x8 k[4];
@@ -187,21 +180,21 @@ __device__ __forceinline__ void wait_vm() {  // at most N vector loads outstandi
   __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
 }
 
-template <int TM, int TT, int WM, int WT, int STAGES, bool EXACT, bool GATED = false>
+template <int TM, int TT, int WM, int WT, int STAGES, bool GATED = false>
 __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a) {
-  static_assert(!GATED || (TM == 2 * kFp8Block && WM == 2 && !EXACT), "a gate and an up block");
+  static_assert(!GATED || (TM == 2 * kFp8Block && WM == 2), "a gate and an up block");
   constexpr int MI = TM / WM / 16, NJ = TT / WT / 16, NW = WM * WT;
   constexpr int W_BYTES = TM * kRow, X_BYTES = TT * kRow, STAGE = W_BYTES + X_BYTES;
   constexpr int PW = TM / 8 / NW, PX = TT / 8 / NW;  // a wave's DMA instructions, 8 rows each
   static_assert(PW % 2 == 0 || PW == 1, "the swizzle of a piece goes by its parity");
   static_assert(PX % 2 == 0 || PX == 1, "the swizzle of a piece goes by its parity");
   static_assert(TM / WM <= kFp8Block && kFp8Block % (TM / WM) == 0, "a wave's rows share a scale");
+  static_assert(NJ % 2 == 0, "column tiles go in pairs");
   static_assert(TT % 64 == 0 && TT / 64 <= NW, "a wave fetches the scales of 64 tokens");
   constexpr int NS = TT / 64, LAG = STAGES - 1;  // waves that fetch scales; blocks in flight
   // with three buffers or more the next block is there while one is multiplied, and
   // its first operands are read behind this one's last matrix instructions
   constexpr bool AHEAD = STAGES >= 3;
-  static_assert(AHEAD || !EXACT, "the bf16 form reads ahead");
   __shared__ __align__(16) uint8_t smem[STAGES * STAGE + STAGES * TT * 4];
 
   // tiles in runs per XCD; within a run, groups of 4 token tiles walked before the
@@ -267,15 +260,11 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
     return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   };
 
-  f32x4 acc[MI][NJ], dp[NJ];
-  float sp[NJ];
+  f32x4 acc[MI][NJ];
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) {
+  for (int j = 0; j < NJ; ++j)
 #pragma unroll
     for (int i = 0; i < MI; ++i) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    dp[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    sp[j] = 0.f;
-  }
 #pragma unroll
   for (int p = 0; p < LAG; ++p) {
     const int c = min(c0 + p, c1 - 1);
@@ -327,92 +316,51 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
     // the block to fetch, and the buffer that block c - 1 has left
     const int cn = min(c + LAG, c1 - 1), nbuf = buf == 0 ? STAGES - 1 : buf - 1;
     const int c2 = min(c + 1, c1 - 1);
+    if constexpr (!AHEAD) {
+      w = frag(wst, wm * (TM / WM) + l16);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) x[j] = frag(xst, 16 * (wt * NJ + j) + l16);
+    }
     float s[NJ];
-    if (EXACT) {
-      issue_s(cn, nbuf);
+    issue_s(cn, nbuf);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) s[j] = sxl[buf * TT + 16 * (wt * NJ + j) + l16] * sw;
-      sw = const_load(swp + c2);
-      Bf32 xw[NJ];
+    for (int j = 0; j < NJ; ++j) s[j] = sxl[buf * TT + 16 * (wt * NJ + j) + l16] * sw;
+    sw = const_load(swp + c2);
+    Bf32 xw[NJ];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        xw[j] = widen(x[j]);
-        x[j] = frag(xnx, 16 * (wt * NJ + j) + l16);
-      }
+    for (int j = 0; j < NJ; ++j) {
+      xw[j] = widen(x[j]);
+      if (AHEAD) x[j] = frag(xnx, 16 * (wt * NJ + j) + l16);
+    }
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const Bf32 ww = widen(w);
-        w = i + 1 < MI ? frag(wst, wm * (TM / WM) + 16 * (i + 1) + l16)
-                       : frag(wnx, wm * (TM / WM) + l16);
+    for (int i = 0; i < MI; ++i) {
+      const Bf32 ww = widen(w);
+      if (i + 1 < MI) w = frag(wst, wm * (TM / WM) + 16 * (i + 1) + l16);
+      else if (AHEAD) w = frag(wnx, wm * (TM / WM) + l16);
 #pragma unroll
-        for (int j = i * PX / MI; j < (i + 1) * PX / MI; ++j) issue_x(j, cn, nbuf);
+      for (int j = i * PX / MI; j < (i + 1) * PX / MI; ++j) issue_x(j, cn, nbuf);
 #pragma unroll
-        for (int j = i * PW / MI; j < (i + 1) * PW / MI; ++j) issue_w(j, cn, nbuf);
-        f32x4 d[NJ];
+      for (int j = i * PW / MI; j < (i + 1) * PW / MI; ++j) issue_w(j, cn, nbuf);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) d[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int j0 = 0; j0 < NJ; j0 += 2) {
+        f32x4 d[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) d[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
-          for (int j = 0; j < NJ; ++j)
-            d[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ww.k[k], xw[j].k[k], d[j], 0, 0, 0);
+          for (int j = 0; j < 2; ++j)
+            d[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ww.k[k], xw[j0 + j].k[k], d[j], 0, 0, 0);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[j][e], s[j], acc[i][j][e]);
-      }
-    } else {
-      if constexpr (!AHEAD) {
-        w = frag(wst, wm * (TM / WM) + l16);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) x[j] = frag(xst, 16 * (wt * NJ + j) + l16);
-      }
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) s[j] = sxl[buf * TT + 16 * (wt * NJ + j) + l16] * sw;
-      sw = const_load(swp + c2);
-      __builtin_amdgcn_sched_barrier(0);
-      issue_s(cn, nbuf);
-#pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        i32x8 wn = w;
-        if (i + 1 < MI) wn = frag(wst, wm * (TM / WM) + 16 * (i + 1) + l16);
-        else if (AHEAD) wn = frag(wnx, wm * (TM / WM) + l16);
-        f32x4 d[NJ];
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          d[j] = block_fast(w, x[j]);
-          if (AHEAD && i + 1 == MI) x[j] = frag(xnx, 16 * (wt * NJ + j) + l16);
-          const int ip = i > 0 ? i - 1 : MI - 1;
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            acc[ip][j][e] = fmaf(dp[j][e], i > 0 ? s[j] : sp[j], acc[ip][j][e]);
-          // the DMA, X's first, after every second matrix instruction where there are
-          // enough of them
-          constexpr int P = PX + PW, SPAN = MI * NJ < 2 * P ? MI * NJ : 2 * P;
-#pragma unroll
-          for (int k = 0; k < P; ++k)
-            if ((k + 1) * SPAN / P - 1 == i * NJ + j) {
-              if (k < PX) issue_x(k, cn, nbuf);
-              else issue_w(k - PX, cn, nbuf);
-            }
-          __builtin_amdgcn_sched_barrier(0);
-        }
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) dp[j] = d[j];
-        w = wn;
+            acc[i][j0 + j][e] = fmaf(d[j][e], s[j0 + j], acc[i][j0 + j][e]);
       }
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) sp[j] = s[j];
     }
     buf = after;
   }
   wait_vm<0>();  // no DMA into this LDS outlives the workgroup
-  if (!EXACT) {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[MI - 1][j][e] = fmaf(dp[j][e], sp[j], acc[MI - 1][j][e]);
-  }
   if constexpr (GATED) {
     constexpr int NH = NJ / 2;  // column tiles that a wave of a pair quantizes
     __syncthreads();            // every operand has been read
@@ -692,9 +640,9 @@ __global__ __launch_bounds__(256) void fp8_gemm_reduce_kernel(GemmArgs a, int ks
 }
 
 // Batches that go through fp8_gemv_kernel: 16 tokens, and 32 over weights that a
-// few microseconds read (32 x 4096 x 4096: 8 us, in narrow tiles 11.5; but
-// 32 x 11008 x 4096: 20 and 15, 32 x 8192 x 28672: 66 and 49, where the tiles'
-// deeper DMA counts).
+// few microseconds read (32 x 4096 x 4096: 8.8 us, in narrow tiles 11.8, 32 x 8192 x 4096
+// 11.0 and 15.9; but 32 x 4096 x 11008 19.6 and 18.6, 32 x 8192 x 28672 57 and 52, where
+// the tiles' deeper DMA counts; 32 x 11008 x 4096 20 either way).
 bool by_gemv(int64_t tokens, int64_t m, int64_t n) {
   return tokens <= 16 || (tokens <= 32 && m * n <= int64_t(1) << 25);
 }
@@ -729,37 +677,42 @@ bool quantizes_itself(int64_t tokens, int64_t n) {
 }
 
 // How a product is cut: tile, and K splits where the tiles do not reach every CU.
-// Measured for bf16 results (us):             256x256  256x128  128x128 (split)
-//   2048 x 8192 x 28672 (256 tiles of 256x256)    420        -        -
-//   512 x 11008 x 4096  (86 of 256x256)            46       43       50
-//   2048 x 4096 x 4096  (128)                      54       45       52
-//   1024 x 4096 x 4096  (256 of 128x128)           43       35       26
-//   512 x 4096 x 11008  (128, 2 splits)            52       42       41
+// Measured (us):                              256x256  256x128  128x128 (split)
+//   2048 x 8192 x 28672 (256 tiles of 256x256)    755      950      995
+//   512 x 22016 x 4096  (172)                     119      139        -
+//   1024 x 16640 x 4096 (260, 520 of 256x128)     213      198        -
+//   4096 x 11008 x 4096 (688, 1376)               326      395        -
+//   512 x 11008 x 4096  (86, 172)                 105       70       78
+//   1024 x 4096 x 4096  (256 of 128x128)          104       67       42
+//   512 x 4096 x 11008  (128, 2 splits)           259      167       61
+// A CU takes one tile after another: a round of 256 x 256 tiles over the CUs takes as
+// long as 1.6 rounds of 256 x 128 tiles, and the fewer of the two are taken.
 enum Tile { T256x256, T256x128, T128x128, T128x64 };
 struct Plan {
   Tile tile;
   int ks;
 };
 
-Plan plan_of(int64_t tokens, int64_t m, int64_t n, bool exact) {
+Plan plan_of(int64_t tokens, int64_t m, int64_t n) {
   const int64_t nb = ceil_div(n, (int64_t)kFp8Block);
   auto tiles = [&](int64_t tm, int64_t tt) { return ceil_div(m, tm) * ceil_div(tokens, tt); };
-  if (!exact && tiles(256, 256) >= 160) return {T256x256, 1};
-  if (tiles(128, 128) > 256) return {T256x128, 1};
+  auto rounds = [&](int64_t tm, int64_t tt) { return ceil_div(tiles(tm, tt), int64_t(256)); };
+  if (tiles(128, 128) > 256)
+    return {8 * rounds(256, 256) <= 5 * rounds(256, 128) ? T256x256 : T256x128, 1};
   // the narrow tile for narrow batches, and where there is little work for each CU
-  // (333 x 1000 x 4112: 16.4 -> 14.4 us, 128 x 4096 x 4096: 17.8 -> 14.9; but
-  // 128 x 8192 x 28672: 62 -> 72)
+  // (128 x 128 and 128 x 64: 333 x 1000 x 4112 19.3 and 17.2 us, 128 x 4096 x 4096 21.3
+  // and 18.5; but 128 x 8192 x 28672 80 and 101)
   const Tile tile = tokens <= 64 || tiles(128, 128) * nb < 8 * 256 ? T128x64 : T128x128;
   const int64_t t = tiles(128, tile == T128x64 ? 64 : 128);
   return {tile, (int)hmax(1, hmin(hmin(256 / t, nb / 4), 16))};
 }
 
-template <int TM, int TT, int WM, int WT, int STAGES, bool EXACT, bool GATED = false>
+template <int TM, int TT, int WM, int WT, int STAGES, bool GATED = false>
 void launch_tile(GemmArgs a, int ks, hipStream_t stream) {
   a.ntm = ceil_div(a.m, (int64_t)(GATED ? TM / 2 : TM));
   a.ntt = ceil_div(a.tokens, (int64_t)TT);
   const int64_t grid = ceil_div(a.ntm * a.ntt, kXcds) * kXcds;
-  hipLaunchKernelGGL((fp8_gemm_tile_kernel<TM, TT, WM, WT, STAGES, EXACT, GATED>),
+  hipLaunchKernelGGL((fp8_gemm_tile_kernel<TM, TT, WM, WT, STAGES, GATED>),
                      dim3((unsigned)grid, (unsigned)ks), dim3(WM * WT * 64), 0, stream, a);
 }
 
@@ -767,9 +720,7 @@ void launch_tile(GemmArgs a, int ks, hipStream_t stream) {
 
 size_t fp8_gemm_ws_bytes(int64_t tokens, int64_t m, int64_t n) {
   if (by_gemv(tokens, m, n)) return 0;
-  // either type of Y
-  const Plan e = plan_of(tokens, m, n, true), f = plan_of(tokens, m, n, false);
-  const int ks = e.ks > f.ks ? e.ks : f.ks;
+  const int ks = plan_of(tokens, m, n).ks;
   return ks == 1 ? 0 : (size_t)ks * tokens * m * 4;
 }
 
@@ -792,22 +743,12 @@ static GemmArgs gemm_args(const Fp8GemmArgs& g) {
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, hipStream_t stream) {
   const GemmArgs a = gemm_args(g);
   if (by_gemv(g.tokens, g.m, g.n)) return launch_gemv<SRC_CODES>(GemvArgs{a, nullptr, 0, 0}, 0, stream);
-  const bool exact = !a.ybf16;
-  const Plan p = plan_of(g.tokens, g.m, g.n, exact);
+  const Plan p = plan_of(g.tokens, g.m, g.n);
   switch (p.tile) {
-    case T256x256: launch_tile<256, 256, 2, 4, 2, false>(a, 1, stream); break;
-    case T256x128:
-      if (exact) launch_tile<256, 128, 2, 4, 3, true>(a, 1, stream);
-      else launch_tile<256, 128, 2, 4, 3, false>(a, 1, stream);
-      break;
-    case T128x128:
-      if (exact) launch_tile<128, 128, 2, 4, 4, true>(a, p.ks, stream);
-      else launch_tile<128, 128, 2, 4, 4, false>(a, p.ks, stream);
-      break;
-    case T128x64:
-      if (exact) launch_tile<128, 64, 4, 2, 6, true>(a, p.ks, stream);
-      else launch_tile<128, 64, 4, 2, 6, false>(a, p.ks, stream);
-      break;
+    case T256x256: launch_tile<256, 256, 2, 4, 2>(a, 1, stream); break;
+    case T256x128: launch_tile<256, 128, 2, 4, 3>(a, 1, stream); break;
+    case T128x128: launch_tile<128, 128, 2, 4, 4>(a, p.ks, stream); break;
+    case T128x64: launch_tile<128, 64, 4, 2, 6>(a, p.ks, stream); break;
   }
   if (p.ks > 1) {
     const int64_t total = g.tokens * ceil_div(g.m, (int64_t)4);
@@ -818,13 +759,13 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, hipStream_t stream) {
 }
 
 // The gated product in one kernel where more than one row of its 256 x 256 tiles is
-// needed and they reach half of the CUs; else the two products into the workspace
-// (bf16 [tokens][m] each) and the quantizer behind them.  In one and in three (us):
-// 512 x 11008 x 4096 71 and 112, 300 x 11008 x 4096 78 and 105, 512 x 8192 x 4096 (128
-// tiles) 60 and 62; but 512 x 4096 x 4096 (64) 57 and 51, 256 x 11008 x 4096 70 and
-// 61, 64 x 28672 x 8192 160 and 118.
+// needed and they reach more than half of the CUs; else the two products into the
+// workspace (bf16 [tokens][m] each) and the quantizer behind them.  In one and in three
+// (us): 512 x 11008 x 4096 (172 tiles) 111 and 145, 300 x 11008 x 4096 111 and 141,
+// 2048 x 11008 x 4096 332 and 427; but 512 x 8192 x 4096 (128 tiles) 111 and 91,
+// 512 x 4096 x 4096 (64) 108 and 67, 256 x 11008 x 4096 110 and 86.
 static bool gated_in_one(int64_t tokens, int64_t m) {
-  return tokens > 256 && ceil_div(tokens, (int64_t)256) * ceil_div(m, (int64_t)128) >= 128;
+  return tokens > 256 && ceil_div(tokens, (int64_t)256) * ceil_div(m, (int64_t)128) > 128;
 }
 
 static int64_t gated_ld(int64_t m) { return (m + 7) / 8 * 8; }
@@ -844,7 +785,7 @@ hipError_t launch_fp8_gated(const Fp8GemmArgs& g, const uint8_t* W2, int64_t ldw
     a.codes = codes; a.ldc = ldc;
     a.scales = scales; a.ldso = ldso;
     a.vec4 = reinterpret_cast<uintptr_t>(codes) % 4 == 0 && ldc % 4 == 0;
-    launch_tile<256, 256, 2, 4, 2, false, true>(a, 1, stream);
+    launch_tile<256, 256, 2, 4, 2, true>(a, 1, stream);
     return hipGetLastError();
   }
   const int64_t ld = gated_ld(g.m);
