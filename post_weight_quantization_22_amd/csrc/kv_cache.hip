@@ -14,6 +14,7 @@
 // from e4m3 in 156 us (5.2 TB/s), 8192 tokens written in 4 bits in 14 us (3.0 TB/s: the
 // index arithmetic and the codes' rounding fill the issue slots), 5 tokens in 5 us (the
 // launch and three dependent round trips: slots, rows, codes).
+#include "bits.hpp"
 #include "fp8.hpp"
 
 namespace gptq {
@@ -374,12 +375,6 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvArgs a) {
   }
 }
 
-inline int log2_at_least(int v) {
-  int p = 0;
-  while ((1 << p) < v) ++p;
-  return p;
-}
-
 // (a lane of `width` values)
 Side side_of(const gptq_kv_cache* c, const KvRows& r, int dt, int width) {
   Side s = {};
@@ -434,7 +429,7 @@ KvArgs args_of(const gptq_kv_cache* kc, const gptq_kv_cache* vc, const int64_t* 
   a.tokens = tokens;
   a.nslots = c->pages * c->page_size;
   a.page_size = c->page_size;
-  a.page_shift = (1 << log2_at_least(c->page_size)) == c->page_size ? log2_at_least(c->page_size) : -1;
+  a.page_shift = log2_exact(c->page_size);
   a.flat = flat(kc) && flat(vc);
   a.info = info;
   return a;
