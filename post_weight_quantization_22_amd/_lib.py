@@ -693,9 +693,11 @@ def _on_gpu(t, name: str):
     return d
 
 
-def _plane(t, name: str, rows: int, cols: int, kinds: str, device) -> int:
+def _plane(t, name: str, rows: int, cols: int, kinds: str, device, exact: str = "") -> int:
     """Checks a 2-D operand (unit column stride, at least rows x cols, on
-    ``device``, a dtype among ``kinds``) and returns its row stride."""
+    ``device``, a dtype among ``kinds``) and returns its row stride.  ``exact``: "r" and
+    "c" for rows and columns that have to be as many as stated -- an operand's, where
+    more of them mean that it belongs to another product; outputs may be larger."""
     if t is None:
         raise ValueError(f"{name} is required")
     if _KIND.get(t.dtype, "?") not in kinds:
@@ -706,6 +708,8 @@ def _plane(t, name: str, rows: int, cols: int, kinds: str, device) -> int:
     if len(shape) != 2 or shape[0] < rows or shape[1] < cols or (stride[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name}: expected a 2-D tensor of at least {rows} x {cols} with unit "
                          f"column stride, got shape {tuple(shape)} strides {stride}")
+    if exact and (("r" in exact and shape[0] != rows) or ("c" in exact and shape[1] != cols)):
+        raise ValueError(f"{name}: expected {rows} x {cols}, got shape {tuple(shape)}")
     # the stride of a single row is not meaningful
     return stride[0] if shape[0] > 1 else max(stride[0], shape[1])
 
@@ -771,7 +775,7 @@ def fp8_swiglu_quantize(gate, up, codes, scales, stream=None) -> None:
     tokens, n = gate.shape
     d = _on_gpu(gate, "gate")
     ldg = _plane(gate, "gate", tokens, n, "bf", d)
-    ldu = _plane(up, "up", tokens, n, _KIND[gate.dtype], d)
+    ldu = _plane(up, "up", tokens, n, _KIND[gate.dtype], d, "rc")
     ldc = _plane(codes, "codes", tokens, n, "8u", d)
     lds = _plane(scales, "scales", -(-n // FP8_BLOCK), tokens, "f", d)
     _launch("fp8_swiglu_quantize", d, stream, gate.data_ptr(), ldg, up.data_ptr(), ldu,
@@ -800,18 +804,22 @@ def fp8_linear_workspace_size(tokens: int, m: int, n: int) -> int:
 
 def fp8_gemm(X, xscales, W, wscales, Y, residual=None, ws=None, stream=None) -> None:
     """Y[tokens, m] (fp32 or bf16) = X W^T of block-scaled e4m3 operands: X[tokens, n] with
-    xscales[ceil(n / 128), tokens], W[m, n] with wscales[ceil(m / 128), ceil(n / 128)]; plus
-    residual[tokens, m] (Y's type, may be Y) where it is given."""
+    xscales[ceil(n / 128), tokens] (it may hold more tokens), W[m, n] with
+    wscales[ceil(m / 128), ceil(n / 128)]; plus residual[tokens, m] (Y's type, may be Y) where
+    it is given.  Y may have more rows and columns, which are left alone."""
     tokens, n = X.shape
     m = W.shape[0]
     d = _on_gpu(X, "X")
     nb = -(-n // FP8_BLOCK)
     ldx = _plane(X, "X", tokens, n, "8u", d)
-    ldxs = _plane(xscales, "xscales", nb, tokens, "f", d)
-    ldw = _plane(W, "W", m, n, "8u", d)
-    ldws = _plane(wscales, "wscales", -(-m // FP8_BLOCK), nb, "f", d)
+    ldxs = _plane(xscales, "xscales", nb, tokens, "f", d, "r")
+    ldw = _plane(W, "W", m, n, "8u", d, "rc")
+    ldws = _plane(wscales, "wscales", -(-m // FP8_BLOCK), nb, "f", d, "rc")
     ldy = _plane(Y, "Y", tokens, m, "bf", d)
-    ldr = 0 if residual is None else _plane(residual, "residual", tokens, m, _KIND[Y.dtype], d)
+    ldr = 0
+    if residual is not None:
+        ldr = _plane(residual, "residual", tokens, m, _KIND[Y.dtype], d,
+                     "" if residual.shape == Y.shape else "rc")
     p, nbytes, ws = _space(fp8_gemm_workspace_size(tokens, m, n), ws, d, stream)
     _launch("fp8_gemm", d, stream, X.data_ptr(), tokens, n, ldx, xscales.data_ptr(), ldxs,
             W.data_ptr(), m, ldw, wscales.data_ptr(), ldws, _ptr(residual), ldr, Y.data_ptr(),
@@ -825,8 +833,8 @@ def fp8_linear(X, W, wscales, Y, ws=None, stream=None) -> None:
     m = W.shape[0]
     d = _on_gpu(X, "X")
     ldx = _plane(X, "X", tokens, n, "bf", d)
-    ldw = _plane(W, "W", m, n, "8u", d)
-    ldws = _plane(wscales, "wscales", -(-m // FP8_BLOCK), -(-n // FP8_BLOCK), "f", d)
+    ldw = _plane(W, "W", m, n, "8u", d, "rc")
+    ldws = _plane(wscales, "wscales", -(-m // FP8_BLOCK), -(-n // FP8_BLOCK), "f", d, "rc")
     ldy = _plane(Y, "Y", tokens, m, "bf", d)
     p, nbytes, ws = _space(fp8_linear_workspace_size(tokens, m, n), ws, d, stream)
     _launch("fp8_linear", d, stream, X.data_ptr(), _FLOAT[_KIND[X.dtype]], tokens, n, ldx,
@@ -846,11 +854,11 @@ def fp8_gated_gemm(X, xscales, Wg, gscales, Wu, uscales, codes, scales, ws=None,
     d = _on_gpu(X, "X")
     nb, mb = -(-n // FP8_BLOCK), -(-m // FP8_BLOCK)
     ldx = _plane(X, "X", tokens, n, "8u", d)
-    ldxs = _plane(xscales, "xscales", nb, tokens, "f", d)
-    ldwg = _plane(Wg, "Wg", m, n, "8u", d)
-    ldgs = _plane(gscales, "gscales", mb, nb, "f", d)
-    ldwu = _plane(Wu, "Wu", m, n, "8u", d)
-    ldus = _plane(uscales, "uscales", mb, nb, "f", d)
+    ldxs = _plane(xscales, "xscales", nb, tokens, "f", d, "r")
+    ldwg = _plane(Wg, "Wg", m, n, "8u", d, "rc")
+    ldgs = _plane(gscales, "gscales", mb, nb, "f", d, "rc")
+    ldwu = _plane(Wu, "Wu", m, n, "8u", d, "rc")
+    ldus = _plane(uscales, "uscales", mb, nb, "f", d, "rc")
     ldc = _plane(codes, "codes", tokens, m, "8u", d)
     lds = _plane(scales, "scales", mb, tokens, "f", d)
     p, nbytes, ws = _space(fp8_gated_gemm_workspace_size(tokens, m, n), ws, d, stream)
