@@ -229,16 +229,22 @@ def quantize_layer_fp8(W: torch.Tensor, stream=None) -> Fp8Layer:
 
 def forward_block_fp8(x: torch.Tensor, block: Fp8Block, out: Optional[torch.Tensor] = None,
                       stream=None) -> torch.Tensor:
-    """x' [tokens, d] (bf16) of one block for x [tokens, d] (bf16); d and f multiples of 16.
+    """x' [tokens, d] (bf16) of one block for x [tokens, d] (bf16); gate and up [f, d], down
+    [d, f], d and f multiples of 16; out: bf16, at least [tokens, d],
+    may be x.
     Enqueued on ``stream`` (default: the current stream of x's device)."""
-    if stream is None:
-        stream = torch.cuda.current_stream(x.device)
-    if stream.device != x.device:
-        raise ValueError(f"the stream is on {stream.device}, x on {x.device}")
     if x.dtype != torch.bfloat16:
         raise TypeError(f"x: dtype {x.dtype}, expected bfloat16")
     T, d = x.shape
     f = block.gate.codes.shape[0]
+    for name, shape in (("gate", (f, d)), ("up", (f, d)), ("down", (d, f))):
+        got = tuple(getattr(block, name).codes.shape)
+        if got != shape:
+            raise ValueError(f"{name}: codes of shape {got}, expected {shape}")
+    if stream is None:
+        stream = torch.cuda.current_stream(x.device)
+    if stream.device != x.device:
+        raise ValueError(f"the stream is on {stream.device}, x on {x.device}")
     with torch.cuda.stream(stream):  # the buffers between the steps belong to the stream
         def buf(rows, cols, dtype):
             return torch.empty((rows, cols), dtype=dtype, device=x.device)
