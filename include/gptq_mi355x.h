@@ -430,7 +430,8 @@ gptq_status fp8_quantize_blocks(const void* W, gptq_dtype wdt, int64_t m, int64_
  * the workspace, then the product.  X as in fp8_quantize_rows; Y apart from X.
  * fp8_gated_gemm: the codes and scales (as fp8_swiglu_quantize writes them) of
  * h = silu(X Wg^T) * (X Wu^T), both products summed as in fp8_gemm and rounded to bf16:
- * the first half of a gated MLP block without its two products in memory.
+ * the first half of a gated MLP block without its two products in memory; codes
+ * apart from X.
  * Workspace (16-byte aligned): fp8_gemm_workspace_size,
  * fp8_linear_workspace_size, fp8_gated_gemm_workspace_size(tokens, m, n).
  * ---------------------------------------------------------------------- */

@@ -848,7 +848,7 @@ def fp8_gated_gemm_workspace_size(tokens: int, m: int, n: int) -> int:
 def fp8_gated_gemm(X, xscales, Wg, gscales, Wu, uscales, codes, scales, ws=None,
                    stream=None) -> None:
     """codes[tokens, m] and scales[ceil(m / 128), tokens] of silu(X Wg^T) * (X Wu^T), the
-    products (operands as in fp8_gemm) rounded to bf16."""
+    products (operands as in fp8_gemm) rounded to bf16; codes apart from X."""
     tokens, n = X.shape
     m = Wg.shape[0]
     d = _on_gpu(X, "X")

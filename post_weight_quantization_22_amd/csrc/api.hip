@@ -489,7 +489,8 @@ gptq_status fp8_gated_gemm(const uint8_t* X, int64_t tokens, int64_t n, int64_t 
   if (ldx > kFp8MaxStride) return GPTQ_ERR_UNSUPPORTED;
   const gptq_status w = check_ws(ws, ws_bytes, fp8_gated_ws_bytes(tokens, m, n));
   if (w != GPTQ_OK) return w;
-  if ((reinterpret_cast<uintptr_t>(ws) & 15) != 0) return GPTQ_ERR_INVALID_ARG;
+  // in one kernel, workgroups read X while others write codes
+  if ((reinterpret_cast<uintptr_t>(ws) & 15) != 0 || codes == X) return GPTQ_ERR_INVALID_ARG;
   Fp8GemmArgs g{X,    ldx,     tokens, n,       xs, ldxs, Wg,      ldwg, m, gscales,
                 ldgs, nullptr, GPTQ_BF16, 0, nullptr, 0, ws};
   return hip_status(launch_fp8_gated(g, Wu, ldwu, uscales, ldus, codes, ldc, scales, lds, stream));
