@@ -400,6 +400,7 @@ gptq_status gptq_layer_error(const void* W, gptq_dtype wdt, int64_t m, int64_t n
  * bits in between).
  * fp8_quantize_blocks: W[m, n] (row stride ldw), one scale per 128 x 128 block;
  * codes[m, n] (row stride ldc), scales[ceil(m / 128)][lds], lds >= ceil(n / 128).
+ * Codes apart from what they are made of (refused where both start at one place).
  * ---------------------------------------------------------------------- */
 gptq_status fp8_quantize_rows(const void* X, gptq_dtype xdt, int64_t tokens, int64_t n,
                               int64_t ldx, uint8_t* codes, int64_t ldc, float* scales,
@@ -420,7 +421,8 @@ gptq_status fp8_quantize_blocks(const void* W, gptq_dtype wdt, int64_t m, int64_
  * fp8_quantize_rows writes them, W[m, n] (row stride ldw) with
  * wscales[ceil(m / 128)][ldws] as fp8_quantize_blocks writes them; Y[tokens, m]
  * (row stride ldy, fp32 or bf16).  R[tokens, m] (row stride ldr, Y's type), where
- * it is not NULL, is added before the rounding to Y's type; it may be Y itself.
+ * it is not NULL, is added before the rounding to Y's type; it may be Y itself.  Y
+ * apart from X.
  * Sums are fp32, in an order that the sizes fix, and NaN codes give NaN: a
  * token's row is the same in calls of other sizes but for the order of its fp32
  * sums.
@@ -482,8 +484,8 @@ gptq_status fp8_gated_gemm(const uint8_t* X, int64_t tokens, int64_t n, int64_t 
  * and is not written.  Where a slot occurs twice the later token's row stays.
  * kv_cache_read: the rows of slots[tokens] as K and V; a negative slot gives
  * zeros, a slot may occur any number of times.  Either cache may be NULL (with
- * its rows); two caches of a call have the same pages and page_size and share no
- * memory.  Strides of dimensions longer than 1 are not 0, but for the rows that
+ * its rows); two caches of a call have the same pages and page_size and, where they
+ * are written, share no memory; rows that are read into share none either.  Strides of dimensions longer than 1 are not 0, but for the rows that
  * kv_cache_write reads (one head's row for several heads).
  * A slot past the last is not accessed (write: skipped, read: zeros), and *info
  * (a device int32 that the caller has cleared, may be NULL) becomes 1.

@@ -385,7 +385,8 @@ gptq_status fp8_quantize_rows(const void* X, gptq_dtype xdt, int64_t tokens, int
   if (tokens < 0 || bad_dim(tokens) || n <= 0 || bad_dim(n) || !valid_dtype(xdt))
     return GPTQ_ERR_INVALID_ARG;
   if (tokens == 0) return GPTQ_OK;
-  if (!X || !codes || !scales || ldx < n || ldc < n || lds < tokens) return GPTQ_ERR_INVALID_ARG;
+  if (!X || !codes || !scales || ldx < n || ldc < n || lds < tokens || codes == X)
+    return GPTQ_ERR_INVALID_ARG;
   return hip_status(launch_fp8_rows(X, ldx, nullptr, 0, xdt, tokens, n, codes, ldc, scales, lds,
                                     stream));
 }
@@ -396,7 +397,8 @@ gptq_status fp8_swiglu_quantize(const void* gate, int64_t ldg, const void* up, i
   if (tokens < 0 || bad_dim(tokens) || n <= 0 || bad_dim(n) || !valid_dtype(dt))
     return GPTQ_ERR_INVALID_ARG;
   if (tokens == 0) return GPTQ_OK;
-  if (!gate || !up || !codes || !scales || ldg < n || ldu < n || ldc < n || lds < tokens)
+  if (!gate || !up || !codes || !scales || ldg < n || ldu < n || ldc < n || lds < tokens ||
+      codes == gate || codes == up)
     return GPTQ_ERR_INVALID_ARG;
   return hip_status(launch_fp8_rows(gate, ldg, up, ldu, dt, tokens, n, codes, ldc, scales, lds,
                                     stream));
@@ -408,7 +410,8 @@ gptq_status fp8_quantize_blocks(const void* W, gptq_dtype wdt, int64_t m, int64_
   if (m < 0 || bad_dim(m) || n <= 0 || bad_dim(n) || !valid_dtype(wdt))
     return GPTQ_ERR_INVALID_ARG;
   if (m == 0) return GPTQ_OK;
-  if (!W || !codes || !scales || ldw < n || ldc < n || lds < ceil_div(n, int64_t(128)))
+  if (!W || !codes || !scales || ldw < n || ldc < n || lds < ceil_div(n, int64_t(128)) ||
+      codes == W)
     return GPTQ_ERR_INVALID_ARG;
   return hip_status(launch_fp8_blocks(W, wdt, m, n, ldw, codes, ldc, scales, lds, stream));
 }
@@ -439,7 +442,7 @@ gptq_status fp8_gemm(const uint8_t* X, int64_t tokens, int64_t n, int64_t ldx, c
   if (ldx > kFp8MaxStride) return GPTQ_ERR_UNSUPPORTED;
   const gptq_status w = check_ws(ws, ws_bytes, fp8_gemm_ws_bytes(tokens, m, n));
   if (w != GPTQ_OK) return w;
-  if ((reinterpret_cast<uintptr_t>(ws) & 15) != 0) return GPTQ_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(ws) & 15) != 0 || X == Y) return GPTQ_ERR_INVALID_ARG;
   Fp8GemmArgs g{X, ldx, tokens, n, xs, ldxs, W, ldw, m, wscales, ldws, Y, ydt, ldy, R, ldr, ws};
   return hip_status(launch_fp8_gemm(g, stream));
 }
@@ -515,7 +518,11 @@ gptq_status kv_cache_write(const void* K, int64_t k_token_stride, int64_t k_head
   const gptq_kv_cache* c = kc ? kc : vc;
   const gptq_status w = check_ws(ws, ws_bytes, kv_write_ws_bytes(tokens, c->pages * c->page_size));
   if (w != GPTQ_OK) return w;
-  if ((reinterpret_cast<uintptr_t>(ws) & 3) != 0) return GPTQ_ERR_INVALID_ARG;
+  // (one cache for both: keys and values would race for its slots)
+  if ((reinterpret_cast<uintptr_t>(ws) & 3) != 0 ||
+      (kc && vc && (kc->codes == vc->codes || kc->scales == vc->scales ||
+                    (kc->zeros && kc->zeros == vc->zeros))))
+    return GPTQ_ERR_INVALID_ARG;
   const KvRows k{const_cast<void*>(K), k_token_stride, k_head_stride};
   const KvRows v{const_cast<void*>(V), v_token_stride, v_head_stride};
   return hip_status(launch_kv_write(k, v, dt, tokens, slots, kc, vc, info, ws, stream));
@@ -529,7 +536,8 @@ gptq_status kv_cache_read(const gptq_kv_cache* kc, const gptq_kv_cache* vc, cons
   if (ok != GPTQ_OK || tokens == 0) return ok;
   // rows that are written share no place
   if ((kc && ((tokens > 1 && k_token_stride == 0) || (kc->heads > 1 && k_head_stride == 0))) ||
-      (vc && ((tokens > 1 && v_token_stride == 0) || (vc->heads > 1 && v_head_stride == 0))))
+      (vc && ((tokens > 1 && v_token_stride == 0) || (vc->heads > 1 && v_head_stride == 0))) ||
+      (kc && vc && K == V))
     return GPTQ_ERR_INVALID_ARG;
   const KvRows k{K, k_token_stride, k_head_stride}, v{V, v_token_stride, v_head_stride};
   return hip_status(launch_kv_read(kc, vc, slots, tokens, k, v, dt, info, stream));

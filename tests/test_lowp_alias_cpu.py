@@ -1,5 +1,7 @@
 """Outputs in the place of operands that other workgroups still read are refused before
 anything is enqueued (the pointers here are never dereferenced)."""
+import ctypes
+
 import pytest
 
 pytest.importorskip("torch")
@@ -15,3 +17,37 @@ def test_gated_product(t, size):
     assert so.fp8_gated_gemm(FAKE, t, size, size, 2 * FAKE, t, 3 * FAKE, size, size, 4 * FAKE, nb,
                              5 * FAKE, size, 6 * FAKE, nb, FAKE, size, 7 * FAKE, t, 8 * FAKE, 1 << 40,
                              None) == BAD
+
+
+def test_quantizers():
+    so = _lib.load()
+    assert so.fp8_quantize_rows(FAKE, 1, 4, 256, 256, FAKE, 512, 2 * FAKE, 4, None) == BAD
+    assert so.fp8_quantize_blocks(FAKE, 1, 4, 256, 256, FAKE, 512, 2 * FAKE, 2, None) == BAD
+    for gate, up in ((FAKE, 2 * FAKE), (2 * FAKE, FAKE)):
+        assert so.fp8_swiglu_quantize(gate, 256, up, 256, 1, 4, 256, FAKE, 512, 3 * FAKE, 4, None) == BAD
+
+
+@pytest.mark.parametrize("t", [4, 300])
+def test_product(t):
+    so = _lib.load()
+    assert so.fp8_gemm(FAKE, t, 256, 256, 2 * FAKE, t, 3 * FAKE, 64, 256, 4 * FAKE, 2, None, 0, FAKE, 0, 64,
+                       5 * FAKE, 1 << 40, None) == BAD
+
+
+def _cache(codes, scales, zeros=None):
+    return _lib.GPTQKVCache(codes=codes, scales=scales, zeros=zeros, pages=4, page_stride=16 * 2 * 64,
+                            slot_stride=2 * 64, head_stride=64, param_page_stride=32, param_slot_stride=2,
+                            param_head_stride=1, page_size=16, heads=2, head_dim=64, group_size=64, format=1)
+
+
+@pytest.mark.parametrize("t", [4, 2000])
+def test_cache(t):
+    so = _lib.load()
+    for c, s, z in ((FAKE, 2 * FAKE, None), (FAKE, 3 * FAKE, None), (4 * FAKE, 2 * FAKE, None),
+                    (4 * FAKE, 3 * FAKE, 9 * FAKE)):
+        kc, vc = _cache(FAKE, 2 * FAKE, 9 * FAKE), _cache(c, s, z)
+        assert so.kv_cache_write(5 * FAKE, 128, 64, 6 * FAKE, 128, 64, 1, t, 7 * FAKE, ctypes.byref(kc),
+                                 ctypes.byref(vc), None, 8 * FAKE, 1 << 20, None) == BAD
+    kc, vc = _cache(FAKE, 2 * FAKE), _cache(3 * FAKE, 4 * FAKE)
+    assert so.kv_cache_read(ctypes.byref(kc), ctypes.byref(vc), 7 * FAKE, t, 5 * FAKE, 128, 64, 5 * FAKE, 128, 64,
+                            1, None, None) == BAD
