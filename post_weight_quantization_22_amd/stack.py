@@ -217,13 +217,19 @@ class Fp8Block:
 
 
 def quantize_layer_fp8(W: torch.Tensor, stream=None) -> Fp8Layer:
-    """W[m, n] (bf16 or fp32) as e4m3 codes and block scales."""
+    """W[m, n] (bf16 or fp32) as e4m3 codes and block scales, enqueued on ``stream`` (default:
+    the current stream of W's device), which their memory belongs to."""
+    if stream is None:
+        stream = torch.cuda.current_stream(W.device)
+    if stream.device != W.device:
+        raise ValueError(f"the stream is on {stream.device}, W on {W.device}")
     m, n = W.shape
     ld = -(-n // 16) * 16
-    codes = torch.empty((m, ld), dtype=torch.float8_e4m3fn, device=W.device)[:, :n]
-    scales = torch.empty((-(-m // _lib.FP8_BLOCK), -(-n // _lib.FP8_BLOCK)), dtype=torch.float32,
-                         device=W.device)
-    _lib.fp8_quantize_blocks(W, codes, scales, stream=stream)
+    with torch.cuda.stream(stream):  # (memory of another stream may still be in use there)
+        codes = torch.empty((m, ld), dtype=torch.float8_e4m3fn, device=W.device)[:, :n]
+        scales = torch.empty((-(-m // _lib.FP8_BLOCK), -(-n // _lib.FP8_BLOCK)),
+                             dtype=torch.float32, device=W.device)
+        _lib.fp8_quantize_blocks(W, codes, scales)
     return Fp8Layer(codes, scales)
 
 
