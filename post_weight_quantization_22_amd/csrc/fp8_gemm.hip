@@ -669,11 +669,12 @@ hipError_t launch_gemv(const GemvArgs& v, size_t lds, hipStream_t stream) {
 }
 
 // Few enough activations that every workgroup quantizes them itself, in at most 4
-// rounds of 32 blocks: no kernel before the product, whose launch costs about 2 us
-// (us, in one and in two kernels: 1 x 4096 x 4096 7.3 and 9.0, 4 x 4096 x 4096 9.7 and
-// 9.5, 7 x 4096 x 4096 12.0 and 9.9, 1 x 28672 x 8192 48 and 62).
+// rounds of 32 blocks of a token: no kernel before the product, whose launch costs about
+// 2 us (us, in one and in two kernels: 1 x 4096 x 4096 5.6 and 7.7, 4 x 4096 x 4096 8.0
+// and 8.2, 4 x 1024 x 4096 7.0 and 7.4, 1 x 8192 x 16384 29.7 and 32.2; but
+// 8 x 4096 x 2048 8.6 and 7.6, 16 x 2048 x 1024 13.1 and 8.1).
 bool quantizes_itself(int64_t tokens, int64_t n) {
-  return tokens <= 16 && tokens * ceil_div(n, (int64_t)kFp8Block) <= 128;
+  return tokens * ceil_div(n, (int64_t)kFp8Block * 4 * kGemvWaves) <= 4;
 }
 
 // How a product is cut: tile, and K splits where the tiles do not reach every CU.
