@@ -434,8 +434,9 @@ gptq_status fp8_quantize_blocks(const void* W, gptq_dtype wdt, int64_t m, int64_
  * h = silu(X Wg^T) * (X Wu^T), both products summed as in fp8_gemm and rounded to bf16:
  * the first half of a gated MLP block without its two products in memory; codes
  * apart from X.
- * Workspace (16-byte aligned): fp8_gemm_workspace_size,
- * fp8_linear_workspace_size, fp8_gated_gemm_workspace_size(tokens, m, n).
+ * Workspace (16-byte aligned, also where a call needs none of it):
+ * fp8_gemm_workspace_size, fp8_linear_workspace_size,
+ * fp8_gated_gemm_workspace_size(tokens, m, n).
  * ---------------------------------------------------------------------- */
 gptq_status fp8_gemm_workspace_size(int64_t tokens, int64_t m, int64_t n, size_t* bytes);
 gptq_status fp8_gemm(const uint8_t* X, int64_t tokens, int64_t n, int64_t ldx, const float* xs,
@@ -535,7 +536,8 @@ gptq_status kv_cache_read(const gptq_kv_cache* kc, const gptq_kv_cache* vc, cons
  * logprob -inf and entropy 0 (its alternatives: the lowest ids, -inf).  A row
  * that holds a NaN or +inf gives NaN throughout (ids rank NaN with -inf).
  * ids with logprob, and entropy, may be NULL; top_ids and top_logprobs when
- * top == 0.  Workspace: token_logprobs_workspace_size(tokens, vocab, top).
+ * top == 0.  Workspace (16-byte aligned, also where a call needs none of it):
+ * token_logprobs_workspace_size(tokens, vocab, top).
  * ---------------------------------------------------------------------- */
 gptq_status token_logprobs_workspace_size(int64_t tokens, int64_t vocab, int32_t top,
                                           size_t* bytes);

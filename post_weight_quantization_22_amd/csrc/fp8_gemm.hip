@@ -446,8 +446,9 @@ __global__ __launch_bounds__(WM * WT * 64) void fp8_gemm_tile_kernel(GemmArgs a)
 // weights and codes of its matrix operand straight into registers (segments q
 // and q + 4 of row l % 16 of the block: an instruction covers 64 bytes of 16
 // rows), D blocks ahead.  SRC says where the activations come from: codes in
-// memory, or bf16 / fp32 rows that the workgroup quantizes into LDS itself while
-// its first weights are on their way (few tokens: every workgroup repeats that).
+// memory, or bf16 / fp32 rows that the workgroup quantizes into LDS itself, each of its
+// loads waiting for those in front of it, the first weights' among them (few tokens:
+// every workgroup repeats that).
 // Measured: 16 x 8192 x 28672 49 us (4.8 TB/s of weights), 1 x 28672 x 8192 48 us with
 // the quantization (4.9), 1 x 4096 x 4096 6.2 us (2.7: launch and one round trip).
 constexpr int SRC_CODES = -1;

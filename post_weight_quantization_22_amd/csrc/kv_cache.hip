@@ -55,8 +55,9 @@ struct KvArgs {
   const int32_t* owner;  // writes: the token that each slot keeps, or null (search)
 };
 
-// x / d for 0 <= x < 2^22 by the reciprocal: (x + 1/2) / d is at least 1 / (2 d)
-// away from an integer, 2^-22 of the quotient or more, and rounds to it by less
+// x / d for 0 <= x < 2^21 + 2^10 (a token's lanes and a workgroup's) by the reciprocal:
+// (x + 1/2) / d is 1 / (2 d) or more from an integer, nearly 2^-22 of the quotient, and
+// the roundings of the reciprocal and the product move it by 2^-23 of itself at most
 __device__ __forceinline__ int small_div(int x, float recip) {
   return (int)(((float)x + 0.5f) * recip);
 }

@@ -16,8 +16,9 @@
 // tree, and the chunks with what each addition rounds off carried along, so the sums'
 // error does not grow with V (one term after another, 1024 equal ones, it is 2^-16).
 //
-// Bound by HBM: each logit is read once (2048 x 32000 fp32 in 57 us, 4.6 TB/s; few rows by
-// latency: 4 x 128000 7.8 us and 5.2 us to join the segments).
+// Bound by HBM: each logit is read once (2048 x 32000 fp32 in 51 us, 5.1 TB/s, with 5
+// alternatives 57; bf16 halves the bytes, not the sums' instructions: 34 and 40 us).  Few
+// rows by latency: 4 x 128000 7.9 us and 5.4 us to join the segments.
 // A workgroup of 256 takes a row (or a segment of it, where there are few rows; a
 // second kernel joins the segments).
 // A lane keeps (m, r, t) of its own logits and the place of its m.  The top
@@ -271,7 +272,7 @@ __device__ __forceinline__ Raw8<DT> load_chunk(const char* x, int64_t col, int64
 
 // A workgroup per row and segment.  Its chunks of 8 logits lie on 16-byte borders, the
 // first one beginning `off` places in front of the row (2048 x 50257 bf16, rows that start
-// on any border: 68 us; by loads of single logits 157).
+// on any border: 51 us; loads of single logits took 2.3 times as long).
 template <int DT>
 __global__ __launch_bounds__(kThreads) void logprobs_kernel(LpArgs a) {
   __shared__ Shared sh;

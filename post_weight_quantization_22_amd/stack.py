@@ -270,7 +270,9 @@ def quantize_stack_fp8(x0: torch.Tensor, weights: Sequence[Tuple[torch.Tensor, t
                                                                  torch.Tensor]],
                        chunk_tokens: int = 16384, stream=None
                        ) -> Tuple[List[Fp8Block], torch.Tensor]:
-    """Quantize every block of the stack to e4m3 and carry x0 (bf16 [tokens, d]) through it;
+    """Quantize every block of the stack to e4m3 and carry x0 (bf16 [tokens, d]) through it,
+    ``chunk_tokens`` at a time (a token does not depend on the others, but the order of
+    its fp32 sums does on a call's size, and a code where a sum lies on a border of it);
     returns the blocks and the quantized network's output activations."""
     if stream is None:
         stream = torch.cuda.current_stream(x0.device)
