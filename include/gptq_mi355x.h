@@ -38,7 +38,7 @@
 extern "C" {
 #endif
 
-#define GPTQ_ABI_VERSION 0x00020006u /* major 2, minor 6 */
+#define GPTQ_ABI_VERSION 0x00020007u /* major 2, minor 7 */
 
 typedef enum gptq_status {
   GPTQ_OK = 0,
@@ -545,6 +545,172 @@ gptq_status token_logprobs(const void* logits, gptq_dtype dt, int64_t tokens, in
                            int64_t ldl, const int64_t* ids, float* logprob, float* entropy,
                            int32_t top, int32_t* top_ids, float* top_logprobs, void* ws,
                            size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A paged cache of 8-bit codes with one scale per block of tokens and head --
+ * "LLM quantization principles", section 2.1 (q = round(x / scale)), with the max
+ * calibrator's scale ("AWQ, MinMax, GPTQ calibration in Model Optimizer", section
+ * 2) -- and the attention that reads it without writing it out.
+ *   GPTQ_KV_INT8: a code q stands for (q - 128) * scale, GPTQ_KV_E4M3: for code * scale.
+ * codes[pages][page_size][heads][head_dim] lie at
+ *   codes + page * page_stride + slot * slot_stride + head * head_stride (bytes),
+ * scales[pages][page_size / block][heads] at
+ *   page * param_page_stride + (slot / block) * param_block_stride + head * param_head_stride
+ * (elements), any order of pages, slots and heads.  head_dim: a multiple of 16, at most
+ * 256; block divides page_size; heads <= 4096; pages * page_size < 2^31; codes 16-byte
+ * aligned, strides multiples of 16 bytes; strides of dimensions longer than 1 are not 0.
+ * block = 1 also fits what kv_cache_write writes in INT8 without zeros or E4M3 with
+ * group_size -1.
+ *
+ * Sequences: table[seqs][width] (row stride ldt) lists each one's pages in order,
+ * lengths[seqs] their lengths with the call's new rows, starts[seqs + 1] (ascending)
+ * where their rows begin: row r of sequence i is row starts[i] + r of the call and
+ * stands at position lengths[i] - (starts[i + 1] - starts[i]) + r (rows at positions
+ * below 0 are left out of writes, and see no key).  Rows behind starts[seqs] are padding
+ * and neither read nor written.  A page number that a position needs and that is not a
+ * page (or a position past the table) is not accessed, and *info (a device int32 that the
+ * caller has cleared, may be NULL) becomes 1.  seqs <= tokens is not needed; a
+ * sequence may have no rows.
+ *
+ * kv_block_write: rows K, V [tokens][heads][head_dim] (strides in elements, fp32 or
+ * bf16) to their sequences' places in kb and vb (either may be NULL with its rows).  With a
+ * the largest finite |x| of a block's new rows of one head, need = max(RN32(a / 448),
+ * 2^-126) (E4M3) or max(RN32(2 a / 255), 2^-126) (INT8):
+ *   a block whose first position is written begins anew: scale = need, 1 where a = 0;
+ *   else its scale s stays where need <= s (or a = 0) and becomes s * 2^k with the
+ *   smallest k that covers need where not; the codes in front of the new rows are then
+ *   rounded to the new scale (ties to even).  (A scale there that is not a normal number
+ *   counts as never written.)
+ * Codes are the nearest to x / scale, ties to even (INT8: of the quotient rounded to
+ * fp32), at most the largest; E4M3: a non-finite x becomes the NaN code; INT8: an
+ * infinity the largest code of its sign, a NaN code 0.  Nothing else is written; rows behind a
+ * sequence's last one keep their bytes.  Blocks that are written belong to one sequence
+ * of the call.
+ *
+ * kv_block_attention: out[t][h] = sum_j w_j V_j, w = softmax_j(scale * Q[t][h] . K_j), over
+ * the keys j of t's sequence at positions 0 .. lengths[i] - 1; causal: those up to t's
+ * own position, and with window > 0 only the last `window` of them.  Query head h
+ * reads key head h / (q_heads / heads); q_heads a multiple of heads.  Q, out
+ * [tokens][q_heads][head_dim], both fp32 or both bf16; out apart from Q.  lse[tokens][q_heads]
+ * (may be NULL): the natural logarithm of the weights' denominator.  A row that sees no key is
+ * 0, its lse -inf.  Places that a row does not see do not reach it, whatever they hold.
+ * Products are those of the codes' values, summed in fp32; with bf16 rows the
+ * weights are rounded to bf16 before the second product, as Q came in bf16; with fp32 rows
+ * both hold 24 bits.  tokens * q_heads < 2^31.  Workspace (16-byte aligned, also where a call
+ * needs none of it): kv_block_attention_workspace_size.
+ * ---------------------------------------------------------------------- */
+typedef struct gptq_kv_blocks {
+  uint8_t* codes;
+  float* scales;
+  int64_t pages;
+  int64_t page_stride, slot_stride, head_stride;                    /* codes, bytes     */
+  int64_t param_page_stride, param_block_stride, param_head_stride; /* scales, elements */
+  int32_t page_size, block, heads, head_dim, format;
+} gptq_kv_blocks;
+
+gptq_status kv_block_write(const void* K, int64_t k_token_stride, int64_t k_head_stride,
+                           const void* V, int64_t v_token_stride, int64_t v_head_stride,
+                           gptq_dtype dt, int64_t tokens, const int32_t* table, int64_t ldt,
+                           int64_t width, const int32_t* lengths, const int32_t* starts,
+                           int64_t seqs, const gptq_kv_blocks* kb, const gptq_kv_blocks* vb,
+                           int32_t* info, hipStream_t stream);
+gptq_status kv_block_attention_workspace_size(const gptq_kv_blocks* kb, int32_t q_heads,
+                                              gptq_dtype dt, int64_t tokens, int64_t seqs,
+                                              int64_t width, size_t* bytes);
+gptq_status kv_block_attention(const void* Q, int64_t q_token_stride, int64_t q_head_stride,
+                               gptq_dtype dt, int64_t tokens, int32_t q_heads,
+                               const gptq_kv_blocks* kb, const gptq_kv_blocks* vb,
+                               const int32_t* table, int64_t ldt, int64_t width,
+                               const int32_t* lengths, const int32_t* starts, int64_t seqs,
+                               int32_t causal, int32_t window, float scale, void* out,
+                               int64_t o_token_stride, int64_t o_head_stride, float* lse,
+                               int32_t* info, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The pages of such caches: table[rows][width] (row stride ldt) and lengths[rows] as
+ * above, refs[pages] the number of holders of each page (0: free; a page may be held by
+ * others than the table's rows too).  A row of length n holds the first
+ * ceil(n / page_size) pages of its table row.  Everything stays on the device; *info
+ * (cleared by the caller, may be NULL) gets bit 0 where an input lies outside its range (it is
+ * left out), bit 1 where pages ran out.
+ *
+ * kv_pages_fork: new row i continues old row parents[i] (negative: an empty row): its pages
+ * and its length, pages behind its end -1; new_refs = refs with the new rows' holdings in the
+ * place of the old rows'.  No page is copied.  The outputs apart from the inputs.
+ * kv_pages_resize, in place: row i gets new_lengths[i] (negative: it stays as it is).
+ *   Pages behind a shorter end go back (entries become -1; 0 frees the row).  A row that grows gets
+ *   fresh pages, and where its last page is partly filled and held by others too, a page
+ *   of its own in the place of that one: src[i], dst[i] name the pair that has to be copied
+ *   before the row is written (-1, -1: none).  If all holders of a page grow in one call,
+ *   the last row keeps it.  Fresh pages are the lowest free ones (those that the call
+ *   gives back among them), rows in order, a row's own copy first.  If they do not suffice,
+ *   no row grows.  A length that the table row cannot hold is left out (bit 0).
+ *   Workspace (4-byte aligned): kv_pages_resize_workspace_size(rows, pages).
+ * kv_pages_compact: *count = pages in use (refs > 0); the k-th page in use behind the
+ *   first *count ones moves to the k-th free one among them: src[k], dst[k], -1 behind the last
+ *   pair (capacity entries, pages / 2 or more); new_table and new_refs name the pages
+ *   by their new places (entries that are no pages stay).  The outputs apart from the
+ *   inputs.  Workspace (4-byte aligned): kv_pages_compact_workspace_size(pages).
+ * kv_pages_copy: page dst[k] = page src[k] in each of n arrays, for every pair with both
+ *   not negative.  A page that is written is neither read nor written by another pair.  An array's page is
+ *   outer x inner rows of row_bytes, their strides in bytes.
+ * rows, new_rows, pages, pairs <= 2^24, rows * width < 2^30, pages * page_size < 2^31.
+ * ---------------------------------------------------------------------- */
+typedef struct gptq_page_array {
+  void* data;
+  int64_t pages, page_stride;
+  int64_t outer, outer_stride, inner, inner_stride, row_bytes;
+} gptq_page_array;
+
+gptq_status kv_pages_fork(const int32_t* table, int64_t ldt, const int32_t* lengths, int64_t rows,
+                          int64_t width, const int32_t* refs, int64_t pages,
+                          const int32_t* parents, int64_t new_rows, int32_t page_size,
+                          int32_t* new_table, int64_t ldn, int32_t* new_lengths,
+                          int32_t* new_refs, int32_t* info, hipStream_t stream);
+gptq_status kv_pages_resize_workspace_size(int64_t rows, int64_t pages, size_t* bytes);
+gptq_status kv_pages_resize(int32_t* table, int64_t ldt, int32_t* lengths, int64_t rows,
+                            int64_t width, int32_t* refs, int64_t pages,
+                            const int32_t* new_lengths, int32_t page_size, int32_t* src,
+                            int32_t* dst, int32_t* info, void* ws, size_t ws_bytes,
+                            hipStream_t stream);
+gptq_status kv_pages_compact_workspace_size(int64_t pages, size_t* bytes);
+gptq_status kv_pages_compact(const int32_t* table, int64_t ldt, int64_t rows, int64_t width,
+                             const int32_t* refs, int64_t pages, int32_t* new_table, int64_t ldn,
+                             int32_t* new_refs, int32_t* src, int32_t* dst, int64_t capacity,
+                             int32_t* count, void* ws, size_t ws_bytes, hipStream_t stream);
+gptq_status kv_pages_copy(const gptq_page_array* arrays, int64_t n, const int32_t* src,
+                          const int32_t* dst, int64_t pairs, int32_t* info, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Drafted tokens against the model that judges them -- a quantized model drafts, the
+ * full one verifies, and the tokens are distributed as if the full one had drawn each
+ * ("Quantized deployment, 1.5 TB to 250 GB", section 3.1, judges a quantized model by
+ * the same probabilities).  Sequence i has rows starts[i] .. starts[i + 1] - 1 (ascending,
+ * rows behind starts[seqs] are padding): ids[t] is the drafted token that row t judges;
+ * the last row judges none (its id is not used).  With p = softmax(target[t] / temperature)
+ * and q = softmax(draft[t] / temperature), or certainty of ids[t] where draft is NULL:
+ *   ids[t] is accepted while u[t] * q(ids[t]) < p(ids[t]);
+ *   the next token has the weights max(p - q, 0) behind a refusal (p if all are 0), p
+ *   behind the last row, and is the smallest v with C(v) > u_next[i] C(vocab - 1), C the
+ *   running sum of the weights.
+ * u[tokens], u_next[seqs] in [0, 1) (u_next: what lies outside counts as the nearest inside, a
+ * NaN as 0).  temperatures[seqs] (may be NULL: 1): 0 takes the
+ * largest logit (ties to the lower id) for the whole law; accepted is what equals it.
+ * accepted[seqs]: the accepted tokens; tokens_out[t]: they, then the next one, then -1;
+ * logprobs[t] (may be NULL): log p of tokens_out[t], 0 where that is -1 or the temperature 0.
+ * target, draft [tokens][vocab] (row strides ldt, ldd; fp32 or bf16 each).  -inf is a masked
+ * logit.  An id outside the vocabulary is refused, as is one whose rows hold a NaN or +inf or
+ * nothing but -inf; from such a target row nothing is drawn (-1).  Acceptance sums in fp32, the
+ * draw in fp64.  Workspace (16-byte aligned): verify_drafts_workspace_size(tokens, vocab, seqs).
+ * ---------------------------------------------------------------------- */
+gptq_status verify_drafts_workspace_size(int64_t tokens, int64_t vocab, int64_t seqs,
+                                         size_t* bytes);
+gptq_status verify_drafts(const void* target, gptq_dtype tdt, int64_t ldt, const void* draft,
+                          gptq_dtype ddt, int64_t ldd, int64_t tokens, int64_t vocab,
+                          const int64_t* ids, const int32_t* starts, int64_t seqs, const float* u,
+                          const float* u_next, const float* temperatures, int32_t* accepted,
+                          int64_t* tokens_out, float* logprobs, void* ws, size_t ws_bytes,
+                          hipStream_t stream);
 
 #ifdef __cplusplus
 }

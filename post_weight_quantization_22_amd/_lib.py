@@ -68,6 +68,17 @@ EXPORTED = (
     "kv_cache_read",
     "token_logprobs_workspace_size",
     "token_logprobs",
+    "kv_block_write",
+    "kv_block_attention_workspace_size",
+    "kv_block_attention",
+    "kv_pages_fork",
+    "kv_pages_resize_workspace_size",
+    "kv_pages_resize",
+    "kv_pages_compact_workspace_size",
+    "kv_pages_compact",
+    "kv_pages_copy",
+    "verify_drafts_workspace_size",
+    "verify_drafts",
 )
 
 FP8_BLOCK = 128  # columns (and weight rows) that share a scale
@@ -110,6 +121,43 @@ class GPTQKVCache(ctypes.Structure):
         ("head_dim", ctypes.c_int32),
         ("group_size", ctypes.c_int32),
         ("format", ctypes.c_int32),
+    ]
+
+
+class GPTQKVBlocks(ctypes.Structure):
+    """A paged cache of 8-bit codes with a scale per block of tokens and head
+    (make_kv_blocks builds one); it keeps its tensors alive."""
+
+    _fields_ = [
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("pages", ctypes.c_int64),
+        ("page_stride", ctypes.c_int64),
+        ("slot_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("param_page_stride", ctypes.c_int64),
+        ("param_block_stride", ctypes.c_int64),
+        ("param_head_stride", ctypes.c_int64),
+        ("page_size", ctypes.c_int32),
+        ("block", ctypes.c_int32),
+        ("heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("format", ctypes.c_int32),
+    ]
+
+
+class GPTQPageArray(ctypes.Structure):
+    """One of the arrays whose pages kv_pages_copy copies (strides in bytes)."""
+
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("pages", ctypes.c_int64),
+        ("page_stride", ctypes.c_int64),
+        ("outer", ctypes.c_int64),
+        ("outer_stride", ctypes.c_int64),
+        ("inner", ctypes.c_int64),
+        ("inner_stride", ctypes.c_int64),
+        ("row_bytes", ctypes.c_int64),
     ]
 
 
@@ -233,6 +281,36 @@ def load() -> ctypes.CDLL:
     lib.token_logprobs.restype = _i32
     lib.token_logprobs.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _i32, _vp, _vp, _vp,
                                    _sz, _vp]
+    lib.kv_block_write.restype = _i32
+    lib.kv_block_write.argtypes = [_vp, _i64, _i64, _vp, _i64, _i64, _i32, _i64, _vp, _i64, _i64, _vp,
+                                   _vp, _i64, _vp, _vp, _vp, _vp]
+    lib.kv_block_attention_workspace_size.restype = _i32
+    lib.kv_block_attention_workspace_size.argtypes = [_vp, _i32, _i32, _i64, _i64, _i64,
+                                                      ctypes.POINTER(_sz)]
+    lib.kv_block_attention.restype = _i32
+    lib.kv_block_attention.argtypes = [_vp, _i64, _i64, _i32, _i64, _i32, _vp, _vp, _vp, _i64, _i64,
+                                       _vp, _vp, _i64, _i32, _i32, ctypes.c_float, _vp, _i64, _i64,
+                                       _vp, _vp, _vp, _sz, _vp]
+    lib.kv_pages_fork.restype = _i32
+    lib.kv_pages_fork.argtypes = [_vp, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _i64,
+                                  _vp, _vp, _vp, _vp]
+    lib.kv_pages_resize_workspace_size.restype = _i32
+    lib.kv_pages_resize_workspace_size.argtypes = [_i64, _i64, ctypes.POINTER(_sz)]
+    lib.kv_pages_resize.restype = _i32
+    lib.kv_pages_resize.argtypes = [_vp, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i32, _vp, _vp, _vp,
+                                    _vp, _sz, _vp]
+    lib.kv_pages_compact_workspace_size.restype = _i32
+    lib.kv_pages_compact_workspace_size.argtypes = [_i64, ctypes.POINTER(_sz)]
+    lib.kv_pages_compact.restype = _i32
+    lib.kv_pages_compact.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64,
+                                     _vp, _vp, _sz, _vp]
+    lib.kv_pages_copy.restype = _i32
+    lib.kv_pages_copy.argtypes = [_vp, _i64, _vp, _vp, _i64, _vp, _vp]
+    lib.verify_drafts_workspace_size.restype = _i32
+    lib.verify_drafts_workspace_size.argtypes = [_i64, _i64, _i64, ctypes.POINTER(_sz)]
+    lib.verify_drafts.restype = _i32
+    lib.verify_drafts.argtypes = [_vp, _i32, _i64, _vp, _i32, _i64, _i64, _i64, _vp, _vp, _i64, _vp,
+                                  _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
     _lib = lib
     return lib
 
@@ -680,13 +758,17 @@ _KIND = {}
 _FLOAT = {"b": GPTQ_BF16, "f": GPTQ_F32}
 
 
-def _on_gpu(t, name: str):
-    """The device of an operand, which has to be a GPU."""
+def _kinds() -> None:
     if not _KIND:
         import torch
 
         _KIND.update({torch.bfloat16: "b", torch.float32: "f", torch.float8_e4m3fn: "8",
                       torch.uint8: "u", torch.int64: "l", torch.int32: "i"})
+
+
+def _on_gpu(t, name: str):
+    """The device of an operand, which has to be a GPU."""
+    _kinds()
     d = t.device
     if d.type != "cuda":
         raise ValueError(f"{name} is on {d}, expected a GPU tensor")
@@ -705,7 +787,8 @@ def _plane(t, name: str, rows: int, cols: int, kinds: str, device, exact: str = 
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     shape, stride = t.shape, t.stride()
-    if len(shape) != 2 or shape[0] < rows or shape[1] < cols or (stride[1] != 1 and shape[1] > 1):
+    if (len(shape) != 2 or shape[0] < rows or shape[1] < cols
+            or (stride[1] != 1 and shape[1] > 1 and shape[0] > 0)):
         raise ValueError(f"{name}: expected a 2-D tensor of at least {rows} x {cols} with unit "
                          f"column stride, got shape {tuple(shape)} strides {stride}")
     if exact and (("r" in exact and shape[0] != rows) or ("c" in exact and shape[1] != cols)):
@@ -1029,3 +1112,315 @@ def token_logprobs(logits, ids, logprob, entropy=None, top_ids=None, top_logprob
     _launch("token_logprobs", d, stream, logits.data_ptr(), _FLOAT[_KIND[logits.dtype]], tokens,
             vocab, ldl, _ptr(ids), _ptr(logprob), _ptr(entropy), top, _ptr(top_ids), _ptr(top_logprobs),
             p, nbytes)
+
+
+# ---------------------------------------------------------------------------
+# The cache with a scale per block of tokens and head, its pages, drafted tokens
+# ---------------------------------------------------------------------------
+def make_kv_blocks(codes, scales, fmt: str = "e4m3") -> GPTQKVBlocks:
+    """The handle of a paged cache of keys or of values with one scale per block of tokens and
+    head.
+
+    codes: uint8 (or e4m3) [pages, page_size, heads, head_dim]; scales: fp32 [pages, blocks, heads], each
+    for page_size / blocks tokens.  fmt: "e4m3" or "int8" (a code q stands for (q - 128) * scale).
+    Pages, slots and heads may lie in any order; the last dimension of codes is dense, its
+    rows 16-byte aligned."""
+    if fmt not in ("int8", "e4m3"):
+        raise ValueError(f"fmt: {fmt!r}, expected 'int8' or 'e4m3'")
+    d = _on_gpu(codes, "codes")
+    if _KIND.get(codes.dtype) not in ("u", "8"):
+        raise TypeError(f"codes: unsupported dtype {codes.dtype}")
+    if _KIND.get(scales.dtype) != "f":
+        raise TypeError(f"scales: dtype {scales.dtype}, expected float32")
+    if scales.device != d:
+        raise ValueError(f"scales is on {scales.device}, expected {d}")
+    shape, cs, ps = codes.shape, codes.stride(), scales.stride()
+    if len(shape) != 4 or (cs[3] != 1 and shape[3] > 1):
+        raise ValueError(f"codes: shape {tuple(shape)} strides {cs}, expected "
+                         "[pages, page_size, heads, head_dim] with a dense last dimension")
+    pages, page_size, heads, head_dim = shape
+    if (scales.dim() != 3 or scales.shape[0] != pages or scales.shape[2] != heads
+            or scales.shape[1] == 0 or page_size % scales.shape[1] != 0):
+        raise ValueError(f"scales: shape {tuple(scales.shape)}, expected ({pages}, blocks, {heads}) "
+                         f"with blocks a divisor of {page_size}")
+    c = GPTQKVBlocks(codes.data_ptr(), scales.data_ptr(), pages, cs[0], cs[1], cs[2], ps[0], ps[1],
+                     ps[2], page_size, page_size // scales.shape[1], heads, head_dim,
+                     _KV_FORMATS[fmt])
+    c.tensors = (codes, scales)
+    c.device = d
+    c.row = (heads, head_dim)
+    c.key = (pages, page_size, c.block, heads, head_dim, c.format)
+    c.ref = ctypes.addressof(c)
+    return c
+
+
+def _kv_sequences(table, lengths, starts, device):
+    """(table, ldt, width, lengths, starts, seqs) of a call's sequences."""
+    if table.dim() != 2:
+        raise ValueError(f"table: shape {tuple(table.shape)}, expected [seqs, width]")
+    seqs, width = table.shape
+    ldt = _plane(table, "table", seqs, width, "i", device)
+    _vector(lengths, "lengths", seqs, "i", device, optional=False)
+    _vector(starts, "starts", seqs + 1, "i", device, optional=False)
+    if lengths.numel() != seqs or starts.numel() != seqs + 1:
+        raise ValueError(f"lengths, starts: {lengths.numel()} and {starts.numel()} elements, expected "
+                         f"{seqs} and {seqs + 1}")
+    return table.data_ptr(), ldt, width, lengths.data_ptr(), starts.data_ptr(), seqs
+
+
+def _info(info, device):
+    if info is not None:
+        _buf(info, "info", (1,), ("int32",), device)
+    return _ptr(info)
+
+
+def kv_block_write(K, V, kb, vb, table, lengths, starts, info=None, stream=None) -> None:
+    """Quantize the new rows K, V [tokens, heads, head_dim] (bf16 or fp32) of the sequences into
+    their blocks of kb and vb (either may be None with its rows).
+
+    table [seqs, width], lengths [seqs] (with the new rows), starts [seqs + 1] (each int32):
+    rows starts[i] .. starts[i + 1] - 1 stand at the last positions of sequence i."""
+    rows = K if K is not None else V
+    if rows is None or (kb is None and vb is None):
+        raise ValueError("keys with their cache or values with theirs are required")
+    d = _on_gpu(rows, "K" if K is not None else "V")
+    dt = _FLOAT.get(_KIND.get(rows.dtype))
+    if dt is None:
+        raise TypeError(f"rows: dtype {rows.dtype}, expected bfloat16 or float32")
+    tokens = rows.shape[0]
+    kp, kt, kh = _kv_rows(K, "K", kb, tokens, d, rows.dtype)
+    vp, vt, vh = _kv_rows(V, "V", vb, tokens, d, rows.dtype)
+    if kb is not None and vb is not None and kb.key != vb.key:
+        raise ValueError("the two caches differ in pages, block, rows or format")
+    s = _kv_sequences(table, lengths, starts, d)
+    _launch("kv_block_write", d, stream, kp, kt, kh, vp, vt, vh, dt, tokens, *s,
+            None if kb is None else kb.ref, None if vb is None else vb.ref, _info(info, d))
+
+
+def kv_block_attention_workspace_size(kb: GPTQKVBlocks, q_heads: int, dtype, tokens: int, seqs: int,
+                                      width: int) -> int:
+    """dtype: the queries' torch dtype; width: entries of a table row."""
+    _kinds()
+    return _attention_space(kb, q_heads, _FLOAT[_KIND[dtype]], tokens, seqs, width)
+
+
+def _attention_space(kb, q_heads, dt, tokens, seqs, width) -> int:
+    """The query, remembered with the cache's handle."""
+    key = (q_heads, dt, tokens, seqs, width)
+    known = kb.__dict__.setdefault("spaces", {})
+    need = known.get(key)
+    if need is None:
+        out = _sz(0)
+        _check(load().kv_block_attention_workspace_size(kb.ref, *key, ctypes.byref(out)),
+               "kv_block_attention_workspace_size")
+        if len(known) >= 1024:
+            known.clear()
+        need = known[key] = out.value
+    return need
+
+
+def kv_block_attention(Q, kb, vb, table, lengths, starts, out, lse=None, causal: bool = True,
+                       window: int = 0, scale: Optional[float] = None, info=None, ws=None,
+                       stream=None) -> None:
+    """out[tokens, q_heads, head_dim] = attention of the sequences' new rows Q (both bf16 or both
+    fp32) to their cached keys and values; table, lengths and starts as in kv_block_write (the
+    lengths hold the new rows, whose keys and values are written before).
+
+    causal: a row sees its own position and those before it, with ``window`` > 0 only the last
+    ``window`` of them; else all of its sequence.  scale: head_dim ** -0.5 unless given.
+    lse[tokens, q_heads] (fp32): the logarithm of each row's denominator."""
+    d = _on_gpu(Q, "Q")
+    dt = _FLOAT.get(_KIND.get(Q.dtype))
+    if dt is None:
+        raise TypeError(f"Q: dtype {Q.dtype}, expected bfloat16 or float32")
+    if kb is None or vb is None:
+        raise ValueError("both caches are required")
+    if kb.key != vb.key:
+        raise ValueError("the two caches differ in pages, block, rows or format")
+    if kb.device != d or vb.device != d:
+        raise ValueError(f"caches on {kb.device} and {vb.device}, expected {d}")
+    heads, dim = kb.row
+    shape, qs = Q.shape, Q.stride()
+    if len(shape) != 3 or shape[2] != dim or shape[1] == 0 or shape[1] % heads or qs[2] != 1:
+        raise ValueError(f"Q: shape {tuple(shape)} strides {qs}, expected [tokens, a multiple of "
+                         f"{heads}, {dim}] with a dense last dimension")
+    tokens, q_heads = shape[:2]
+    if out.dtype is not Q.dtype:
+        raise TypeError(f"out: dtype {out.dtype}, expected {Q.dtype}")
+    os_ = out.stride()
+    if out.shape != shape or os_[2] != 1 or out.device != d:
+        raise ValueError(f"out: shape {tuple(out.shape)} strides {os_} on {out.device}, expected "
+                         f"{tuple(shape)} with a dense last dimension on {d}")
+    _vector(lse, "lse", tokens * q_heads, "f", d)
+    s = _kv_sequences(table, lengths, starts, d)
+    p, nbytes, ws = _space(_attention_space(kb, q_heads, dt, tokens, s[5], s[2]), ws, d, stream)
+    _launch("kv_block_attention", d, stream, Q.data_ptr(), qs[0], qs[1], dt, tokens, q_heads, kb.ref,
+            vb.ref, *s, 1 if causal else 0, window, dim ** -0.5 if scale is None else scale,
+            out.data_ptr(), os_[0], os_[1], _ptr(lse), _info(info, d), p, nbytes)
+
+
+def kv_pages_fork(table, lengths, refs, parents, page_size: int, new_table, new_lengths, new_refs,
+                  info=None, stream=None) -> None:
+    """Row i of new_table, new_lengths continues row parents[i] (negative: an empty row) of table
+    [rows, width], lengths [rows]; new_refs[pages] counts the pages' holders from then on.  All
+    int32.  No page is copied: kv_pages_resize does so where a shared page is written."""
+    d = _on_gpu(table, "table")
+    if table.dim() != 2 or new_table.dim() != 2:
+        raise ValueError("table, new_table: expected [rows, width]")
+    rows, width = table.shape
+    new_rows = new_table.shape[0]
+    ldt = _plane(table, "table", rows, width, "i", d)
+    ldn = _plane(new_table, "new_table", new_rows, width, "i", d, "c")
+    pages = refs.numel()
+    for t, name, n in ((lengths, "lengths", rows), (parents, "parents", new_rows),
+                       (new_lengths, "new_lengths", new_rows), (refs, "refs", pages),
+                       (new_refs, "new_refs", pages)):
+        _vector(t, name, n, "i", d, optional=False)
+    _launch("kv_pages_fork", d, stream, table.data_ptr(), ldt, lengths.data_ptr(), rows, width,
+            refs.data_ptr(), pages, parents.data_ptr(), new_rows, page_size, new_table.data_ptr(),
+            ldn, new_lengths.data_ptr(), new_refs.data_ptr(), _info(info, d))
+
+
+def kv_pages_resize_workspace_size(rows: int, pages: int) -> int:
+    return _size_of("kv_pages_resize_workspace_size", rows, pages)
+
+
+def kv_pages_resize(table, lengths, refs, new_lengths, page_size: int, src, dst, info=None, ws=None,
+                    stream=None) -> None:
+    """Rows of table [rows, width] get new_lengths[rows] (negative: left as they are), in place:
+    pages behind shorter ends are given back, longer rows get the lowest free pages, and a shared
+    last page that a row grows in is replaced by one of its own: page src[i] has to be
+    copied to dst[i] (both -1: none) by kv_pages_copy.  All int32; info: 2 where pages ran out (no
+    row has grown)."""
+    d = _on_gpu(table, "table")
+    if table.dim() != 2:
+        raise ValueError("table: expected [rows, width]")
+    rows, width = table.shape
+    ldt = _plane(table, "table", rows, width, "i", d)
+    pages = refs.numel()
+    for t, name, n in ((lengths, "lengths", rows), (new_lengths, "new_lengths", rows),
+                       (src, "src", rows), (dst, "dst", rows), (refs, "refs", pages)):
+        _vector(t, name, n, "i", d, optional=False)
+    p, nbytes, ws = _space(kv_pages_resize_workspace_size(rows, pages), ws, d, stream)
+    _launch("kv_pages_resize", d, stream, table.data_ptr(), ldt, lengths.data_ptr(), rows, width,
+            refs.data_ptr(), pages, new_lengths.data_ptr(), page_size, src.data_ptr(),
+            dst.data_ptr(), _info(info, d), p, nbytes)
+
+
+def kv_pages_compact_workspace_size(pages: int) -> int:
+    return _size_of("kv_pages_compact_workspace_size", pages)
+
+
+def kv_pages_compact(table, refs, new_table, new_refs, src, dst, count, ws=None, stream=None) -> None:
+    """The pages in use move to the front of the cache: count[1] of them, src and dst (pages // 2
+    entries or more, -1 behind the last pair) the pairs that kv_pages_copy has to copy, new_table
+    and new_refs the table and holders with the pages' new places.  All int32."""
+    d = _on_gpu(table, "table")
+    if table.dim() != 2:
+        raise ValueError("table: expected [rows, width]")
+    rows, width = table.shape
+    ldt = _plane(table, "table", rows, width, "i", d)
+    ldn = _plane(new_table, "new_table", rows, width, "i", d, "rc")
+    pages = refs.numel()
+    capacity = src.numel()
+    for t, name, n in ((refs, "refs", pages), (new_refs, "new_refs", pages), (src, "src", pages // 2),
+                       (dst, "dst", capacity), (count, "count", 1)):
+        _vector(t, name, n, "i", d, optional=False)
+    p, nbytes, ws = _space(kv_pages_compact_workspace_size(pages), ws, d, stream)
+    _launch("kv_pages_compact", d, stream, table.data_ptr(), ldt, rows, width, refs.data_ptr(), pages,
+            new_table.data_ptr(), ldn, new_refs.data_ptr(), src.data_ptr(), dst.data_ptr(), capacity,
+            count.data_ptr(), p, nbytes)
+
+
+def _page_arrays(cache):
+    """The arrays of a cache's handle, as kv_pages_copy takes them."""
+    known = cache.__dict__.get("arrays")
+    if known is None:
+        known = []
+        for t in cache.tensors:
+            if t is None:
+                continue
+            size, shape, stride = t.element_size(), list(t.shape[1:]), list(t.stride()[1:])
+            # dimensions that lie one behind the other are one
+            rows = [(shape[-1], stride[-1] * size)]
+            if rows[0][0] == 1 or rows[0][1] == size:
+                run = shape[-1] * size
+                rows = []
+            else:
+                run = size
+            for n, s in zip(reversed(shape[:-1]), reversed(stride[:-1])):
+                if n == 1:
+                    continue
+                if not rows and s * size == run:
+                    run *= n
+                elif rows and s * size == rows[-1][0] * rows[-1][1]:
+                    rows[-1] = (rows[-1][0] * n, rows[-1][1])
+                else:
+                    rows.append((n, s * size))
+            while len(rows) < 2:
+                rows.append((1, 0))
+            if len(rows) > 2:
+                raise ValueError("kv_pages_copy: a cache whose pages lie in more than three runs of strides")
+            known.append(GPTQPageArray(t.data_ptr(), t.shape[0], t.stride(0) * size, rows[1][0],
+                                       rows[1][1], rows[0][0], rows[0][1], run))
+        cache.arrays = known
+    return known
+
+
+def kv_pages_copy(caches, src, dst, info=None, stream=None) -> None:
+    """Page dst[k] = page src[k] (int32, negative: no pair) in every one of ``caches`` (handles of
+    make_kv_blocks or make_kv_cache, any number: keys and values of all layers in one call)."""
+    d = _on_gpu(src, "src")
+    pairs = src.numel()
+    _vector(src, "src", pairs, "i", d, optional=False)
+    _vector(dst, "dst", pairs, "i", d, optional=False)
+    if dst.numel() != pairs:
+        raise ValueError(f"dst: {dst.numel()} elements, expected {pairs}")
+    arrays = []
+    for c in caches:
+        if c.device != d:
+            raise ValueError(f"a cache is on {c.device}, expected {d}")
+        arrays += _page_arrays(c)
+    call = (GPTQPageArray * len(arrays))(*arrays)
+    _launch("kv_pages_copy", d, stream, ctypes.addressof(call), len(arrays), src.data_ptr(),
+            dst.data_ptr(), pairs, _info(info, d))
+
+
+def verify_drafts_workspace_size(tokens: int, vocab: int, seqs: int) -> int:
+    return _size_of("verify_drafts_workspace_size", tokens, vocab, seqs)
+
+
+def verify_drafts(target, draft, ids, starts, u, u_next, accepted, tokens, logprobs=None,
+                  temperatures=None, ws=None, stream=None) -> None:
+    """Accept or refuse drafted tokens by the target's logits target[rows, vocab] (bf16 or fp32) and
+    the drafter's, draft (the same shape; None: each drafted token was certain), and draw each
+    sequence's next token.
+
+    Sequence i has rows starts[i] .. starts[i + 1] - 1 (int32): row t judges ids[t] (int64), the last
+    one of a sequence judges none.  u[rows], u_next[seqs] (fp32): numbers in [0, 1).  accepted[seqs] (int32)
+    counts the accepted tokens, tokens[rows] (int64) holds them, the drawn one behind them,
+    then -1; logprobs[rows] (fp32) their log probabilities.  temperatures[seqs] (fp32): 0 takes the
+    largest logit."""
+    if target.dim() != 2:
+        raise ValueError(f"target: shape {tuple(target.shape)}, expected [rows, vocab]")
+    rows, vocab = target.shape
+    d = _on_gpu(target, "target")
+    ldt = _plane(target, "target", rows, vocab, "bf", d)
+    ddt = ldd = 0
+    if draft is not None:
+        ldd = _plane(draft, "draft", rows, vocab, "bf", d, "rc")
+        ddt = _FLOAT[_KIND[draft.dtype]]
+    seqs = starts.numel() - 1
+    if seqs < 0:
+        raise ValueError("starts: expected [seqs + 1]")
+    for t, name, n, kind in ((ids, "ids", rows, "l"), (starts, "starts", seqs + 1, "i"),
+                             (u, "u", rows, "f"), (u_next, "u_next", seqs, "f"),
+                             (accepted, "accepted", seqs, "i"), (tokens, "tokens", rows, "l")):
+        _vector(t, name, n, kind, d, optional=False)
+    _vector(logprobs, "logprobs", rows, "f", d)
+    _vector(temperatures, "temperatures", seqs, "f", d)
+    p, nbytes, ws = _space(verify_drafts_workspace_size(rows, vocab, seqs), ws, d, stream)
+    _launch("verify_drafts", d, stream, target.data_ptr(), _FLOAT[_KIND[target.dtype]], ldt,
+            _ptr(draft), ddt, ldd, rows, vocab, ids.data_ptr(), starts.data_ptr(), seqs,
+            u.data_ptr(), u_next.data_ptr(), _ptr(temperatures), accepted.data_ptr(),
+            tokens.data_ptr(), _ptr(logprobs), p, nbytes)

@@ -87,6 +87,52 @@ gptq_status kv_call_ok(const void* K, const void* V, int dt, int64_t tokens, con
   return GPTQ_OK;
 }
 
+gptq_status kv_blocks_ok(const gptq_kv_blocks* c) {
+  if (!c || !c->codes || !c->scales || c->pages <= 0 || c->page_size <= 0 || c->block <= 0 ||
+      c->heads <= 0 || c->head_dim <= 0 || c->page_size % c->block != 0 ||
+      (c->format != GPTQ_KV_INT8 && c->format != GPTQ_KV_E4M3))
+    return GPTQ_ERR_INVALID_ARG;
+  if (c->head_dim % 16 != 0 || c->head_dim > 256 || c->heads > 4096 ||
+      c->pages > INT32_MAX / c->page_size)
+    return GPTQ_ERR_UNSUPPORTED;
+  // an expanded dimension would have two places share their bytes
+  if ((c->pages > 1 && (c->page_stride <= 0 || c->param_page_stride <= 0)) ||
+      (c->page_size > 1 && c->slot_stride <= 0) ||
+      (c->page_size > c->block && c->param_block_stride <= 0) ||
+      (c->heads > 1 && (c->head_stride <= 0 || c->param_head_stride <= 0)))
+    return GPTQ_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(c->codes) & 15) != 0 || (c->page_stride & 15) != 0 ||
+      (c->slot_stride & 15) != 0 || (c->head_stride & 15) != 0 ||
+      (reinterpret_cast<uintptr_t>(c->scales) & 3) != 0)
+    return GPTQ_ERR_INVALID_ARG;
+  return GPTQ_OK;
+}
+
+// two caches of one call: the same pages and rows
+bool kv_blocks_alike(const gptq_kv_blocks* a, const gptq_kv_blocks* b) {
+  return a->pages == b->pages && a->page_size == b->page_size && a->block == b->block &&
+         a->heads == b->heads && a->head_dim == b->head_dim && a->format == b->format;
+}
+
+gptq_status kv_sequences_ok(const KvSequences& q) {
+  if (q.tokens < 0 || bad_dim(q.tokens) || q.seqs < 0 || bad_dim(q.seqs) || q.width < 0 ||
+      bad_dim(q.width))
+    return GPTQ_ERR_INVALID_ARG;
+  if (q.tokens == 0 || q.seqs == 0) return GPTQ_OK;
+  if (!q.table || !q.lengths || !q.starts || q.width == 0 || q.ldt < q.width)
+    return GPTQ_ERR_INVALID_ARG;
+  return GPTQ_OK;
+}
+
+// tables of pages: their sizes
+gptq_status pages_ok(int64_t rows, int64_t width, int64_t pages, int32_t page_size) {
+  if (rows < 0 || width <= 0 || pages <= 0 || page_size <= 0) return GPTQ_ERR_INVALID_ARG;
+  if (bad_dim(rows) || bad_dim(pages) || bad_dim(width) || pages > INT32_MAX / page_size ||
+      rows >= (int64_t(1) << 30) / width)
+    return GPTQ_ERR_UNSUPPORTED;
+  return GPTQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -568,6 +614,195 @@ gptq_status token_logprobs(const void* logits, gptq_dtype dt, int64_t tokens, in
   if ((reinterpret_cast<uintptr_t>(ws) & 15) != 0) return GPTQ_ERR_INVALID_ARG;
   return hip_status(launch_logprobs(logits, dt, tokens, vocab, ldl, ids, logprob, entropy, top,
                                     top_ids, top_logprobs, ws, stream));
+}
+
+gptq_status kv_block_write(const void* K, int64_t k_token_stride, int64_t k_head_stride,
+                           const void* V, int64_t v_token_stride, int64_t v_head_stride,
+                           gptq_dtype dt, int64_t tokens, const int32_t* table, int64_t ldt,
+                           int64_t width, const int32_t* lengths, const int32_t* starts,
+                           int64_t seqs, const gptq_kv_blocks* kb, const gptq_kv_blocks* vb,
+                           int32_t* info, hipStream_t stream) {
+  const KvSequences q{table, ldt, width, lengths, starts, seqs, tokens};
+  if (!valid_dtype(dt) || (!kb && !vb)) return GPTQ_ERR_INVALID_ARG;
+  for (const gptq_kv_blocks* c : {kb, vb})
+    if (c) {
+      const gptq_status ok = kv_blocks_ok(c);
+      if (ok != GPTQ_OK) return ok;
+    }
+  // (one cache for both: keys and values would race for its places)
+  if (kb && vb && (!kv_blocks_alike(kb, vb) || kb->codes == vb->codes || kb->scales == vb->scales))
+    return GPTQ_ERR_INVALID_ARG;
+  const gptq_status ok = kv_sequences_ok(q);
+  if (ok != GPTQ_OK || tokens == 0 || seqs == 0) return ok;
+  if ((K != nullptr) != (kb != nullptr) || (V != nullptr) != (vb != nullptr) ||
+      k_token_stride < 0 || k_head_stride < 0 || v_token_stride < 0 || v_head_stride < 0)
+    return GPTQ_ERR_INVALID_ARG;
+  const KvRows k{const_cast<void*>(K), k_token_stride, k_head_stride};
+  const KvRows v{const_cast<void*>(V), v_token_stride, v_head_stride};
+  return hip_status(launch_kv_block_write(k, v, dt, q, kb, vb, info, stream));
+}
+
+gptq_status kv_block_attention_workspace_size(const gptq_kv_blocks* kb, int32_t q_heads,
+                                              gptq_dtype dt, int64_t tokens, int64_t seqs,
+                                              int64_t width, size_t* bytes) {
+  if (!bytes || !valid_dtype(dt) || tokens < 0 || bad_dim(tokens) || seqs < 0 || bad_dim(seqs) ||
+      width < 0 || bad_dim(width))
+    return GPTQ_ERR_INVALID_ARG;
+  const gptq_status ok = kv_blocks_ok(kb);
+  if (ok != GPTQ_OK) return ok;
+  if (q_heads <= 0 || q_heads % kb->heads != 0) return GPTQ_ERR_INVALID_ARG;
+  if (tokens * q_heads > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
+  *bytes = tokens == 0 || seqs == 0 ? 0 : kv_attention_ws_bytes(kb, q_heads, dt, tokens, seqs, width);
+  return GPTQ_OK;
+}
+
+gptq_status kv_block_attention(const void* Q, int64_t q_token_stride, int64_t q_head_stride,
+                               gptq_dtype dt, int64_t tokens, int32_t q_heads,
+                               const gptq_kv_blocks* kb, const gptq_kv_blocks* vb,
+                               const int32_t* table, int64_t ldt, int64_t width,
+                               const int32_t* lengths, const int32_t* starts, int64_t seqs,
+                               int32_t causal, int32_t window, float scale, void* out,
+                               int64_t o_token_stride, int64_t o_head_stride, float* lse,
+                               int32_t* info, void* ws, size_t ws_bytes, hipStream_t stream) {
+  const KvSequences q{table, ldt, width, lengths, starts, seqs, tokens};
+  size_t need = 0;
+  gptq_status ok = kv_block_attention_workspace_size(kb, q_heads, dt, tokens, seqs, width, &need);
+  if (ok != GPTQ_OK) return ok;
+  ok = kv_blocks_ok(vb);
+  if (ok != GPTQ_OK) return ok;
+  if (!kv_blocks_alike(kb, vb) || (causal != 0 && causal != 1) || window < 0 ||
+      (window > 0 && !causal) || !std::isfinite(scale))
+    return GPTQ_ERR_INVALID_ARG;
+  ok = kv_sequences_ok(q);
+  if (ok != GPTQ_OK || tokens == 0 || seqs == 0) return ok;
+  if (!Q || !out || out == Q || q_token_stride < 0 || q_head_stride < 0 ||
+      (tokens > 1 && o_token_stride <= 0) || (q_heads > 1 && o_head_stride <= 0))
+    return GPTQ_ERR_INVALID_ARG;
+  ok = check_ws(ws, ws_bytes, need);
+  if (ok != GPTQ_OK) return ok;
+  if ((reinterpret_cast<uintptr_t>(ws) & 15) != 0) return GPTQ_ERR_INVALID_ARG;
+  KvAttention t;
+  t.q = KvRows{const_cast<void*>(Q), q_token_stride, q_head_stride};
+  t.out = KvRows{out, o_token_stride, o_head_stride};
+  t.lse = lse;
+  t.dt = dt; t.q_heads = q_heads; t.causal = causal; t.window = window; t.scale = scale;
+  return hip_status(launch_kv_attention(t, q, kb, vb, info, ws, stream));
+}
+
+gptq_status kv_pages_fork(const int32_t* table, int64_t ldt, const int32_t* lengths, int64_t rows,
+                          int64_t width, const int32_t* refs, int64_t pages,
+                          const int32_t* parents, int64_t new_rows, int32_t page_size,
+                          int32_t* new_table, int64_t ldn, int32_t* new_lengths,
+                          int32_t* new_refs, int32_t* info, hipStream_t stream) {
+  gptq_status ok = pages_ok(rows, width, pages, page_size);
+  if (ok == GPTQ_OK) ok = pages_ok(new_rows, width, pages, page_size);
+  if (ok != GPTQ_OK) return ok;
+  if (!refs || !new_refs || refs == new_refs ||
+      (rows > 0 && (!table || !lengths || (rows > 1 && ldt < width))) ||
+      (new_rows > 0 && (!parents || !new_table || !new_lengths || (new_rows > 1 && ldn < width) ||
+                        new_table == table || new_lengths == lengths)))
+    return GPTQ_ERR_INVALID_ARG;
+  return hip_status(launch_kv_pages_fork(table, ldt, lengths, rows, refs, pages, parents, new_rows,
+                                         page_size, new_table, ldn, width, new_lengths, new_refs,
+                                         info, stream));
+}
+
+gptq_status kv_pages_resize_workspace_size(int64_t rows, int64_t pages, size_t* bytes) {
+  if (!bytes || rows < 0 || bad_dim(rows) || pages <= 0 || bad_dim(pages)) return GPTQ_ERR_INVALID_ARG;
+  *bytes = kv_pages_resize_ws_bytes(rows, pages);
+  return GPTQ_OK;
+}
+
+gptq_status kv_pages_resize(int32_t* table, int64_t ldt, int32_t* lengths, int64_t rows,
+                            int64_t width, int32_t* refs, int64_t pages,
+                            const int32_t* new_lengths, int32_t page_size, int32_t* src,
+                            int32_t* dst, int32_t* info, void* ws, size_t ws_bytes,
+                            hipStream_t stream) {
+  const gptq_status ok = pages_ok(rows, width, pages, page_size);
+  if (ok != GPTQ_OK || rows == 0) return ok;
+  if (!table || !lengths || !refs || !new_lengths || !src || !dst || src == dst ||
+      new_lengths == lengths || (rows > 1 && ldt < width))
+    return GPTQ_ERR_INVALID_ARG;
+  const gptq_status w = check_ws(ws, ws_bytes, kv_pages_resize_ws_bytes(rows, pages));
+  if (w != GPTQ_OK) return w;
+  if ((reinterpret_cast<uintptr_t>(ws) & 3) != 0) return GPTQ_ERR_INVALID_ARG;
+  return hip_status(launch_kv_pages_resize(table, ldt, width, lengths, rows, refs, pages,
+                                           new_lengths, page_size, src, dst, info, ws, stream));
+}
+
+gptq_status kv_pages_compact_workspace_size(int64_t pages, size_t* bytes) {
+  if (!bytes || pages <= 0 || bad_dim(pages)) return GPTQ_ERR_INVALID_ARG;
+  *bytes = kv_pages_compact_ws_bytes(pages);
+  return GPTQ_OK;
+}
+
+gptq_status kv_pages_compact(const int32_t* table, int64_t ldt, int64_t rows, int64_t width,
+                             const int32_t* refs, int64_t pages, int32_t* new_table, int64_t ldn,
+                             int32_t* new_refs, int32_t* src, int32_t* dst, int64_t capacity,
+                             int32_t* count, void* ws, size_t ws_bytes, hipStream_t stream) {
+  const gptq_status ok = pages_ok(rows, width, pages, 1);
+  if (ok != GPTQ_OK) return ok;
+  if (!refs || !new_refs || refs == new_refs || !count || capacity < pages / 2 || bad_dim(capacity) ||
+      (capacity > 0 && (!src || !dst || src == dst)) ||
+      (rows > 0 && (!table || !new_table || new_table == table ||
+                    (rows > 1 && (ldt < width || ldn < width)))))
+    return GPTQ_ERR_INVALID_ARG;
+  const gptq_status w = check_ws(ws, ws_bytes, kv_pages_compact_ws_bytes(pages));
+  if (w != GPTQ_OK) return w;
+  if ((reinterpret_cast<uintptr_t>(ws) & 3) != 0) return GPTQ_ERR_INVALID_ARG;
+  return hip_status(launch_kv_pages_compact(table, ldt, rows, width, refs, pages, new_table, ldn,
+                                            new_refs, src, dst, capacity, count, ws, stream));
+}
+
+gptq_status kv_pages_copy(const gptq_page_array* arrays, int64_t n, const int32_t* src,
+                          const int32_t* dst, int64_t pairs, int32_t* info, hipStream_t stream) {
+  if (n < 0 || bad_dim(n) || pairs < 0 || bad_dim(pairs) || (n > 0 && !arrays)) return GPTQ_ERR_INVALID_ARG;
+  for (int64_t i = 0; i < n; ++i) {
+    const gptq_page_array& v = arrays[i];
+    if (!v.data || v.pages <= 0 || v.outer <= 0 || v.inner <= 0 || v.row_bytes <= 0 ||
+        v.page_stride < 0 || v.outer_stride < 0 || v.inner_stride < 0 ||
+        (v.pages > 1 && v.page_stride == 0) || (v.outer > 1 && v.outer_stride == 0) ||
+        (v.inner > 1 && v.inner_stride == 0))
+      return GPTQ_ERR_INVALID_ARG;
+  }
+  if (n == 0 || pairs == 0) return GPTQ_OK;
+  if (!src || !dst) return GPTQ_ERR_INVALID_ARG;
+  return hip_status(launch_kv_pages_copy(arrays, n, src, dst, pairs, info, stream));
+}
+
+gptq_status verify_drafts_workspace_size(int64_t tokens, int64_t vocab, int64_t seqs,
+                                         size_t* bytes) {
+  if (!bytes || tokens < 0 || bad_dim(tokens) || vocab <= 0 || bad_dim(vocab) || seqs < 0 ||
+      bad_dim(seqs))
+    return GPTQ_ERR_INVALID_ARG;
+  *bytes = seqs == 0 ? 0 : verify_ws_bytes(tokens, vocab, seqs);
+  return GPTQ_OK;
+}
+
+gptq_status verify_drafts(const void* target, gptq_dtype tdt, int64_t ldt, const void* draft,
+                          gptq_dtype ddt, int64_t ldd, int64_t tokens, int64_t vocab,
+                          const int64_t* ids, const int32_t* starts, int64_t seqs, const float* u,
+                          const float* u_next, const float* temperatures, int32_t* accepted,
+                          int64_t* tokens_out, float* logprobs, void* ws, size_t ws_bytes,
+                          hipStream_t stream) {
+  size_t need = 0;
+  const gptq_status ok = verify_drafts_workspace_size(tokens, vocab, seqs, &need);
+  if (ok != GPTQ_OK) return ok;
+  if (!valid_dtype(tdt) || (draft && !valid_dtype(ddt))) return GPTQ_ERR_INVALID_ARG;
+  if (seqs == 0) return GPTQ_OK;
+  if (!starts || !accepted ||
+      (tokens > 0 && (!target || ldt < vocab || (draft && ldd < vocab) || !ids || !u || !u_next ||
+                      !tokens_out || tokens_out == ids || logprobs == u)))
+    return GPTQ_ERR_INVALID_ARG;
+  const gptq_status w = check_ws(ws, ws_bytes, need);
+  if (w != GPTQ_OK) return w;
+  if ((reinterpret_cast<uintptr_t>(ws) & 15) != 0) return GPTQ_ERR_INVALID_ARG;
+  VerifyArgs a{};
+  a.target = target; a.draft = draft; a.tdt = tdt; a.ddt = ddt; a.ldt = ldt; a.ldd = ldd;
+  a.tokens = tokens; a.vocab = vocab; a.seqs = seqs;
+  a.ids = ids; a.starts = starts; a.u = u; a.u_next = u_next; a.temps = temperatures;
+  a.accepted = accepted; a.out = tokens_out; a.logprobs = logprobs; a.ws = ws;
+  return hip_status(launch_verify(a, stream));
 }
 
 }  // extern "C"

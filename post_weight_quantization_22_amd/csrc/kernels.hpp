@@ -170,6 +170,73 @@ hipError_t launch_kv_read(const gptq_kv_cache* kc, const gptq_kv_cache* vc, cons
                           int64_t tokens, const KvRows& k, const KvRows& v, int dt, int32_t* info,
                           hipStream_t stream);
 
+// the sequences of a call on a block cache: pages, lengths, where their rows begin
+struct KvSequences {
+  const int32_t* table;  // [seqs][ldt], width entries each
+  int64_t ldt, width;
+  const int32_t* lengths;
+  const int32_t* starts;  // [seqs + 1]
+  int64_t seqs, tokens;
+};
+
+// ---- kv_block_write.hip ---------------------------------------------------
+hipError_t launch_kv_block_write(const KvRows& k, const KvRows& v, int dt, const KvSequences& seqs,
+                                 const gptq_kv_blocks* kb, const gptq_kv_blocks* vb, int32_t* info,
+                                 hipStream_t stream);
+
+// ---- kv_attention.hip -----------------------------------------------------
+struct KvAttention {
+  KvRows q, out;  // out.p of q's type
+  float* lse;     // [tokens][q_heads], may be null
+  int dt, q_heads, causal, window;
+  float scale;
+};
+size_t kv_attention_ws_bytes(const gptq_kv_blocks* c, int q_heads, int dt, int64_t tokens,
+                             int64_t seqs, int64_t width);
+hipError_t launch_kv_attention(const KvAttention& t, const KvSequences& seqs,
+                               const gptq_kv_blocks* kb, const gptq_kv_blocks* vb, int32_t* info,
+                               void* ws, hipStream_t stream);
+
+// ---- kv_pages.hip ---------------------------------------------------------
+hipError_t launch_kv_pages_fork(const int32_t* table, int64_t ldt, const int32_t* lengths,
+                                int64_t rows, const int32_t* refs, int64_t pages,
+                                const int32_t* parents, int64_t new_rows, int page_size,
+                                int32_t* new_table, int64_t ldn, int64_t width,
+                                int32_t* new_lengths, int32_t* new_refs, int32_t* info,
+                                hipStream_t stream);
+size_t kv_pages_resize_ws_bytes(int64_t rows, int64_t pages);
+hipError_t launch_kv_pages_resize(int32_t* table, int64_t ldt, int64_t width, int32_t* lengths,
+                                  int64_t rows, int32_t* refs, int64_t pages,
+                                  const int32_t* new_lengths, int page_size, int32_t* src,
+                                  int32_t* dst, int32_t* info, void* ws, hipStream_t stream);
+size_t kv_pages_compact_ws_bytes(int64_t pages);
+hipError_t launch_kv_pages_compact(const int32_t* table, int64_t ldt, int64_t rows, int64_t width,
+                                   const int32_t* refs, int64_t pages, int32_t* new_table,
+                                   int64_t ldn, int32_t* new_refs, int32_t* src, int32_t* dst,
+                                   int64_t capacity, int32_t* count, void* ws, hipStream_t stream);
+hipError_t launch_kv_pages_copy(const gptq_page_array* arrays, int64_t n, const int32_t* src,
+                                const int32_t* dst, int64_t pairs, int32_t* info,
+                                hipStream_t stream);
+
+// ---- verify.hip -----------------------------------------------------------
+struct VerifyArgs {
+  const void* target;
+  const void* draft;  // may be null: each drafted token was certain
+  int tdt, ddt;
+  int64_t ldt, ldd, tokens, vocab, seqs;
+  const int64_t* ids;
+  const int32_t* starts;
+  const float* u;
+  const float* u_next;
+  const float* temps;  // may be null
+  int32_t* accepted;
+  int64_t* out;
+  float* logprobs;  // may be null
+  void* ws;
+};
+size_t verify_ws_bytes(int64_t tokens, int64_t vocab, int64_t seqs);
+hipError_t launch_verify(const VerifyArgs& a, hipStream_t stream);
+
 // ---- logprobs.hip ---------------------------------------------------------
 size_t logprobs_ws_bytes(int64_t tokens, int64_t vocab, int top);
 hipError_t launch_logprobs(const void* X, int dt, int64_t tokens, int64_t vocab, int64_t ldx,

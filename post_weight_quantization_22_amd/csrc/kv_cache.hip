@@ -153,41 +153,6 @@ __device__ __forceinline__ void minmax_params_fast(float lo, float hi, float max
     zero = rintf(__fdiv_rn(num, span));
 }
 
-// The 8 integer codes of quant_code(x, scale, zero, maxq), BITS each.  A quotient is at
-// most 255 and its form by the reciprocal within 2^-22 of it, 6.1e-5: the integers
-// agree unless a half-integer is that near, and then the division decides.
-// kRound + an integer below 2^22 has that integer in its low bits, so one fma both
-// rounds the quotient and adds the zero-point, and the codes' bit patterns can be
-// shifted and added as they are, what kRound adds taken off at the end (modulo 2^32).
-template <int BITS>
-__device__ __forceinline__ uint2 int_codes8(const Vals8& x, float scale, float zero, float maxq) {
-  constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
-  const float rs = approx_recip(scale), off = zero + kRound;
-  float c[8], far = 0.0f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    c[e] = fmaf(x.v[e], rs, off);
-    far = fmaxf(far, fabsf(fmaf(x.v[e], rs, off - c[e])));
-  }
-  // (a NaN has code 0 either way)
-  if (!(far < 0.4999f) || !(scale > 0x1p-120f && scale < 0x1p120f)) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) c[e] = rintf(__fdiv_rn(x.v[e], scale)) + off;
-  }
-  constexpr int PER = 32 / BITS;  // codes in a word
-  constexpr uint32_t ONES = BITS == 4 ? 0x11111111u : 0x01010101u;
-  uint32_t w[8 / PER];
-#pragma unroll
-  for (int i = 0; i < 8 / PER; ++i) {
-    w[i] = 0u - 0x4B400000u * ONES;  // kRound's bit pattern
-#pragma unroll
-    for (int e = 0; e < PER; ++e)  // (the middle of three passes over a NaN: code 0)
-      w[i] += __float_as_uint(__builtin_amdgcn_fmed3f(c[PER * i + e], kRound, kRound + maxq))
-              << (BITS * e);
-  }
-  return make_uint2(w[0], BITS == 4 ? 0u : w[8 / PER - 1]);
-}
-
 // A lane takes 8 V consecutive values, LPG lanes a group.
 template <int DT, int LPG, int V>
 __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvArgs a) {
