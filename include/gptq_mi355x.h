@@ -557,8 +557,8 @@ gptq_status token_logprobs(const void* logits, gptq_dtype dt, int64_t tokens, in
  * scales[pages][page_size / block][heads] at
  *   page * param_page_stride + (slot / block) * param_block_stride + head * param_head_stride
  * (elements), any order of pages, slots and heads.  head_dim: a multiple of 16, at most
- * 256; block divides page_size; heads <= 4096; pages * page_size < 2^31; codes 16-byte
- * aligned, strides multiples of 16 bytes; strides of dimensions longer than 1 are not 0.
+ * 256; block divides page_size; heads <= 4096; pages * page_size < 2^31; slot_stride at
+ * most 2^26, param_block_stride below 2^31; codes 16-byte aligned, strides multiples of 16 bytes; strides of dimensions longer than 1 are not 0.
  * block = 1 also fits what kv_cache_write writes in INT8 without zeros or E4M3 with
  * group_size -1.
  *

@@ -92,8 +92,10 @@ gptq_status kv_blocks_ok(const gptq_kv_blocks* c) {
       c->heads <= 0 || c->head_dim <= 0 || c->page_size % c->block != 0 ||
       (c->format != GPTQ_KV_INT8 && c->format != GPTQ_KV_E4M3))
     return GPTQ_ERR_INVALID_ARG;
+  // (16 slots' offsets are counted in 32 bits)
   if (c->head_dim % 16 != 0 || c->head_dim > 256 || c->heads > 4096 ||
-      c->pages > INT32_MAX / c->page_size)
+      c->pages > INT32_MAX / c->page_size || c->slot_stride > (int64_t(1) << 26) ||
+      c->param_block_stride > INT32_MAX)
     return GPTQ_ERR_UNSUPPORTED;
   // an expanded dimension would have two places share their bytes
   if ((c->pages > 1 && (c->page_stride <= 0 || c->param_page_stride <= 0)) ||

@@ -53,7 +53,7 @@ struct AttnArgs {
   int32_t causal, window, qvec, ovec;
   float scale;  // times log2(e)
   int32_t splits;
-  Divisor by_rows;  // rows of a tile
+  Divisor by_rows, by_group, by_splits;  // rows of a tile, query heads of a key head
   float* parts;     // [task][head][split][rows][DP]
   float2* stats;    // [task][head][split][rows]: maximum, sum
 };
@@ -118,20 +118,21 @@ __device__ __forceinline__ TileRows tile_rows(const AttnArgs& a, int task, int p
   t.hi = t.sp.length;
   t.lo = 0;
   if (t.rows > 0 && a.causal) {
-    const int p0 = base + t.row0 / a.group, p1 = base + (t.row0 + t.rows - 1) / a.group;
+    const int p0 = base + divided(t.row0, a.by_group), p1 = base + divided(t.row0 + t.rows - 1, a.by_group);
     t.hi = max(min(t.hi, p1 + 1), 0);
     if (a.window > 0) t.lo = max(p0 - a.window + 1, 0) & ~15;
   }
   return t;
 }
 
-// a split's keys: whole rounds of the workgroup's waves
-__device__ __forceinline__ void split_keys(const TileRows& t, int splits, int i, int& k0, int& k1) {
-  const int n = max(t.hi - t.lo, 0);
-  const int per = ((n + splits - 1) / splits + kTile * kWaves - 1) / (kTile * kWaves) * (kTile * kWaves);
-  const int64_t b = (int64_t)i * per;
-  k0 = t.lo + (int)min((int64_t)n, b);
-  k1 = t.lo + (int)min((int64_t)n, b + per);
+// a split's keys: whole rounds of the workgroup's waves (counted in 32 bits: a 64-bit comparison has
+// no scalar form, and what hangs on it would be held in every lane)
+__device__ __forceinline__ void split_keys(const AttnArgs& a, const TileRows& t, int i, int& k0, int& k1) {
+  const uint32_t n = (uint32_t)max(t.hi - t.lo, 0);
+  const uint32_t per = ((uint32_t)divided((int)n, a.by_splits) + kTile * kWaves) & ~(uint32_t)(kTile * kWaves - 1);
+  const uint32_t b = (uint32_t)i * per;  // (at most n + 64 rounds)
+  k0 = t.lo + (int)min(n, b);
+  k1 = t.lo + (int)min(n, b + per);
 }
 
 // Row rr (of rows * group) of the sequence: DP / 16 values from column c on, and its statistics.
@@ -139,7 +140,7 @@ template <int DP, bool F32>
 __device__ __forceinline__ void finish_row(const AttnArgs& a, const Span& sp, int head, int rr, int c,
                                            const float* o, float m, float l) {
   constexpr int N = DP / 16;
-  const int r = rr / a.group;
+  const int r = divided(rr, a.by_group);
   const int64_t row = sp.start + r;
   const int qh = head * a.group + (rr - r * a.group);
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // (no key: zeros)
@@ -177,10 +178,206 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, const Span& sp, in
     a.lse[row * (int64_t)(a.heads * a.group) + qh] = l == 0.0f ? kNegInf : m * kLn2 + logf(l);
 }
 
-// DP: head_dim rounded up to 64, 128 or 256.  EVEN: the 16 keys of a half tile share a page and
-// a block.  fp32 rows: queries and probabilities as three bf16 terms each.
+// One of the two caches, at the workgroup's head.
+struct Side {
+  const uint8_t* codes;
+  const float* scales;
+  int64_t cpage, ppage;
+  int32_t cslot, pblock;
+};
+
+__device__ __forceinline__ Side side_of(const BlockCache& c, int head) {
+  return Side{c.codes + head * c.chead, c.scales + head * c.phead, c.cpage, c.ppage, (int32_t)c.cslot, (int32_t)c.pblock};
+}
+
+// A zero that the compiler takes for a lane's own: loads that all lanes make of one address go the
+// vector loads' way, and are waited for where they are used, in order with the others (a scalar
+// load is waited for as soon as its value is put anywhere).
+__device__ __forceinline__ int lane_zero() {
+  int z = 0;
+  __asm__ volatile("" : "+v"(z));
+  return z;
+}
+
+// Where the 32 keys of a tile lie.  EVEN: the 16 keys of a half tile share a page and a block, and
+// all of this is the same in every lane; else lane i (and i + 32) knows key i.  A key behind the
+// end, or whose page is none, has page 0 and is marked as such: its loads go somewhere and count
+// for nothing, so that no load depends on a branch.
+template <bool EVEN>
+struct Place {
+  static constexpr int N = EVEN ? 2 : 1;
+  int page[N], slot[N];
+  bool there[N];
+};
+
+// The table's entries for the tile at k0 (loads under way until place_of).
+template <bool EVEN>
+struct Entries {
+  int v[EVEN ? 2 : 1];
+};
+
+template <bool EVEN>
+__device__ __forceinline__ Entries<EVEN> entries_of(const AttnArgs& a, const int32_t* table, int k0, int ke, int zero) {
+  Entries<EVEN> e;
+#pragma unroll
+  for (int u = 0; u < Place<EVEN>::N; ++u) {
+    const int kk = min(EVEN ? k0 + 16 * u : k0 + ((int)threadIdx.x & 31), ke - 1);
+    e.v[u] = table[min(divided(kk, a.s.by_page), a.s.width - 1) + zero];
+  }
+  return e;
+}
+
+template <bool EVEN>
+__device__ __forceinline__ Place<EVEN> place_of(const AttnArgs& a, const Entries<EVEN>& e, int k0, int ke, bool& bad) {
+  Place<EVEN> p;
+#pragma unroll
+  for (int u = 0; u < Place<EVEN>::N; ++u) {
+    const int key = EVEN ? k0 + 16 * u : k0 + ((int)threadIdx.x & 31), kk = min(key, ke - 1);
+    const int entry = divided(kk, a.s.by_page);
+    const int page = EVEN ? __builtin_amdgcn_readfirstlane(e.v[u]) : e.v[u];
+    const bool ok = entry < a.s.width && (uint32_t)page < (uint32_t)a.s.pages;
+    bad = bad || (key < ke && !ok);
+    p.there[u] = key < ke && ok;
+    p.page[u] = ok ? page : 0;
+    p.slot[u] = kk - entry * a.s.page_size;
+    if (EVEN) p.slot[u] &= ~15;  // (kk may have been moved to the last key)
+  }
+  return p;
+}
+
+// The scales of a lane's 8 keys, 16 u + 4 g + i: EVEN: of the half tiles; else of key i in lane i.
+template <bool EVEN>
+struct Scales {
+  float v[EVEN ? 2 : 1];
+};
+template <bool EVEN>
+__device__ __forceinline__ Scales<EVEN> scales_of(const AttnArgs& a, const Side& c, const Place<EVEN>& p, int zero) {
+  Scales<EVEN> s;
+#pragma unroll
+  for (int u = 0; u < Place<EVEN>::N; ++u)
+    s.v[u] = c.scales[p.page[u] * c.ppage + (int64_t)divided(p.slot[u], a.s.by_block) * c.pblock + zero];
+  return s;
+}
+template <bool EVEN>
+__device__ __forceinline__ void spread(const Scales<EVEN>& s, float (&v)[2][4]) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (EVEN) v[u][i] = s.v[u];
+      else v[u][i] = __shfl(s.v[0], 16 * u + 4 * (((int)threadIdx.x & 63) >> 4) + i);
+    }
+}
+
+// The codes of key row 16 u + r in cache c.
+template <bool EVEN>
+__device__ __forceinline__ const uint8_t* row_of(const Side& c, const Place<EVEN>& p, int u, int r) {
+  if constexpr (EVEN) {
+    return c.codes + (p.page[u] * c.cpage + (int64_t)p.slot[u] * c.cslot) + (uint32_t)(r * c.cslot);
+  } else {
+    const int page = __shfl(p.page[0], 16 * u + r), slot = __shfl(p.slot[0], 16 * u + r);
+    return c.codes + (page * c.cpage + (int64_t)slot * c.cslot);
+  }
+}
+
+template <int W>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
+  if constexpr (W == 1) w[0] = *reinterpret_cast<const uint32_t*>(p);
+  else if constexpr (W == 2) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    w[0] = x.x; w[1] = x.y;
+  } else {
+    const uint4 x = *reinterpret_cast<const uint4*>(p);
+    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+  }
+}
+
+// 8 codes as an operand of the first product
+template <int FMT>
+__device__ __forceinline__ Frag frag_of(uint32_t w0, uint32_t w1) {
+  Frag f;
+  w0 = signed_codes<FMT>(w0);
+  w1 = signed_codes<FMT>(w1);
+  f.p[0] = pair_of<FMT, false>(w0);
+  f.p[1] = pair_of<FMT, true>(w0);
+  f.p[2] = pair_of<FMT, false>(w1);
+  f.p[3] = pair_of<FMT, true>(w1);
+  return f;
+}
+
+// Byte b of each of 8 words (the lane's keys): an operand of the second product
+template <int FMT, int B>
+__device__ __forceinline__ Frag column_of(const uint32_t (&two)[2][4]) {
+  Frag f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) f.p[k] = pair_of<FMT, (B & 1) != 0>(two[B / 2][k]);
+  return f;
+}
+template <int FMT, typename F>
+__device__ __forceinline__ void columns_of(const uint32_t (&w)[8], F&& use) {
+  uint32_t two[2][4];  // bytes 0, 1 and 2, 3 of keys 2 k and 2 k + 1
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t x = signed_codes<FMT>(w[2 * k]), y = signed_codes<FMT>(w[2 * k + 1]);
+    two[0][k] = __builtin_amdgcn_perm(y, x, 0x05010400u);
+    two[1][k] = __builtin_amdgcn_perm(y, x, 0x07030602u);
+  }
+  use(0, column_of<FMT, 0>(two));
+  use(1, column_of<FMT, 1>(two));
+  use(2, column_of<FMT, 2>(two));
+  use(3, column_of<FMT, 3>(two));
+}
+
+// Queries of 16 rows: lane (row c16, group g) holds columns 64 (s / 2) + 16 g + 8 (s % 2) .. + 7 of
+// step s, as the keys' rows are loaded.
+template <int STEPS, int TERMS>
+__device__ __forceinline__ void load_queries(const AttnArgs& a, const TileRows& t, int head, int r16, int g,
+                                             Frag (&q)[STEPS][TERMS], int& pos) {
+  constexpr bool F32 = TERMS == 3;
+  constexpr int DT = F32 ? GPTQ_F32 : GPTQ_BF16;
+  // (rows behind the tile's last are its first one's: nothing of them is stored)
+  const int rr = t.row0 + (r16 < t.rows ? r16 : 0), r = divided(rr, a.by_group);
+  pos = t.sp.length - t.sp.rows + r;
+  const char* p = a.q + ((int64_t)(t.sp.start + r) * a.qt + (int64_t)(head * a.group + (rr - r * a.group)) * a.qh) * (F32 ? 4 : 2);
+  Raw8<DT> raw[STEPS];
+  if (a.qvec) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int c = 64 * (s / 2) + 16 * g + 8 * (s % 2);
+      const uint32_t keep = c < a.dim ? ~0u : 0u;  // (head_dim is a multiple of 16)
+      const uint4* x = reinterpret_cast<const uint4*>(p + (c < a.dim ? c : 0) * (F32 ? 4 : 2));
+#pragma unroll
+      for (int k = 0; k < (F32 ? 2 : 1); ++k) {
+        const uint4 y = x[k];
+        raw[s].w[4 * k] = y.x & keep; raw[s].w[4 * k + 1] = y.y & keep;
+        raw[s].w[4 * k + 2] = y.z & keep; raw[s].w[4 * k + 3] = y.w & keep;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) raw[s] = load_raw8<DT>(p, 64 * (s / 2) + 16 * g + 8 * (s % 2), a.dim, false);
+  }
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    if constexpr (F32) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float tm[TERMS];
+        split_terms<TERMS>(__uint_as_float(raw[s].w[e]), tm);
+#pragma unroll
+        for (int k = 0; k < TERMS; ++k) q[s][k].v[e] = (__bf16)tm[k];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q[s][0].w[e] = raw[s].w[e];
+    }
+  }
+}
+
+// DP: head_dim rounded up to 64, 128 or 256.  fp32 rows: queries and probabilities as three
+// bf16 terms each.
 template <int DP, int FMT, bool F32, int MT, bool EVEN>
-__global__ __launch_bounds__(kThreads) void kv_attention_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, MT == 1 && DP <= 128 && !F32 ? 3 : 1) void kv_attention_kernel(AttnArgs a) {
   constexpr int TERMS = F32 ? 3 : 1;
   constexpr int STEPS = DP / 32;   // of the first product
   constexpr int NT = DP / 16;      // tiles of 16 columns of the output; bytes of a V row in a lane
@@ -195,41 +392,58 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(AttnArgs a) {
   const TileRows t = tile_rows(a, (int)blockIdx.x, 16 * MT);
   if (t.rows <= 0) return;
   int kb, ke;
-  split_keys(t, a.splits, (int)blockIdx.z, kb, ke);
+  split_keys(a, t, (int)blockIdx.z, kb, ke);
+  const int32_t* table = a.s.table + t.sp.seq * a.s.ldt;
+  const int kfirst = kb + kTile * wave;
+  const Side kc = side_of(a.k, head), vc = side_of(a.v, head);
+  bool bad = false;
 
-  // queries: lane (row c16, group g) holds columns (DP / 4) g .. + DP / 4 - 1
+  const int zero = lane_zero();
+  uint32_t kraw[2][KW], vraw[VW][8];
+  Scales<EVEN> ksc, vsc;
+  // (columns behind head_dim: the row's first ones, whose queries and outputs are not there)
+  int ck[KW / 4];
+#pragma unroll
+  for (int p = 0; p < KW / 4; ++p) ck[p] = 64 * p + 16 * g < a.dim ? 64 * p + 16 * g : 0;
+  const int cv = NT * c16 < a.dim ? NT * c16 : 0;
+  auto load_keys = [&](const Place<EVEN>& p) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint8_t* row = row_of<EVEN>(kc, p, u, c16);
+#pragma unroll
+      for (int w = 0; w < KW / 4; ++w) load_words<4>(row + ck[w], kraw[u] + 4 * w);
+    }
+    ksc = scales_of<EVEN>(a, kc, p, zero);
+  };
+  auto load_values = [&](const Place<EVEN>& p) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w[VW];
+        load_words<VW>(row_of<EVEN>(vc, p, u, 4 * g + i) + cv, w);
+#pragma unroll
+        for (int x = 0; x < VW; ++x) vraw[x][4 * u + i] = w[x];
+      }
+    vsc = scales_of<EVEN>(a, vc, p, zero);
+  };
+
+  Place<EVEN> now = {};
+  Entries<EVEN> ahead = {};
+  if (kfirst < ke) {
+    const Entries<EVEN> e = entries_of<EVEN>(a, table, kfirst, ke, zero);
+    ahead = entries_of<EVEN>(a, table, kfirst + kTile * kWaves, ke, zero);
+    now = place_of<EVEN>(a, e, kfirst, ke, bad);
+    load_keys(now);
+    load_values(now);
+  }
   Frag q[MT][STEPS][TERMS];
   int pos[MT];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const int rr = t.row0 + 16 * mt + c16;
-    const bool live = 16 * mt + c16 < t.rows;
-    const int r = live ? rr / a.group : 0;
-    pos[mt] = t.sp.length - t.sp.rows + r;
-    const char* p = a.q + ((int64_t)(t.sp.start + r) * a.qt +
-                           (int64_t)(head * a.group + (live ? rr - r * a.group : 0)) * a.qh) * (F32 ? 4 : 2);
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      const int c0 = (DP / 4) * g + 8 * s;
-      const Raw8<F32 ? GPTQ_F32 : GPTQ_BF16> raw =
-          load_raw8<F32 ? GPTQ_F32 : GPTQ_BF16>(p, c0, live ? a.dim : 0, a.qvec);
-      if constexpr (F32) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float tm[TERMS];
-          split_terms<TERMS>(__uint_as_float(raw.w[e]), tm);
-#pragma unroll
-          for (int k = 0; k < TERMS; ++k) q[mt][s][k].v[e] = (__bf16)tm[k];
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) q[mt][s][0].w[e] = raw.w[e];
-      }
-    }
-  }
+  for (int mt = 0; mt < MT; ++mt) load_queries<STEPS, TERMS>(a, t, head, 16 * mt + c16, g, q[mt], pos[mt]);
   // (bounds of the tile's rows, for its masks)
-  const int pos_first = t.sp.length - t.sp.rows + t.row0 / a.group;
-  const int pos_last = t.sp.length - t.sp.rows + (t.row0 + t.rows - 1) / a.group;
+  const int pos_first = t.sp.length - t.sp.rows + divided(t.row0, a.by_group);
+  const int pos_last = t.sp.length - t.sp.rows + divided(t.row0 + t.rows - 1, a.by_group);
 
   f32x4 o[NT][MT];
   float m[MT], l[MT];
@@ -241,109 +455,13 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(AttnArgs a) {
     for (int n = 0; n < NT; ++n) o[n][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
-  const int32_t* table = a.s.table + t.sp.seq * a.s.ldt;
-  const int ck = KW * 4 * g;           // first column of the lane's part of a K row
-  const int cv = NT * c16;             // of a V row
-  for (int k0 = kb + kTile * wave; k0 < ke; k0 += kTile * kWaves) {
-    // where the keys lie: pages and slots
-    bool bad = false;
-    uint32_t kraw[2][KW], vraw[8][VW];
+  // A tile's registers are refilled as soon as they have been used: the next keys travel during the
+  // softmax and the second product, the next values during the first product behind it, the
+  // places two tiles ahead.
+  for (int k0 = kfirst; k0 < ke; k0 += kTile * kWaves) {
+    const int k1 = k0 + kTile * kWaves;
     float ks[2][4], vs[2][4];
-    bool usable[2] = {true, true};
-    uint32_t good = 0xFF;  // the lane's 8 keys: a bit each
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      if constexpr (EVEN) {
-        const int kk = k0 + 16 * u;
-        const int entry = divided(kk, a.s.by_page);
-        int page = -1;
-        if (kk < ke) {
-          page = entry < a.s.width ? table[entry] : -1;
-          if (page < 0 || page >= a.s.pages) { bad = true; page = -1; }
-        }
-        page = __builtin_amdgcn_readfirstlane(page);
-        usable[u] = page >= 0;
-        const int slot = kk - entry * a.s.page_size;
-        const int64_t ko = page * a.k.cpage + slot * a.k.cslot + head * a.k.chead;
-        const int64_t vo = page * a.v.cpage + slot * a.v.cslot + head * a.v.chead;
-        const int blk = divided(slot, a.s.by_block);
-        float sk = 0.0f, sv = 0.0f;
-        if (usable[u]) {
-          sk = a.k.scales[page * a.k.ppage + blk * a.k.pblock + head * a.k.phead];
-          sv = a.v.scales[page * a.v.ppage + blk * a.v.pblock + head * a.v.phead];
-        } else {
-          good &= u ? 0x0F : 0xF0;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) { ks[u][i] = sk; vs[u][i] = sv; }
-#pragma unroll
-        for (int w = 0; w < KW; w += 4) {
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (usable[u] && kk + c16 < ke && ck + 4 * w < a.dim)
-            x = *reinterpret_cast<const uint4*>(a.k.codes + ko + c16 * a.k.cslot + ck + 4 * w);
-          kraw[u][w] = x.x; kraw[u][w + 1] = x.y; kraw[u][w + 2] = x.z; kraw[u][w + 3] = x.w;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool in = usable[u] && kk + 4 * g + i < ke && cv < a.dim;
-          const uint8_t* p = a.v.codes + vo + (4 * g + i) * a.v.cslot + cv;
-          if constexpr (VW == 1) vraw[4 * u + i][0] = in ? *reinterpret_cast<const uint32_t*>(p) : 0;
-          else if constexpr (VW == 2) {
-            uint2 x = make_uint2(0, 0);
-            if (in) x = *reinterpret_cast<const uint2*>(p);
-            vraw[4 * u + i][0] = x.x; vraw[4 * u + i][1] = x.y;
-          } else {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (in) x = *reinterpret_cast<const uint4*>(p);
-            vraw[4 * u + i][0] = x.x; vraw[4 * u + i][1] = x.y; vraw[4 * u + i][2] = x.z; vraw[4 * u + i][3] = x.w;
-          }
-        }
-      }
-    }
-    if constexpr (!EVEN) {
-      // lane i (and i + 32) looks up key k0 + i
-      const int kk = k0 + (lane & 31);
-      int page = -1, slot = 0;
-      float sk = 0.0f, sv = 0.0f;
-      if (kk < ke) {
-        const int entry = divided(kk, a.s.by_page);
-        page = entry < a.s.width ? table[entry] : -1;
-        slot = kk - entry * a.s.page_size;
-        if (page < 0 || page >= a.s.pages) { bad = true; page = -1; }
-        else {
-          const int blk = divided(slot, a.s.by_block);
-          sk = a.k.scales[page * a.k.ppage + blk * a.k.pblock + head * a.k.phead];
-          sv = a.v.scales[page * a.v.ppage + blk * a.v.pblock + head * a.v.phead];
-        }
-      }
-      usable[0] = usable[1] = __all(page >= 0);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int pg = __shfl(page, 16 * u + c16), sl_ = __shfl(slot, 16 * u + c16);
-        const uint8_t* p = a.k.codes + pg * a.k.cpage + sl_ * a.k.cslot + head * a.k.chead + ck;
-#pragma unroll
-        for (int w = 0; w < KW; w += 4) {
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (pg >= 0 && ck + 4 * w < a.dim) x = *reinterpret_cast<const uint4*>(p + 4 * w);
-          kraw[u][w] = x.x; kraw[u][w + 1] = x.y; kraw[u][w + 2] = x.z; kraw[u][w + 3] = x.w;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int from = 16 * u + 4 * g + i;
-          const int pv = __shfl(page, from), sv_ = __shfl(slot, from);
-          ks[u][i] = __shfl(sk, from);
-          vs[u][i] = __shfl(sv, from);
-          if (pv < 0) good &= ~(1u << (4 * u + i));
-          const bool in = pv >= 0 && cv < a.dim;
-          const uint8_t* pp = a.v.codes + pv * a.v.cpage + sv_ * a.v.cslot + head * a.v.chead + cv;
-#pragma unroll
-          for (int w = 0; w < VW; ++w)
-            vraw[4 * u + i][w] = in ? reinterpret_cast<const uint32_t*>(pp)[w] : 0;
-        }
-      }
-    }
-    if (bad && a.s.info) *a.s.info = 1;
-
+    spread<EVEN>(ksc, ks);
     // S^T = K Q^T: two tiles of 16 keys
     f32x4 s[2][MT];
 #pragma unroll
@@ -352,12 +470,7 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(AttnArgs a) {
       for (int mt = 0; mt < MT; ++mt) s[u][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int st = 0; st < STEPS; ++st) {
-        const uint32_t w0 = signed_codes<FMT>(kraw[u][2 * st]), w1 = signed_codes<FMT>(kraw[u][2 * st + 1]);
-        Frag f;
-        f.p[0] = pair_of<FMT, false>(w0);
-        f.p[1] = pair_of<FMT, true>(w0);
-        f.p[2] = pair_of<FMT, false>(w1);
-        f.p[3] = pair_of<FMT, true>(w1);
+        const Frag f = frag_of<FMT>(kraw[u][2 * st], kraw[u][2 * st + 1]);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -372,23 +485,44 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(AttnArgs a) {
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[u][mt][i] *= ks[u][i] * a.scale;
+    const Place<EVEN> at = now;
+    if (k1 < ke) {
+      now = place_of<EVEN>(a, ahead, k1, ke, bad);
+      ahead = entries_of<EVEN>(a, table, k1 + kTile * kWaves, ke, zero);
+      load_keys(now);
+    }
+    spread<EVEN>(vsc, vs);
     // which of them count: a tile inside every row's range has no mask
-    const bool partial = !usable[0] || !usable[1] || k0 + kTile > ke ||
+    bool whole = true;
+#pragma unroll
+    for (int u = 0; u < Place<EVEN>::N; ++u) whole = whole && at.there[u];
+    if constexpr (!EVEN) whole = __all(whole);
+    const bool partial = !whole || k0 + kTile > ke ||
                          (a.causal && (k0 + kTile > pos_first + 1 ||
                                        (a.window > 0 && k0 <= pos_last - a.window)));
     uint32_t seen[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) seen[mt] = 0xFF;
     if (partial) {
+      uint32_t there = 0;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          bool known;  // (every lane takes part in the exchange)
+          if constexpr (EVEN) known = at.there[u];
+          else known = __shfl((int)at.there[0], 16 * u + 4 * g + i) != 0;
+          there |= (known && k0 + 16 * u + 4 * g + i < ke ? 1u : 0u) << (4 * u + i);
+        }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        seen[mt] = good;
+        seen[mt] = there;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int key = k0 + 16 * u + 4 * g + i;
-            if (key >= ke || (a.causal && (key > pos[mt] || (a.window > 0 && key <= pos[mt] - a.window))))
+            if (a.causal && (key > pos[mt] || (a.window > 0 && key <= pos[mt] - a.window)))
               seen[mt] &= ~(1u << (4 * u + i));
             if (!(seen[mt] >> (4 * u + i) & 1)) s[u][mt][i] = kNegInf;
           }
@@ -424,15 +558,13 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(AttnArgs a) {
         }
     }
     // masked places may hold e4m3's NaN: it must reach the rows that see it, and no other
-    bool nans = false;
     if (FMT == GPTQ_KV_E4M3 && partial) {
       uint32_t any = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int w = 0; w < VW; ++w)
 #pragma unroll
-        for (int w = 0; w < VW; ++w) any |= nan_bytes(vraw[i][w]);
-      nans = __any(any != 0);
-      if (nans) {
+        for (int i = 0; i < 8; ++i) any |= nan_bytes(vraw[w][i]);
+      if (__any(any != 0)) {
         Frag ind[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -440,21 +572,14 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(AttnArgs a) {
           for (int i = 0; i < 8; ++i) ind[mt].v[i] = (__bf16)(seen[mt] >> i & 1 ? 1.0f : 0.0f);
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
-          uint32_t nb[8];
+          uint32_t ones[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            nb[i] = nan_bytes(vraw[i][w]);
-            vraw[i][w] &= ~nb[i];
-            nb[i] &= 0x38383838u;  // e4m3's 1
+            const uint32_t nb = nan_bytes(vraw[w][i]);
+            vraw[w][i] &= ~nb;
+            ones[i] = nb & 0x38383838u;  // e4m3's 1
           }
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            Frag f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t two = __builtin_amdgcn_perm(nb[2 * k + 1], nb[2 * k], b < 2 ? 0x05010400u : 0x07030602u);
-              f.p[k] = b & 1 ? pair_of<FMT, true>(two) : pair_of<FMT, false>(two);
-            }
+          columns_of<FMT>(ones, [&](int b, const Frag& f) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
               const f32x4 c = mfma(f, ind[mt], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
@@ -462,38 +587,25 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(AttnArgs a) {
               for (int i = 0; i < 4; ++i)
                 o[4 * w + b][mt][i] += c[i] > 0.0f ? __builtin_nanf("") : 0.0f;
             }
-          }
+          });
         }
       }
     }
     // O^T += V^T P^T: column NT r + n of V is row r of tile n
 #pragma unroll
-    for (int w = 0; w < VW; ++w) {
-      uint32_t lo[4], hi[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t x = signed_codes<FMT>(vraw[2 * k][w]), y = signed_codes<FMT>(vraw[2 * k + 1][w]);
-        lo[k] = __builtin_amdgcn_perm(y, x, 0x05010400u);
-        hi[k] = __builtin_amdgcn_perm(y, x, 0x07030602u);
-      }
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        Frag f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t two = b < 2 ? lo[k] : hi[k];
-          f.p[k] = b & 1 ? pair_of<FMT, true>(two) : pair_of<FMT, false>(two);
-        }
+    for (int w = 0; w < VW; ++w)
+      columns_of<FMT>(vraw[w], [&](int b, const Frag& f) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int k = 0; k < TERMS; ++k) o[4 * w + b][mt] = mfma(f, p[mt][k], o[4 * w + b][mt]);
-      }
-    }
+      });
+    if (k1 < ke) load_values(now);
   }
   // the loop's branch stands between the last product and its readers: wait the product's length
   __asm__ volatile("s_nop 15" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
+  if (bad && a.s.info) *a.s.info = 1;
 
   // join the waves, 16 rows at a time
   const int64_t part = ((int64_t)blockIdx.x * a.heads + head) * a.splits + blockIdx.z;
@@ -548,22 +660,47 @@ __global__ __launch_bounds__(kThreads) void kv_attention_join_kernel(AttnArgs a,
   const int tid = threadIdx.x, head = blockIdx.y;
   const TileRows t = tile_rows(a, (int)blockIdx.x, per);
   const int64_t part = ((int64_t)blockIdx.x * a.heads + head) * a.splits;
+  constexpr int B = 8;  // parts whose loads are under way together
   for (int row = tid >> 4; row < t.rows; row += 16) {
     const int c = (tid & 15) * NT;
-    float mx = kNegInf;
-    for (int s = 0; s < a.splits; ++s) mx = fmaxf(mx, a.stats[(part + s) * per + row].x);
-    const float base = mx == kNegInf ? 0.0f : mx;
-    float v[NT] = {}, tl = 0.0f;
-    for (int s = 0; s < a.splits; ++s) {
-      const int64_t at = (part + s) * per + row;
-      const float2 st = a.stats[at];
-      const float f = __builtin_amdgcn_exp2f(st.x - base);
-      tl += st.y * f;
-      const float* d = a.parts + at * DP + c;
+    float m = kNegInf, l = 0.0f, v[NT] = {};
+    for (int s0 = 0; s0 < a.splits; s0 += B) {
+      float2 st[B];
+      float4 d[B][NT / 4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) v[n] += d[n] * f;
+      for (int k = 0; k < B; ++k) {
+        const int64_t at = (part + min(s0 + k, a.splits - 1)) * per + row;
+        st[k] = a.stats[at];
+#pragma unroll
+        for (int n = 0; n < NT / 4; ++n) d[k][n] = reinterpret_cast<const float4*>(a.parts + at * DP + c)[n];
+      }
+      float mx = m;
+#pragma unroll
+      for (int k = 0; k < B; ++k) {
+        if (s0 + k >= a.splits) st[k] = make_float2(kNegInf, 0.0f);
+        mx = fmaxf(mx, st[k].x);
+      }
+      const float base = mx == kNegInf ? 0.0f : mx;
+      const float f0 = __builtin_amdgcn_exp2f(m - base);
+      m = mx;
+      l *= f0;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) v[n] *= f0;
+#pragma unroll
+      for (int k = 0; k < B; ++k) {
+        const float f = __builtin_amdgcn_exp2f(st[k].x - base);
+        l += st[k].y * f;
+#pragma unroll
+        for (int n = 0; n < NT / 4; ++n) {
+          // (a part behind the last one may hold anything)
+          v[4 * n] += s0 + k < a.splits ? d[k][n].x * f : 0.0f;
+          v[4 * n + 1] += s0 + k < a.splits ? d[k][n].y * f : 0.0f;
+          v[4 * n + 2] += s0 + k < a.splits ? d[k][n].z * f : 0.0f;
+          v[4 * n + 3] += s0 + k < a.splits ? d[k][n].w * f : 0.0f;
+        }
+      }
     }
-    finish_row<DP, F32>(a, t.sp, head, t.row0 + row, c, v, mx, tl);
+    finish_row<DP, F32>(a, t.sp, head, t.row0 + row, c, v, m, l);
   }
 }
 
@@ -581,10 +718,12 @@ Plan plan_of(const gptq_kv_blocks* c, int q_heads, int dt, int64_t tokens, int64
   const int64_t each = ceil_div(tokens * group, seqs);  // rows of a sequence on average
   p.mt = each > 16 && dt == GPTQ_BF16 && c->head_dim <= 128 ? 4 : 1;
   p.tasks = tokens * group / (16 * p.mt) + seqs;
-  // splits: as many as give 1024 workgroups, 256 keys each at least
+  // Splits: as many as give 512 workgroups, two a CU, whose waves' loads fill the memory's queue
+  // (16 sequences of 12000, 8 heads of 128: 128 workgroups 115 us, 512 80, 768 88, 1024 91, 2048 87),
+  // 512 keys each at least (5 sequences of 300: one 10.1 us, two and their join 13.5).
   const int64_t tiles = hmin(p.tasks, seqs * ceil_div(each, int64_t(16) * p.mt)) * c->heads;
   const int64_t keys = hmin(width * c->page_size, int64_t(1) << 30);
-  p.splits = (int)hmax(1, hmin(hmin(ceil_div(1024, tiles), 64), keys / 256));
+  p.splits = (int)hmax(1, hmin(hmin(ceil_div(512, tiles), 64), keys / 512));
   return p;
 }
 
@@ -622,6 +761,8 @@ hipError_t launch_kv_attention(const KvAttention& t, const KvSequences& seqs,
   a.scale = t.scale * kLog2e;
   a.splits = p.splits;
   a.by_rows = divisor_of(16 * p.mt);
+  a.by_group = divisor_of(a.group);
+  a.by_splits = divisor_of(p.splits);
   a.stats = static_cast<float2*>(ws);
   a.parts = reinterpret_cast<float*>(a.stats + p.tasks * kb->heads * p.splits * 16 * p.mt);
   const bool even = kb->page_size % 16 == 0 && kb->block % 16 == 0;

@@ -6,23 +6,22 @@
 
 namespace gptq {
 
-// n / d for 0 <= n < 2^31: mul = floor(2^(32 + shift) / d) + 1, shift = floor(log2 d), is
-// off by at most d < 2^(shift + 1) of 2^(32 + shift), too little to reach the next
-// quotient; mul == 0 where d is a power of two.
+// n / d for 0 <= n < 2^31 as n * mul >> shift: with 2^k >= d, mul = ceil(2^(31 + k) / d) is off by
+// less than d <= 2^k of 2^(31 + k), and n times that is less than 2^(31 + k), too little to reach
+// the next quotient.
 struct Divisor {
   uint32_t mul;
   int32_t shift;
 };
 
 inline Divisor divisor_of(int64_t d) {
-  int s = 0;
-  while ((int64_t(2) << s) <= d) ++s;
-  if ((d & (d - 1)) == 0) return Divisor{0, s};
-  return Divisor{(uint32_t)((uint64_t(1) << (32 + s)) / (uint64_t)d + 1), s};
+  int k = 0;
+  while ((int64_t(1) << k) < d) ++k;
+  return Divisor{(uint32_t)(((uint64_t(1) << (31 + k)) + (uint64_t)d - 1) / (uint64_t)d), 31 + k};
 }
 
 __device__ __forceinline__ int divided(int n, const Divisor& d) {
-  return d.mul ? (int)(__umulhi((uint32_t)n, d.mul) >> d.shift) : n >> d.shift;
+  return (int)(((uint64_t)(uint32_t)n * d.mul) >> d.shift);
 }
 
 struct BlockCache {  // one of the two caches
@@ -57,22 +56,26 @@ __device__ __forceinline__ Span span_of(const Sequences& q, int t, int num, cons
                                         int extra, int& first) {
   const int lane = threadIdx.x & 63;
   auto start_at = [&](int i) { return min(max(q.starts[i], 0), q.tokens); };
-  auto task_at = [&](int i) { return divided(start_at(i) * num, den) + i * extra; };
+  auto task_at = [&](int start, int i) { return divided(start * num, den) + i * extra; };
   int lo = 0, n = q.seqs;  // the last i in lo .. lo + n - 1 with task_at(i) <= t
-  while (n > 1) {
-    const int step = (n + 63) / 64, i = lo + lane * step;
-    const bool below = lane * step < n && task_at(i) <= t;
+  while (n > 64) {
+    const int step = (n + 63) / 64, i = lo + min(lane * step, n - 1);
+    const bool below = (lane * step < n) & (task_at(start_at(i), i) <= t);
     const int k = max(__popcll(__ballot(below)) - 1, 0);
     n = min(step, n - k * step);
     lo += k * step;
   }
-  lo = __builtin_amdgcn_readfirstlane(lo);
+  // the last step reads all that the answer may need: one round trip for up to 64 sequences
+  const int i = lo + min(lane, n - 1);
+  const int s0 = start_at(i), s1 = start_at(i + 1), len = q.lengths[i];
+  // (& and no branch: what is computed on both sides of one counts as different in every lane)
+  const int k = max(__popcll(__ballot((lane < n) & (task_at(s0, i) <= t))) - 1, 0);
   Span s;
-  s.seq = lo;
-  s.start = start_at(lo);
-  s.rows = max(start_at(lo + 1) - s.start, 0);
-  s.length = max(q.lengths[lo], 0);
-  first = task_at(lo);
+  s.seq = __builtin_amdgcn_readfirstlane(lo + k);
+  s.start = __builtin_amdgcn_readlane(s0, k);
+  s.rows = max(__builtin_amdgcn_readlane(s1, k) - s.start, 0);
+  s.length = max(__builtin_amdgcn_readlane(len, k), 0);
+  first = task_at(s.start, s.seq);
   return s;
 }
 

@@ -57,7 +57,7 @@ __device__ __forceinline__ Span row_span(const Kernel& a, int row) {
   q.seqs = (int32_t)a.v.seqs;
   q.tokens = (int32_t)a.v.tokens;
   int first;
-  return span_of(q, row, 1, Divisor{0, 0}, 0, first);
+  return span_of(q, row, 1, Divisor{1, 0}, 0, first);
 }
 
 __device__ __forceinline__ float logit(const Kernel& a, bool draft, int64_t row, int64_t i) {
