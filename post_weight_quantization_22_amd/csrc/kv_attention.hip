@@ -92,12 +92,44 @@ __device__ __forceinline__ uint32_t bf16_bits(float v) {
 
 // TERMS bf16 numbers whose sum is x (1: rounded; 3: 24 bits and more)
 template <int TERMS>
-__device__ __forceinline__ void split_terms(float x, float (&t)[TERMS]) {
+__device__ __forceinline__ void split_terms(float x, __bf16 (&t)[TERMS]) {
 #pragma unroll
   for (int k = 0; k < TERMS; ++k) {
-    t[k] = (float)(__bf16)x;
-    x = x - t[k];
+    t[k] = (__bf16)x;
+    x = x - (float)t[k];
     if (!is_finite(x)) x = 0.0f;  // an infinity or a NaN is in its first term
+  }
+}
+
+// The weights of one row, keys 16 u + 4 g + i, as the second product's operands: e^(s - base) times
+// the values' scales; their sum is added to l.  MASKED: a weight whose key is not seen is 0, whatever
+// its scale is (apart from the other form, which costs half as many instructions).
+template <bool MASKED, int TERMS>
+__device__ __forceinline__ void weights_of(const f32x4 (&s)[2], const float (&vs)[2][4], uint32_t seen, float base,
+                                           float& l, Frag (&p)[TERMS]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {  // pairs
+    float x[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int u = k / 2, i = 2 * (k % 2) + e;
+      const float w = __builtin_amdgcn_exp2f(s[u][i] - base);
+      l += w;
+      x[e] = w * vs[u][i];
+      if (MASKED) x[e] = (seen >> (4 * u + i) & 1) ? x[e] : 0.0f;
+    }
+    if constexpr (TERMS == 1) {
+      p[0].p[k][0] = (__bf16)x[0];
+      p[0].p[k][1] = (__bf16)x[1];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        __bf16 t[TERMS];
+        split_terms<TERMS>(x[e], t);
+#pragma unroll
+        for (int n = 0; n < TERMS; ++n) p[n].p[k][e] = t[n];
+      }
+    }
   }
 }
 
@@ -135,11 +167,10 @@ __device__ __forceinline__ void split_keys(const AttnArgs& a, const TileRows& t,
   k1 = t.lo + (int)min(n, b + per);
 }
 
-// Row rr (of rows * group) of the sequence: DP / 16 values from column c on, and its statistics.
-template <int DP, bool F32>
+// N values of row rr (of rows * group) of the sequence from column c on, and its statistics.
+template <int N, bool F32>
 __device__ __forceinline__ void finish_row(const AttnArgs& a, const Span& sp, int head, int rr, int c,
                                            const float* o, float m, float l) {
-  constexpr int N = DP / 16;
   const int r = divided(rr, a.by_group);
   const int64_t row = sp.start + r;
   const int qh = head * a.group + (rr - r * a.group);
@@ -176,6 +207,15 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, const Span& sp, in
   }
   if (a.lse && c == 0)
     a.lse[row * (int64_t)(a.heads * a.group) + qh] = l == 0.0f ? kNegInf : m * kLn2 + logf(l);
+}
+
+// The same for a split: its part in the workspace.
+template <int N, int DP>
+__device__ __forceinline__ void store_part(const AttnArgs& a, int64_t at, int c, const float* v, float m, float l) {
+  float* d = a.parts + at * DP + c;
+#pragma unroll
+  for (int n = 0; n < N; n += 4) *reinterpret_cast<float4*>(d + n) = make_float4(v[n], v[n + 1], v[n + 2], v[n + 3]);
+  if (c == 0) a.stats[at] = make_float2(m, l);
 }
 
 // One of the two caches, at the workgroup's head.
@@ -332,7 +372,7 @@ __device__ __forceinline__ void columns_of(const uint32_t (&w)[8], F&& use) {
 // step s, as the keys' rows are loaded.
 template <int STEPS, int TERMS>
 __device__ __forceinline__ void load_queries(const AttnArgs& a, const TileRows& t, int head, int r16, int g,
-                                             Frag (&q)[STEPS][TERMS], int& pos) {
+                                             Frag (&q)[STEPS][TERMS], int& pos) {  // (r16: the row in the tile)
   constexpr bool F32 = TERMS == 3;
   constexpr int DT = F32 ? GPTQ_F32 : GPTQ_BF16;
   // (rows behind the tile's last are its first one's: nothing of them is stored)
@@ -340,32 +380,32 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const TileRows& 
   pos = t.sp.length - t.sp.rows + r;
   const char* p = a.q + ((int64_t)(t.sp.start + r) * a.qt + (int64_t)(head * a.group + (rr - r * a.group)) * a.qh) * (F32 ? 4 : 2);
   Raw8<DT> raw[STEPS];
-  if (a.qvec) {
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      const int c = 64 * (s / 2) + 16 * g + 8 * (s % 2);
-      const uint32_t keep = c < a.dim ? ~0u : 0u;  // (head_dim is a multiple of 16)
-      const uint4* x = reinterpret_cast<const uint4*>(p + (c < a.dim ? c : 0) * (F32 ? 4 : 2));
+  for (int s = 0; s < STEPS; ++s) {
+    const int c = 64 * (s / 2) + 16 * g + 8 * (s % 2);
+    const bool in = c < a.dim;  // (head_dim is a multiple of 16)
+    const char* x = p + (in ? c : 0) * (F32 ? 4 : 2);
+    if (a.qvec) {
 #pragma unroll
-      for (int k = 0; k < (F32 ? 2 : 1); ++k) {
-        const uint4 y = x[k];
-        raw[s].w[4 * k] = y.x & keep; raw[s].w[4 * k + 1] = y.y & keep;
-        raw[s].w[4 * k + 2] = y.z & keep; raw[s].w[4 * k + 3] = y.w & keep;
+      for (int k = 0; k < (F32 ? 2 : 1); ++k) load_words<4>(reinterpret_cast<const uint8_t*>(x) + 16 * k, raw[s].w + 4 * k);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if constexpr (F32) raw[s].w[k] = reinterpret_cast<const uint32_t*>(x)[k];
+        else if (k % 2 == 0) raw[s].w[k / 2] = reinterpret_cast<const uint16_t*>(x)[k] | (uint32_t)reinterpret_cast<const uint16_t*>(x)[k + 1] << 16;
       }
     }
-  } else {
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) raw[s] = load_raw8<DT>(p, 64 * (s / 2) + 16 * g + 8 * (s % 2), a.dim, false);
+    if (!in) raw[s] = {};
   }
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
     if constexpr (F32) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        float tm[TERMS];
+        __bf16 tm[TERMS];
         split_terms<TERMS>(__uint_as_float(raw[s].w[e]), tm);
 #pragma unroll
-        for (int k = 0; k < TERMS; ++k) q[s][k].v[e] = (__bf16)tm[k];
+        for (int k = 0; k < TERMS; ++k) q[s][k].v[e] = tm[k];
       }
     } else {
 #pragma unroll
@@ -463,18 +503,18 @@ __global__ __launch_bounds__(kThreads, MT == 1 && DP <= 128 && !F32 ? 3 : 1) voi
     float ks[2][4], vs[2][4];
     spread<EVEN>(ksc, ks);
     // S^T = K Q^T: two tiles of 16 keys
-    f32x4 s[2][MT];
+    f32x4 s[MT][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) s[u][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int mt = 0; mt < MT; ++mt) s[mt][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int st = 0; st < STEPS; ++st) {
         const Frag f = frag_of<FMT>(kraw[u][2 * st], kraw[u][2 * st + 1]);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int k = 0; k < TERMS; ++k) s[u][mt] = mfma(f, q[mt][st][k], s[u][mt]);
+          for (int k = 0; k < TERMS; ++k) s[mt][u] = mfma(f, q[mt][st][k], s[mt][u]);
       }
     }
     // scores of the lane's row, keys 16 u + 4 g + i (scaled before any branch: a branch between a
@@ -484,7 +524,7 @@ __global__ __launch_bounds__(kThreads, MT == 1 && DP <= 128 && !F32 ? 3 : 1) voi
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[u][mt][i] *= ks[u][i] * a.scale;
+        for (int i = 0; i < 4; ++i) s[mt][u][i] *= ks[u][i] * a.scale;
     const Place<EVEN> at = now;
     if (k1 < ke) {
       now = place_of<EVEN>(a, ahead, k1, ke, bad);
@@ -524,7 +564,7 @@ __global__ __launch_bounds__(kThreads, MT == 1 && DP <= 128 && !F32 ? 3 : 1) voi
             const int key = k0 + 16 * u + 4 * g + i;
             if (a.causal && (key > pos[mt] || (a.window > 0 && key <= pos[mt] - a.window)))
               seen[mt] &= ~(1u << (4 * u + i));
-            if (!(seen[mt] >> (4 * u + i) & 1)) s[u][mt][i] = kNegInf;
+            if (!(seen[mt] >> (4 * u + i) & 1)) s[mt][u][i] = kNegInf;
           }
       }
     }
@@ -532,8 +572,8 @@ __global__ __launch_bounds__(kThreads, MT == 1 && DP <= 128 && !F32 ? 3 : 1) voi
     Frag p[MT][TERMS];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      float mx = fmaxf(fmaxf(fmaxf(s[0][mt][0], s[0][mt][1]), fmaxf(s[0][mt][2], s[0][mt][3])),
-                       fmaxf(fmaxf(s[1][mt][0], s[1][mt][1]), fmaxf(s[1][mt][2], s[1][mt][3])));
+      float mx = fmaxf(fmaxf(fmaxf(s[mt][0][0], s[mt][0][1]), fmaxf(s[mt][0][2], s[mt][0][3])),
+                       fmaxf(fmaxf(s[mt][1][0], s[mt][1][1]), fmaxf(s[mt][1][2], s[mt][1][3])));
       mx = fmaxf(mx, lane_xorf<16>(mx));
       mx = fmaxf(mx, lane_xorf<32>(mx));
       const float mn = fmaxf(m[mt], mx);
@@ -543,19 +583,8 @@ __global__ __launch_bounds__(kThreads, MT == 1 && DP <= 128 && !F32 ? 3 : 1) voi
       l[mt] *= alpha;
 #pragma unroll
       for (int n = 0; n < NT; ++n) o[n][mt] *= alpha;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float e = __builtin_amdgcn_exp2f(s[u][mt][i] - base);
-          l[mt] += e;
-          float x = e * vs[u][i];
-          if (partial && !(seen[mt] >> (4 * u + i) & 1)) x = 0.0f;  // (a scale may be anything there)
-          float tm[TERMS];
-          split_terms<TERMS>(x, tm);
-#pragma unroll
-          for (int k = 0; k < TERMS; ++k) p[mt][k].v[4 * u + i] = (__bf16)tm[k];
-        }
+      if (partial) weights_of<true, TERMS>(s[mt], vs, seen[mt], base, l[mt], p[mt]);
+      else weights_of<false, TERMS>(s[mt], vs, 0, base, l[mt], p[mt]);
     }
     // masked places may hold e4m3's NaN: it must reach the rows that see it, and no other
     if (FMT == GPTQ_KV_E4M3 && partial) {
@@ -642,13 +671,315 @@ __global__ __launch_bounds__(kThreads, MT == 1 && DP <= 128 && !F32 ? 3 : 1) voi
     }
     if (16 * mt + row >= t.rows) continue;
     if (a.splits == 1) {
-      finish_row<DP, F32>(a, t.sp, head, t.row0 + 16 * mt + row, c, v, mx, tl);
+      finish_row<NT, F32>(a, t.sp, head, t.row0 + 16 * mt + row, c, v, mx, tl);
     } else {
-      const int64_t at = part * (16 * MT) + 16 * mt + row;
-      float* d = a.parts + at * DP + c;
+      store_part<NT, DP>(a, part * (16 * MT) + 16 * mt + row, c, v, mx, tl);
+    }
+  }
+}
+
+// Many rows: a workgroup takes 64 MT rows, each wave 16 MT of them, over tiles of 8192 / DP keys.
+// What a tile's codes become on the way to the matrix instructions is the same for all rows, so
+// the waves share that work: each converts a quarter of a tile to operands (two 16-byte pieces of
+// 16 keys, one 4-byte column of 32 values), which lie in LDS as the lanes take them, 16 bytes each
+// in order, without conflicts.  Two tiles alternate; while one is multiplied, the codes of the
+// next are on their way, and the places of the one behind it are looked up, a key a thread.
+// An operand read from LDS feeds MT matrix instructions: 4 waves read 1 KB each in 16 MT cycles.
+//
+// The running maximum is a reference that is at most 2^kSlack below the true one: scores are
+// compared with it lane by lane, and only where one of a wave passes it (the first tiles) are
+// maxima exchanged and sums rescaled.  The weights are then up to 2^kSlack, which fp32 sums and
+// bf16 weights hold as well as 1.
+constexpr float kSlack = 8.0f;
+
+template <int DP>
+struct TileShared {
+  static constexpr int KEYS = 8192 / DP;
+  uint4 k[2][KEYS / 16][DP / 32][64];  // operands of both products
+  uint4 v[2][KEYS / 32][DP / 16][64];
+  float ks[2][KEYS], vs[2][KEYS];
+  int64_t kat[2][KEYS], vat[2][KEYS];  // where a key's codes begin
+  uint8_t there[2][KEYS];              // 0: no such key
+  uint8_t nan[2][KEYS][DP / 4];        // bit n: value 4 c + n of a key is e4m3's NaN (and 0 in v), where
+  uint32_t odd[2];                     // bit w: wave w's part of the values has any; bit 4: a key is not there
+};
+
+template <int DP, int FMT, bool F32, int MT>
+__global__ __launch_bounds__(kThreads, DP == 256 && !F32 ? 1 : 2) void kv_attention_tile_kernel(AttnArgs a) {
+  constexpr int TERMS = F32 ? 3 : 1;
+  constexpr int STEPS = DP / 32, NT = DP / 16, P = DP / 64;
+  constexpr int KEYS = TileShared<DP>::KEYS;
+  extern __shared__ __align__(16) char shared_bytes[];
+  TileShared<DP>& sh = *reinterpret_cast<TileShared<DP>*>(shared_bytes);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c16 = lane & 15, g = lane >> 4;
+  // heads run fastest, so that the tiles of a head meet in one L2; the last tiles, which have the
+  // most keys where masked, come first
+  const int task = (int)(gridDim.x / a.heads) - 1 - (int)(blockIdx.x / a.heads), head = (int)(blockIdx.x % a.heads);
+  const TileRows t = tile_rows(a, task, 64 * MT);
+  if (t.rows <= 0) return;
+  int kb, ke;
+  split_keys(a, t, (int)blockIdx.z, kb, ke);
+  const int32_t* table = a.s.table + t.sp.seq * a.s.ldt;
+  const Side kc = side_of(a.k, head), vc = side_of(a.v, head);
+
+  Frag q[MT][STEPS][TERMS];
+  int pos[MT];
 #pragma unroll
-      for (int n = 0; n < NT; n += 4) *reinterpret_cast<float4*>(d + n) = make_float4(v[n], v[n + 1], v[n + 2], v[n + 3]);
-      if (c == 0) a.stats[at] = make_float2(mx, tl);
+  for (int mt = 0; mt < MT; ++mt)
+    load_queries<STEPS, TERMS>(a, t, head, 16 * (MT * wave + mt) + c16, g, q[mt], pos[mt]);
+  const int w0 = min(16 * MT * wave, t.rows - 1), w1 = min(16 * MT * (wave + 1), t.rows) - 1;
+  const bool idle = 16 * MT * wave >= t.rows;
+  const int pos_first = t.sp.length - t.sp.rows + divided(t.row0 + w0, a.by_group);
+  const int pos_last = t.sp.length - t.sp.rows + divided(t.row0 + max(w0, w1), a.by_group);
+
+  // this wave's part of the conversion
+  const int ku[2] = {(2 * wave) / P, (2 * wave + 1) / P}, kp[2] = {(2 * wave) % P, (2 * wave + 1) % P};
+  const int vh = wave / P, vw = wave % P;
+  // (columns behind head_dim: the row's first ones, whose queries and outputs are not there)
+  int ck[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) ck[i] = 64 * kp[i] + 16 * g < a.dim ? 64 * kp[i] + 16 * g : 0;
+  const int cv = 64 * vw + 4 * c16 < a.dim ? 64 * vw + 4 * c16 : 0;
+  uint32_t kraw[2][4], vraw[8];
+  auto load_codes = [&](int b) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) load_words<4>(kc.codes + sh.kat[b][16 * ku[i] + c16] + ck[i], kraw[i]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      load_words<1>(vc.codes + sh.vat[b][32 * vh + 16 * (i / 4) + 4 * g + i % 4] + cv, vraw + i);
+  };
+  auto convert = [&](int b) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        const Frag f = frag_of<FMT>(kraw[i][2 * st], kraw[i][2 * st + 1]);
+        sh.k[b][ku[i]][2 * kp[i] + st][lane] = make_uint4(f.w[0], f.w[1], f.w[2], f.w[3]);
+      }
+    if (FMT == GPTQ_KV_E4M3) {
+      uint32_t any = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) any |= nan_bytes(vraw[i]);
+      if (__any(any != 0)) {  // no operand holds a NaN, which would reach every row
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t x = nan_bytes(vraw[i]);
+          vraw[i] &= ~x;
+          sh.nan[b][32 * vh + 16 * (i / 4) + 4 * g + i % 4][16 * vw + c16] =
+              (uint8_t)((x & 1u) | (x >> 7 & 2u) | (x >> 14 & 4u) | (x >> 21 & 8u));
+        }
+        if (lane == 0) atomicOr(&sh.odd[b], 1u << wave);
+      }
+    }
+    columns_of<FMT>(vraw, [&](int n, const Frag& f) {
+      sh.v[b][vh][4 * vw + n][lane] = make_uint4(f.w[0], f.w[1], f.w[2], f.w[3]);
+    });
+  };
+  // places: thread i looks up key i of a tile, its table entry a round ahead
+  const bool looks = tid < KEYS;
+  bool bad = false;
+  float ksc = 0.0f, vsc = 0.0f;
+  bool known = false;
+  auto entry_of = [&](int k0) {
+    return looks ? table[min(divided(min(k0 + tid, ke - 1), a.s.by_page), a.s.width - 1)] : 0;
+  };
+  auto look_up = [&](int k0, int e, int b) {  // (its scales go to LDS with the tile's operands)
+    if (!looks) return;
+    const int kk = min(k0 + tid, ke - 1), entry = divided(kk, a.s.by_page);
+    const bool ok = entry < a.s.width && (uint32_t)e < (uint32_t)a.s.pages;
+    bad = bad || (k0 + tid < ke && !ok);
+    known = k0 + tid < ke && ok;
+    const int page = ok ? e : 0, slot = kk - entry * a.s.page_size, blk = divided(slot, a.s.by_block);
+    sh.kat[b][tid] = page * kc.cpage + (int64_t)slot * kc.cslot;
+    sh.vat[b][tid] = page * vc.cpage + (int64_t)slot * vc.cslot;
+    ksc = kc.scales[page * kc.ppage + (int64_t)blk * kc.pblock];
+    vsc = vc.scales[page * vc.ppage + (int64_t)blk * vc.pblock];
+  };
+  auto put_scales = [&](int b) {
+    if (!looks) return;
+    sh.ks[b][tid] = ksc * a.scale;
+    sh.vs[b][tid] = vsc;
+    sh.there[b][tid] = known;
+    if (!known) atomicOr(&sh.odd[b], 16u);
+  };
+
+  f32x4 o[NT][MT];
+  float m[MT], l[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    m[mt] = kNegInf;
+    l[mt] = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) o[n][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+
+  if (kb < ke) {  // the first tile, the second one's places, the third one's entries
+    if (tid < 2) sh.odd[tid] = 0;
+    look_up(kb, entry_of(kb), 0);
+    __syncthreads();
+    load_codes(0);
+    put_scales(0);
+    look_up(kb + KEYS, entry_of(kb + KEYS), 1);
+    convert(0);
+  }
+  int e = kb < ke ? entry_of(kb + 2 * KEYS) : 0;
+  for (int k0 = kb, b = 0; k0 < ke; k0 += KEYS, b ^= 1) {
+    __syncthreads();  // tile b's operands, the next one's places
+    const uint32_t odd = __builtin_amdgcn_readfirstlane(sh.odd[b]);
+    load_codes(b ^ 1);  // (behind the last tile: somewhere)
+#pragma unroll 1
+    for (int h = 0; h < KEYS / 32; ++h) {
+      const int kh = k0 + 32 * h;
+      // keys that none of the wave's rows sees
+      if (idle || kh >= ke || (a.causal && (kh > pos_last || (a.window > 0 && kh + 31 <= pos_first - a.window)))) continue;
+      f32x4 s[MT][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) s[mt][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int st = 0; st < STEPS; ++st) {
+          const uint4 w = sh.k[b][2 * h + u][st][lane];
+          Frag f;
+          f.w[0] = w.x; f.w[1] = w.y; f.w[2] = w.z; f.w[3] = w.w;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int k = 0; k < TERMS; ++k) s[mt][u] = mfma(f, q[mt][st][k], s[mt][u]);
+        }
+      }
+      float vs[2][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float4 x = *reinterpret_cast<const float4*>(&sh.ks[b][32 * h + 16 * u + 4 * g]);
+        const float4 y = *reinterpret_cast<const float4*>(&sh.vs[b][32 * h + 16 * u + 4 * g]);
+        vs[u][0] = y.x; vs[u][1] = y.y; vs[u][2] = y.z; vs[u][3] = y.w;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          s[mt][u][0] *= x.x; s[mt][u][1] *= x.y; s[mt][u][2] *= x.z; s[mt][u][3] *= x.w;
+        }
+      }
+      const bool partial = (odd & 16u) || kh + 32 > ke ||
+                           (a.causal && (kh + 32 > pos_first + 1 || (a.window > 0 && kh <= pos_last - a.window)));
+      uint32_t seen[MT];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) seen[mt] = 0xFF;
+      if (partial) {
+        uint32_t there = 0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) there |= (sh.there[b][32 * h + 16 * u + 4 * g + i] ? 1u : 0u) << (4 * u + i);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          seen[mt] = there;
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int key = kh + 16 * u + 4 * g + i;
+              if (a.causal && (key > pos[mt] || (a.window > 0 && key <= pos[mt] - a.window)))
+                seen[mt] &= ~(1u << (4 * u + i));
+              if (!(seen[mt] >> (4 * u + i) & 1)) s[mt][u][i] = kNegInf;
+            }
+        }
+      }
+      float mx[MT];
+      bool grows = false;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        mx[mt] = fmaxf(fmaxf(fmaxf(s[mt][0][0], s[mt][0][1]), fmaxf(s[mt][0][2], s[mt][0][3])),
+                       fmaxf(fmaxf(s[mt][1][0], s[mt][1][1]), fmaxf(s[mt][1][2], s[mt][1][3])));
+        grows = grows || mx[mt] > m[mt] + kSlack;  // (any score passes -inf)
+      }
+      if (__any(grows)) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          float x = fmaxf(mx[mt], lane_xorf<16>(mx[mt]));
+          x = fmaxf(x, lane_xorf<32>(x));
+          const float mn = fmaxf(m[mt], x);
+          const float alpha = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[mt] - mn);
+          m[mt] = mn;
+          l[mt] *= alpha;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) o[n][mt] *= alpha;
+        }
+      }
+      Frag p[MT][TERMS];
+      if (partial) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+          weights_of<true, TERMS>(s[mt], vs, seen[mt], m[mt] == kNegInf ? 0.0f : m[mt], l[mt], p[mt]);
+      } else {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) weights_of<false, TERMS>(s[mt], vs, 0, m[mt], l[mt], p[mt]);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint4 w = sh.v[b][h][n][lane];
+        Frag f;
+        f.w[0] = w.x; f.w[1] = w.y; f.w[2] = w.z; f.w[3] = w.w;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int k = 0; k < TERMS; ++k) o[n][mt] = mfma(f, p[mt][k], o[n][mt]);
+      }
+      if (FMT == GPTQ_KV_E4M3 && (odd >> (P * h) & ((1u << P) - 1)) != 0) {
+        // a NaN among the values reaches the rows that see its key
+        __asm__ volatile("s_nop 15" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll 1
+        for (int key = 0; key < 32; ++key) {
+          bool sees[MT];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            sees[mt] = __shfl((int)seen[mt], 16 * (key % 16 / 4) + c16) >> (4 * (key / 16) + key % 4) & 1;
+#pragma unroll
+          for (int w = 0; w < P; ++w) {
+            if ((odd >> (P * h + w) & 1u) == 0) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t x = sh.nan[b][32 * h + key][16 * w + 4 * g + i];
+#pragma unroll
+              for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                  if (sees[mt] && (x >> n & 1u)) o[4 * w + n][mt][i] = __builtin_nanf("");
+            }
+          }
+        }
+      }
+    }
+    __syncthreads();  // (everyone has read tile b's mark and places)
+    if (tid == 0) sh.odd[b] = 0;
+    put_scales(b ^ 1);
+    convert(b ^ 1);
+    look_up(k0 + 2 * KEYS, e, b);
+    e = entry_of(k0 + 3 * KEYS);
+  }
+  // (the loop's branch stands between the last product and its readers: wait the product's length)
+  __asm__ volatile("s_nop 15" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  if (bad && a.s.info) *a.s.info = 1;
+
+  const int64_t part = ((int64_t)task * a.heads + head) * a.splits + blockIdx.z;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int row = 16 * (MT * wave + mt) + c16;
+    float sum = l[mt];
+    sum += lane_xorf<16>(sum);
+    sum += lane_xorf<32>(sum);
+    if (row >= t.rows) continue;
+#pragma unroll
+    for (int w = 0; w < P; ++w) {
+      float v[16];  // columns 64 w + 16 g + 4 i + n
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) v[4 * i + n] = o[4 * w + n][mt][i];
+      if (a.splits == 1) finish_row<16, F32>(a, t.sp, head, t.row0 + row, 64 * w + 16 * g, v, m[mt], sum);
+      else store_part<16, DP>(a, part * (64 * MT) + row, 64 * w + 16 * g, v, m[mt], sum);
     }
   }
 }
@@ -700,31 +1031,58 @@ __global__ __launch_bounds__(kThreads) void kv_attention_join_kernel(AttnArgs a,
         }
       }
     }
-    finish_row<DP, F32>(a, t.sp, head, t.row0 + row, c, v, m, l);
+    finish_row<NT, F32>(a, t.sp, head, t.row0 + row, c, v, m, l);
   }
 }
 
 int padded_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
 struct Plan {
-  int mt;       // tiles of 16 rows
+  bool tiles;   // the tile kernel
+  int mt;       // 16 rows each, of a wave
+  int per;      // rows of a workgroup
   int64_t tasks;
   int splits;
 };
 
+// rows of a wave in the tile kernel: as many as 256 registers hold
+int tile_mt(int dp, bool f32) { return dp == 256 ? (f32 ? 1 : 2) : f32 ? 2 : 3; }
+
 Plan plan_of(const gptq_kv_blocks* c, int q_heads, int dt, int64_t tokens, int64_t seqs, int64_t width) {
   Plan p;
+  const bool f32 = dt == GPTQ_F32;
+  const int dp = padded_dim(c->head_dim);
   const int64_t group = q_heads / c->heads;
   const int64_t each = ceil_div(tokens * group, seqs);  // rows of a sequence on average
-  p.mt = each > 16 && dt == GPTQ_BF16 && c->head_dim <= 128 ? 4 : 1;
-  p.tasks = tokens * group / (16 * p.mt) + seqs;
+  p.tiles = each > 64;
+  p.mt = p.tiles ? tile_mt(dp, f32) : each > 16 && !f32 && dp <= 128 ? 4 : 1;
+  p.per = p.tiles ? 64 * p.mt : 16 * p.mt;
+  p.tasks = tokens * group / p.per + seqs;
   // Splits: as many as give 512 workgroups, two a CU, whose waves' loads fill the memory's queue
   // (16 sequences of 12000, 8 heads of 128: 128 workgroups 115 us, 512 80, 768 88, 1024 91, 2048 87),
   // 512 keys each at least (5 sequences of 300: one 10.1 us, two and their join 13.5).
-  const int64_t tiles = hmin(p.tasks, seqs * ceil_div(each, int64_t(16) * p.mt)) * c->heads;
+  const int64_t tiles = hmin(p.tasks, seqs * ceil_div(each, p.per)) * c->heads;
   const int64_t keys = hmin(width * c->page_size, int64_t(1) << 30);
   p.splits = (int)hmax(1, hmin(hmin(ceil_div(512, tiles), 64), keys / 512));
   return p;
+}
+
+template <int DP, int FMT, bool F32, int MT>
+hipError_t launch_tiles(const AttnArgs& a, const dim3& grid, hipStream_t stream) {
+  auto* kernel = kv_attention_tile_kernel<DP, FMT, F32, MT>;
+  constexpr int bytes = (int)sizeof(TileShared<DP>);
+  // (more than 64 KB of LDS has to be asked for; the same each time)
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kernel, grid, dim3(kThreads), bytes, stream, a);
+  return hipGetLastError();
+}
+
+template <int FMT, bool F32>
+hipError_t launch_tiles_of(int dp, const AttnArgs& a, const dim3& grid, hipStream_t stream) {
+  if (dp == 64) return launch_tiles<64, FMT, F32, F32 ? 2 : 3>(a, grid, stream);
+  if (dp == 128) return launch_tiles<128, FMT, F32, F32 ? 2 : 3>(a, grid, stream);
+  return launch_tiles<256, FMT, F32, F32 ? 1 : 2>(a, grid, stream);
 }
 
 }  // namespace
@@ -733,7 +1091,7 @@ size_t kv_attention_ws_bytes(const gptq_kv_blocks* c, int q_heads, int dt, int64
                              int64_t seqs, int64_t width) {
   const Plan p = plan_of(c, q_heads, dt, tokens, seqs, width);
   if (p.splits == 1) return 0;
-  return (size_t)p.tasks * c->heads * p.splits * 16 * p.mt * (padded_dim(c->head_dim) + 2) * 4;
+  return (size_t)p.tasks * c->heads * p.splits * p.per * (padded_dim(c->head_dim) + 2) * 4;
 }
 
 hipError_t launch_kv_attention(const KvAttention& t, const KvSequences& seqs,
@@ -760,13 +1118,22 @@ hipError_t launch_kv_attention(const KvAttention& t, const KvSequences& seqs,
   a.ovec = (reinterpret_cast<uintptr_t>(t.out.p) & 15) == 0 && a.ot % per16 == 0 && a.oh % per16 == 0;
   a.scale = t.scale * kLog2e;
   a.splits = p.splits;
-  a.by_rows = divisor_of(16 * p.mt);
+  a.by_rows = divisor_of(p.per);
   a.by_group = divisor_of(a.group);
   a.by_splits = divisor_of(p.splits);
   a.stats = static_cast<float2*>(ws);
-  a.parts = reinterpret_cast<float*>(a.stats + p.tasks * kb->heads * p.splits * 16 * p.mt);
+  a.parts = reinterpret_cast<float*>(a.stats + p.tasks * kb->heads * p.splits * p.per);
   const bool even = kb->page_size % 16 == 0 && kb->block % 16 == 0;
-  const dim3 grid((unsigned)p.tasks, (unsigned)kb->heads, (unsigned)p.splits), block(kThreads);
+  const dim3 block(kThreads);
+  if (p.tiles) {
+    const dim3 tgrid((unsigned)(p.tasks * kb->heads), 1, (unsigned)p.splits);
+    const hipError_t e =
+        kb->format == GPTQ_KV_E4M3
+            ? (f32 ? launch_tiles_of<GPTQ_KV_E4M3, true>(dp, a, tgrid, stream) : launch_tiles_of<GPTQ_KV_E4M3, false>(dp, a, tgrid, stream))
+            : (f32 ? launch_tiles_of<GPTQ_KV_INT8, true>(dp, a, tgrid, stream) : launch_tiles_of<GPTQ_KV_INT8, false>(dp, a, tgrid, stream));
+    if (e != hipSuccess) return e;
+  }
+  const dim3 grid((unsigned)p.tasks, (unsigned)kb->heads, (unsigned)p.splits);
 #define GPTQ_ATTN_E(DP, F, W, MT)                                                                  \
   do {                                                                                             \
     if (even) hipLaunchKernelGGL((kv_attention_kernel<DP, F, W, MT, true>), grid, block, 0, stream, a); \
@@ -783,7 +1150,8 @@ hipError_t launch_kv_attention(const KvAttention& t, const KvSequences& seqs,
     else if (p.mt == 1) GPTQ_ATTN_F(DP, false, 1); \
     else GPTQ_ATTN_F(DP, false, 4);           \
   } while (0)
-  if (dp == 64) GPTQ_ATTN(64);
+  if (p.tiles) {}
+  else if (dp == 64) GPTQ_ATTN(64);
   else if (dp == 128) GPTQ_ATTN(128);
   else if (f32) GPTQ_ATTN_F(256, true, 1);
   else GPTQ_ATTN_F(256, false, 1);
@@ -794,8 +1162,8 @@ hipError_t launch_kv_attention(const KvAttention& t, const KvSequences& seqs,
     const dim3 jgrid((unsigned)p.tasks, (unsigned)kb->heads);
 #define GPTQ_JOIN(DP)                                                                                     \
   do {                                                                                                    \
-    if (f32) hipLaunchKernelGGL((kv_attention_join_kernel<DP, true>), jgrid, block, 0, stream, a, 16 * p.mt); \
-    else hipLaunchKernelGGL((kv_attention_join_kernel<DP, false>), jgrid, block, 0, stream, a, 16 * p.mt);    \
+    if (f32) hipLaunchKernelGGL((kv_attention_join_kernel<DP, true>), jgrid, block, 0, stream, a, p.per); \
+    else hipLaunchKernelGGL((kv_attention_join_kernel<DP, false>), jgrid, block, 0, stream, a, p.per);    \
   } while (0)
     if (dp == 64) GPTQ_JOIN(64);
     else if (dp == 128) GPTQ_JOIN(128);
