@@ -76,10 +76,12 @@ __device__ __forceinline__ uint32_t signed_codes(uint32_t w) {
   return FMT == GPTQ_KV_INT8 ? w ^ 0x80808080u : w;
 }
 
+// bit 7 of each byte of w that is e4m3's NaN (the other bits: anything)
+__device__ __forceinline__ uint32_t nan_marks(uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u; }
+
 // bytes of w that are e4m3's NaN, as 0xFF
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
-  const uint32_t t = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-  return (t >> 7) * 255u;
+  return ((nan_marks(w) & 0x80808080u) >> 7) * 255u;
 }
 
 __device__ __forceinline__ f32x4 mfma(const Frag& a, const Frag& b, f32x4 c) {
@@ -101,6 +103,36 @@ __device__ __forceinline__ void split_terms(float x, __bf16 (&t)[TERMS]) {
   }
 }
 
+// All ones where bit k of `bits` is set, else 0 (masks of lanes in scalar registers, one for each
+// of so many values, would crowd out what is kept there).
+__device__ __forceinline__ uint32_t spread_bit(uint32_t bits, int k) { return (uint32_t)((int32_t)(bits << (31 - k)) >> 31); }
+__device__ __forceinline__ float kept(float x, uint32_t mask) { return __uint_as_float(__float_as_uint(x) & mask); }
+__device__ __forceinline__ float kept_or_neg_inf(float x, uint32_t mask) {
+  return __uint_as_float((__float_as_uint(x) & mask) | (0xFF800000u & ~mask));
+}
+
+// The largest of 8 (written out: the compiler would first turn each that went through a mask into a
+// quiet number, 8 instructions more).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  __asm__("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+__device__ __forceinline__ float max_of(const f32x4 (&s)[2]) {
+  return max3(max3(max3(s[0][0], s[0][1], s[0][2]), s[0][3], s[1][0]), s[1][1], max3(s[1][2], s[1][3], s[1][3]));
+}
+
+// Which of the keys base + 16 u + i (u < 2, i < 4; bit 4 u + i) lie in lo .. hi.
+__device__ __forceinline__ uint32_t keys_between(int base, int lo, int hi) {
+  uint32_t bits = 0;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int to = min(max(hi - base - 16 * u + 1, 0), 4), from = min(max(lo - base - 16 * u, 0), 4);
+    bits |= (((1u << to) - 1) & ~((1u << from) - 1)) << (4 * u);
+  }
+  return bits;
+}
+
 // The weights of one row, keys 16 u + 4 g + i, as the second product's operands: e^(s - base) times
 // the values' scales; their sum is added to l.  MASKED: a weight whose key is not seen is 0, whatever
 // its scale is (apart from the other form, which costs half as many instructions).
@@ -116,7 +148,7 @@ __device__ __forceinline__ void weights_of(const f32x4 (&s)[2], const float (&vs
       const float w = __builtin_amdgcn_exp2f(s[u][i] - base);
       l += w;
       x[e] = w * vs[u][i];
-      if (MASKED) x[e] = (seen >> (4 * u + i) & 1) ? x[e] : 0.0f;
+      if (MASKED) x[e] = kept(x[e], spread_bit(seen, 4 * u + i));
     }
     if constexpr (TERMS == 1) {
       p[0].p[k][0] = (__bf16)x[0];
@@ -557,15 +589,11 @@ __global__ __launch_bounds__(kThreads, MT == 1 && DP <= 128 && !F32 ? 3 : 1) voi
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         seen[mt] = there;
+        if (a.causal) seen[mt] &= keys_between(k0 + 4 * g, a.window > 0 ? pos[mt] - a.window + 1 : 0, pos[mt]);
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = k0 + 16 * u + 4 * g + i;
-            if (a.causal && (key > pos[mt] || (a.window > 0 && key <= pos[mt] - a.window)))
-              seen[mt] &= ~(1u << (4 * u + i));
-            if (!(seen[mt] >> (4 * u + i) & 1)) s[mt][u][i] = kNegInf;
-          }
+          for (int i = 0; i < 4; ++i) s[mt][u][i] = kept_or_neg_inf(s[mt][u][i], spread_bit(seen[mt], 4 * u + i));
       }
     }
     // running maximum, probabilities, P^T as the second product's operand
@@ -592,8 +620,8 @@ __global__ __launch_bounds__(kThreads, MT == 1 && DP <= 128 && !F32 ? 3 : 1) voi
 #pragma unroll
       for (int w = 0; w < VW; ++w)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) any |= nan_bytes(vraw[w][i]);
-      if (__any(any != 0)) {
+        for (int i = 0; i < 8; ++i) any |= nan_marks(vraw[w][i]);
+      if (__any((any & 0x80808080u) != 0)) {
         Frag ind[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -701,11 +729,11 @@ struct TileShared {
   int64_t kat[2][KEYS], vat[2][KEYS];  // where a key's codes begin
   uint8_t there[2][KEYS];              // 0: no such key
   uint8_t nan[2][KEYS][DP / 4];        // bit n: value 4 c + n of a key is e4m3's NaN (and 0 in v), where
-  uint32_t odd[2];                     // bit w: wave w's part of the values has any; bit 4: a key is not there
+  uint32_t odd[3];                     // (tiles in turn) bit w: wave w's part of the values has any; bit 4: a key is not there
 };
 
 template <int DP, int FMT, bool F32, int MT>
-__global__ __launch_bounds__(kThreads, DP == 256 && !F32 ? 1 : 2) void kv_attention_tile_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, DP == 256 && F32 ? 1 : 2) void kv_attention_tile_kernel(AttnArgs a) {
   constexpr int TERMS = F32 ? 3 : 1;
   constexpr int STEPS = DP / 32, NT = DP / 16, P = DP / 64;
   constexpr int KEYS = TileShared<DP>::KEYS;
@@ -749,7 +777,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 && !F32 ? 1 : 2) void kv_attent
     for (int i = 0; i < 8; ++i)
       load_words<1>(vc.codes + sh.vat[b][32 * vh + 16 * (i / 4) + 4 * g + i % 4] + cv, vraw + i);
   };
-  auto convert = [&](int b) {
+  auto convert = [&](int b, int mark) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -760,8 +788,8 @@ __global__ __launch_bounds__(kThreads, DP == 256 && !F32 ? 1 : 2) void kv_attent
     if (FMT == GPTQ_KV_E4M3) {
       uint32_t any = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) any |= nan_bytes(vraw[i]);
-      if (__any(any != 0)) {  // no operand holds a NaN, which would reach every row
+      for (int i = 0; i < 8; ++i) any |= nan_marks(vraw[i]);
+      if (__any((any & 0x80808080u) != 0)) {  // no operand holds a NaN, which would reach every row
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const uint32_t x = nan_bytes(vraw[i]);
@@ -769,64 +797,68 @@ __global__ __launch_bounds__(kThreads, DP == 256 && !F32 ? 1 : 2) void kv_attent
           sh.nan[b][32 * vh + 16 * (i / 4) + 4 * g + i % 4][16 * vw + c16] =
               (uint8_t)((x & 1u) | (x >> 7 & 2u) | (x >> 14 & 4u) | (x >> 21 & 8u));
         }
-        if (lane == 0) atomicOr(&sh.odd[b], 1u << wave);
+        if (lane == 0) atomicOr(&sh.odd[mark], 1u << wave);
       }
     }
     columns_of<FMT>(vraw, [&](int n, const Frag& f) {
       sh.v[b][vh][4 * vw + n][lane] = make_uint4(f.w[0], f.w[1], f.w[2], f.w[3]);
     });
   };
-  // places: thread i looks up key i of a tile, its table entry a round ahead
-  const bool looks = tid < KEYS;
-  bool bad = false;
-  float ksc = 0.0f, vsc = 0.0f;
-  bool known = false;
+  // places: thread i looks up key i of a tile for the keys' cache, thread KEYS + i for the values',
+  // the table's entries a round ahead
+  const bool looks = tid < 2 * KEYS, of_keys = tid < KEYS;
+  const int ti = of_keys ? tid : tid - KEYS;
+  const int64_t tpage = of_keys ? kc.cpage : vc.cpage, tppage = of_keys ? kc.ppage : vc.ppage;
+  const int32_t tslot = of_keys ? kc.cslot : vc.cslot, tblock = of_keys ? kc.pblock : vc.pblock;
+  const float* const tscales = of_keys ? kc.scales : vc.scales;
+  bool bad = false, known = false;
+  float sc = 0.0f;
   auto entry_of = [&](int k0) {
-    return looks ? table[min(divided(min(k0 + tid, ke - 1), a.s.by_page), a.s.width - 1)] : 0;
+    return looks ? table[min(divided(min(k0 + ti, ke - 1), a.s.by_page), a.s.width - 1)] : 0;
   };
-  auto look_up = [&](int k0, int e, int b) {  // (its scales go to LDS with the tile's operands)
+  auto look_up = [&](int k0, int e, int b) {  // (its scale goes to LDS with the tile's operands)
     if (!looks) return;
-    const int kk = min(k0 + tid, ke - 1), entry = divided(kk, a.s.by_page);
+    const int kk = min(k0 + ti, ke - 1), entry = divided(kk, a.s.by_page);
     const bool ok = entry < a.s.width && (uint32_t)e < (uint32_t)a.s.pages;
-    bad = bad || (k0 + tid < ke && !ok);
-    known = k0 + tid < ke && ok;
+    bad = bad || (k0 + ti < ke && !ok);
+    known = k0 + ti < ke && ok;
     const int page = ok ? e : 0, slot = kk - entry * a.s.page_size, blk = divided(slot, a.s.by_block);
-    sh.kat[b][tid] = page * kc.cpage + (int64_t)slot * kc.cslot;
-    sh.vat[b][tid] = page * vc.cpage + (int64_t)slot * vc.cslot;
-    ksc = kc.scales[page * kc.ppage + (int64_t)blk * kc.pblock];
-    vsc = vc.scales[page * vc.ppage + (int64_t)blk * vc.pblock];
+    (of_keys ? sh.kat : sh.vat)[b][ti] = page * tpage + (int64_t)slot * tslot;
+    sc = tscales[page * tppage + (int64_t)blk * tblock];
   };
-  auto put_scales = [&](int b) {
+  auto put_scales = [&](int b, int mark) {
     if (!looks) return;
-    sh.ks[b][tid] = ksc * a.scale;
-    sh.vs[b][tid] = vsc;
-    sh.there[b][tid] = known;
-    if (!known) atomicOr(&sh.odd[b], 16u);
+    (of_keys ? sh.ks : sh.vs)[b][ti] = of_keys ? sc * a.scale : sc;
+    if (of_keys) sh.there[b][ti] = known;
+    if (!known) atomicOr(&sh.odd[mark], 16u);
   };
 
   f32x4 o[NT][MT];
   float m[MT], l[MT];
+  bool set[MT];  // whether a row has seen a key, and m is its reference
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
-    m[mt] = kNegInf;
-    l[mt] = 0.0f;
+    m[mt] = l[mt] = 0.0f;
+    set[mt] = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n) o[n][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
   if (kb < ke) {  // the first tile, the second one's places, the third one's entries
-    if (tid < 2) sh.odd[tid] = 0;
+    if (tid < 3) sh.odd[tid] = 0;
     look_up(kb, entry_of(kb), 0);
     __syncthreads();
     load_codes(0);
-    put_scales(0);
+    put_scales(0, 0);
     look_up(kb + KEYS, entry_of(kb + KEYS), 1);
-    convert(0);
+    convert(0, 0);
   }
   int e = kb < ke ? entry_of(kb + 2 * KEYS) : 0;
-  for (int k0 = kb, b = 0; k0 < ke; k0 += KEYS, b ^= 1) {
+  // One barrier a tile: what is written behind it belongs to the next tile's buffers, which were read
+  // last in front of it, or to marks that are read two barriers later.
+  for (int k0 = kb, b = 0, mark = 0; k0 < ke; k0 += KEYS, b ^= 1) {
     __syncthreads();  // tile b's operands, the next one's places
-    const uint32_t odd = __builtin_amdgcn_readfirstlane(sh.odd[b]);
+    const uint32_t odd = __builtin_amdgcn_readfirstlane(sh.odd[mark]);
     load_codes(b ^ 1);  // (behind the last tile: somewhere)
 #pragma unroll 1
     for (int h = 0; h < KEYS / 32; ++h) {
@@ -834,21 +866,32 @@ __global__ __launch_bounds__(kThreads, DP == 256 && !F32 ? 1 : 2) void kv_attent
       // keys that none of the wave's rows sees
       if (idle || kh >= ke || (a.causal && (kh > pos_last || (a.window > 0 && kh + 31 <= pos_first - a.window)))) continue;
       f32x4 s[MT][2];
+      {
+        uint4 kw[2][STEPS];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) s[mt][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          for (int st = 0; st < STEPS; ++st) kw[u][st] = sh.k[b][2 * h + u][st][lane];
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int st = 0; st < STEPS; ++st) {
-          const uint4 w = sh.k[b][2 * h + u][st][lane];
-          Frag f;
-          f.w[0] = w.x; f.w[1] = w.y; f.w[2] = w.z; f.w[3] = w.w;
+        for (int u = 0; u < 2; ++u) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+          for (int mt = 0; mt < MT; ++mt) s[mt][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int k = 0; k < TERMS; ++k) s[mt][u] = mfma(f, q[mt][st][k], s[mt][u]);
+          for (int st = 0; st < STEPS; ++st) {
+            Frag f;
+            f.w[0] = kw[u][st].x; f.w[1] = kw[u][st].y; f.w[2] = kw[u][st].z; f.w[3] = kw[u][st].w;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int k = 0; k < TERMS; ++k) s[mt][u] = mfma(f, q[mt][st][k], s[mt][u]);
+          }
         }
       }
+      uint4 vw_[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) vw_[n] = sh.v[b][h][n][lane];
       float vs[2][4];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -856,10 +899,13 @@ __global__ __launch_bounds__(kThreads, DP == 256 && !F32 ? 1 : 2) void kv_attent
         const float4 y = *reinterpret_cast<const float4*>(&sh.vs[b][32 * h + 16 * u + 4 * g]);
         vs[u][0] = y.x; vs[u][1] = y.y; vs[u][2] = y.z; vs[u][3] = y.w;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          s[mt][u][0] *= x.x; s[mt][u][1] *= x.y; s[mt][u][2] *= x.z; s[mt][u][3] *= x.w;
+        for (int mt = 0; mt < MT; ++mt) {  // scores relative to the row's reference
+          s[mt][u][0] = fmaf(s[mt][u][0], x.x, -m[mt]); s[mt][u][1] = fmaf(s[mt][u][1], x.y, -m[mt]);
+          s[mt][u][2] = fmaf(s[mt][u][2], x.z, -m[mt]); s[mt][u][3] = fmaf(s[mt][u][3], x.w, -m[mt]);
         }
       }
+      __builtin_amdgcn_s_setprio(0);
+      __builtin_amdgcn_sched_barrier(0);
       const bool partial = (odd & 16u) || kh + 32 > ke ||
                            (a.causal && (kh + 32 > pos_first + 1 || (a.window > 0 && kh <= pos_last - a.window)));
       uint32_t seen[MT];
@@ -868,73 +914,76 @@ __global__ __launch_bounds__(kThreads, DP == 256 && !F32 ? 1 : 2) void kv_attent
       if (partial) {
         uint32_t there = 0;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) there |= (sh.there[b][32 * h + 16 * u + 4 * g + i] ? 1u : 0u) << (4 * u + i);
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t x = *reinterpret_cast<const uint32_t*>(&sh.there[b][32 * h + 16 * u + 4 * g]);  // 4 bytes, 0 or 1
+          there |= ((x | x >> 7 | x >> 14 | x >> 21) & 15u) << (4 * u);
+        }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           seen[mt] = there;
+          if (a.causal) seen[mt] &= keys_between(kh + 4 * g, a.window > 0 ? pos[mt] - a.window + 1 : 0, pos[mt]);
 #pragma unroll
           for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int key = kh + 16 * u + 4 * g + i;
-              if (a.causal && (key > pos[mt] || (a.window > 0 && key <= pos[mt] - a.window)))
-                seen[mt] &= ~(1u << (4 * u + i));
-              if (!(seen[mt] >> (4 * u + i) & 1)) s[mt][u][i] = kNegInf;
-            }
+            for (int i = 0; i < 4; ++i) s[mt][u][i] = kept_or_neg_inf(s[mt][u][i], spread_bit(seen[mt], 4 * u + i));
         }
       }
       float mx[MT];
       bool grows = false;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        mx[mt] = fmaxf(fmaxf(fmaxf(s[mt][0][0], s[mt][0][1]), fmaxf(s[mt][0][2], s[mt][0][3])),
-                       fmaxf(fmaxf(s[mt][1][0], s[mt][1][1]), fmaxf(s[mt][1][2], s[mt][1][3])));
-        grows = grows || mx[mt] > m[mt] + kSlack;  // (any score passes -inf)
+        mx[mt] = max_of(s[mt]);
+        grows = grows || mx[mt] > (set[mt] ? kSlack : kNegInf);
       }
       if (__any(grows)) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           float x = fmaxf(mx[mt], lane_xorf<16>(mx[mt]));
           x = fmaxf(x, lane_xorf<32>(x));
-          const float mn = fmaxf(m[mt], x);
-          const float alpha = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[mt] - mn);
-          m[mt] = mn;
+          if (set[mt]) x = fmaxf(x, 0.0f);
+          const bool moves = x > kNegInf;
+          const float by = moves ? x : 0.0f, alpha = set[mt] ? __builtin_amdgcn_exp2f(-by) : 1.0f;
+          set[mt] = set[mt] || moves;
+          m[mt] += by;
           l[mt] *= alpha;
 #pragma unroll
           for (int n = 0; n < NT; ++n) o[n][mt] *= alpha;
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[mt][u][i] -= by;
         }
       }
       Frag p[MT][TERMS];
       if (partial) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
-          weights_of<true, TERMS>(s[mt], vs, seen[mt], m[mt] == kNegInf ? 0.0f : m[mt], l[mt], p[mt]);
+          weights_of<true, TERMS>(s[mt], vs, seen[mt], 0.0f, l[mt], p[mt]);
       } else {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) weights_of<false, TERMS>(s[mt], vs, 0, m[mt], l[mt], p[mt]);
+        for (int mt = 0; mt < MT; ++mt) weights_of<false, TERMS>(s[mt], vs, 0, 0.0f, l[mt], p[mt]);
       }
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const uint4 w = sh.v[b][h][n][lane];
         Frag f;
-        f.w[0] = w.x; f.w[1] = w.y; f.w[2] = w.z; f.w[3] = w.w;
+        f.w[0] = vw_[n].x; f.w[1] = vw_[n].y; f.w[2] = vw_[n].z; f.w[3] = vw_[n].w;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int k = 0; k < TERMS; ++k) o[n][mt] = mfma(f, p[mt][k], o[n][mt]);
       }
+      __builtin_amdgcn_s_setprio(0);
       if (FMT == GPTQ_KV_E4M3 && (odd >> (P * h) & ((1u << P) - 1)) != 0) {
         // a NaN among the values reaches the rows that see its key
         __asm__ volatile("s_nop 15" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll 1
         for (int key = 0; key < 32; ++key) {
-          bool sees[MT];
+          uint32_t sees[MT];
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
-            sees[mt] = __shfl((int)seen[mt], 16 * (key % 16 / 4) + c16) >> (4 * (key / 16) + key % 4) & 1;
+            sees[mt] = spread_bit(__shfl((int)seen[mt], 16 * (key % 16 / 4) + c16), 4 * (key / 16) + key % 4) & 0x7FC00000u;
 #pragma unroll
           for (int w = 0; w < P; ++w) {
             if ((odd >> (P * h + w) & 1u) == 0) continue;
@@ -945,16 +994,16 @@ __global__ __launch_bounds__(kThreads, DP == 256 && !F32 ? 1 : 2) void kv_attent
               for (int n = 0; n < 4; ++n)
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
-                  if (sees[mt] && (x >> n & 1u)) o[4 * w + n][mt][i] = __builtin_nanf("");
+                  o[4 * w + n][mt][i] = __uint_as_float(__float_as_uint(o[4 * w + n][mt][i]) | (sees[mt] & spread_bit(x, n)));
             }
           }
         }
       }
     }
-    __syncthreads();  // (everyone has read tile b's mark and places)
-    if (tid == 0) sh.odd[b] = 0;
-    put_scales(b ^ 1);
-    convert(b ^ 1);
+    mark = mark == 2 ? 0 : mark + 1;
+    if (tid == 0) sh.odd[mark == 2 ? 0 : mark + 1] = 0;
+    put_scales(b ^ 1, mark);
+    convert(b ^ 1, mark);
     look_up(k0 + 2 * KEYS, e, b);
     e = entry_of(k0 + 3 * KEYS);
   }
@@ -979,7 +1028,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 && !F32 ? 1 : 2) void kv_attent
 #pragma unroll
         for (int n = 0; n < 4; ++n) v[4 * i + n] = o[4 * w + n][mt][i];
       if (a.splits == 1) finish_row<16, F32>(a, t.sp, head, t.row0 + row, 64 * w + 16 * g, v, m[mt], sum);
-      else store_part<16, DP>(a, part * (64 * MT) + row, 64 * w + 16 * g, v, m[mt], sum);
+      else store_part<16, DP>(a, part * (64 * MT) + row, 64 * w + 16 * g, v, set[mt] ? m[mt] : kNegInf, sum);
     }
   }
 }
@@ -1045,8 +1094,9 @@ struct Plan {
   int splits;
 };
 
-// rows of a wave in the tile kernel: as many as 256 registers hold
-int tile_mt(int dp, bool f32) { return dp == 256 ? (f32 ? 1 : 2) : f32 ? 2 : 3; }
+// 16 rows each of a wave in the tile kernel: as many as 256 registers hold beside the operands that
+// are read ahead (2 x 2048 rows over 4096 tokens: 2 279 us, 3, which spills, 373).
+constexpr int tile_mt(int dp, bool f32) { return dp == 64 ? (f32 ? 2 : 3) : f32 ? 1 : dp == 128 ? 2 : 1; }
 
 Plan plan_of(const gptq_kv_blocks* c, int q_heads, int dt, int64_t tokens, int64_t seqs, int64_t width) {
   Plan p;
@@ -1080,9 +1130,9 @@ hipError_t launch_tiles(const AttnArgs& a, const dim3& grid, hipStream_t stream)
 
 template <int FMT, bool F32>
 hipError_t launch_tiles_of(int dp, const AttnArgs& a, const dim3& grid, hipStream_t stream) {
-  if (dp == 64) return launch_tiles<64, FMT, F32, F32 ? 2 : 3>(a, grid, stream);
-  if (dp == 128) return launch_tiles<128, FMT, F32, F32 ? 2 : 3>(a, grid, stream);
-  return launch_tiles<256, FMT, F32, F32 ? 1 : 2>(a, grid, stream);
+  if (dp == 64) return launch_tiles<64, FMT, F32, tile_mt(64, F32)>(a, grid, stream);
+  if (dp == 128) return launch_tiles<128, FMT, F32, tile_mt(128, F32)>(a, grid, stream);
+  return launch_tiles<256, FMT, F32, tile_mt(256, F32)>(a, grid, stream);
 }
 
 }  // namespace
