@@ -449,7 +449,7 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const TileRows& 
 // DP: head_dim rounded up to 64, 128 or 256.  fp32 rows: queries and probabilities as three
 // bf16 terms each.
 template <int DP, int FMT, bool F32, int MT, bool EVEN>
-__global__ __launch_bounds__(kThreads, MT == 1 && DP <= 128 && !F32 ? 3 : 1) void kv_attention_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, F32 || DP == 256 ? 1 : MT == 1 ? 3 : 2) void kv_attention_kernel(AttnArgs a) {
   constexpr int TERMS = F32 ? 3 : 1;
   constexpr int STEPS = DP / 32;   // of the first product
   constexpr int NT = DP / 16;      // tiles of 16 columns of the output; bytes of a V row in a lane
@@ -1033,55 +1033,67 @@ __global__ __launch_bounds__(kThreads, DP == 256 && F32 ? 1 : 2) void kv_attenti
   }
 }
 
-// A workgroup per tile and head joins its splits, in their order.
+// A wave joins the splits of a row of a tile: a group of 16 lanes takes every fourth one, in order, their
+// sums are joined in a fixed order.
 template <int DP, bool F32>
 __global__ __launch_bounds__(kThreads) void kv_attention_join_kernel(AttnArgs a, int per) {
   constexpr int NT = DP / 16;
-  const int tid = threadIdx.x, head = blockIdx.y;
+  constexpr int B = 4;  // parts of a lane whose loads are under way together
+  const int lane = threadIdx.x & 63, head = blockIdx.y, row = blockIdx.z * kWaves + (threadIdx.x >> 6);
   const TileRows t = tile_rows(a, (int)blockIdx.x, per);
+  if (row >= t.rows) return;
   const int64_t part = ((int64_t)blockIdx.x * a.heads + head) * a.splits;
-  constexpr int B = 8;  // parts whose loads are under way together
-  for (int row = tid >> 4; row < t.rows; row += 16) {
-    const int c = (tid & 15) * NT;
-    float m = kNegInf, l = 0.0f, v[NT] = {};
-    for (int s0 = 0; s0 < a.splits; s0 += B) {
-      float2 st[B];
-      float4 d[B][NT / 4];
+  const int c = (lane & 15) * NT, sub = lane >> 4;
+  float m = kNegInf, l = 0.0f, v[NT] = {};
+  for (int s0 = sub; s0 < a.splits; s0 += 4 * B) {
+    float2 st[B];
+    float4 d[B][NT / 4];
 #pragma unroll
-      for (int k = 0; k < B; ++k) {
-        const int64_t at = (part + min(s0 + k, a.splits - 1)) * per + row;
-        st[k] = a.stats[at];
+    for (int k = 0; k < B; ++k) {
+      const int64_t at = (part + min(s0 + 4 * k, a.splits - 1)) * per + row;
+      st[k] = a.stats[at];
 #pragma unroll
-        for (int n = 0; n < NT / 4; ++n) d[k][n] = reinterpret_cast<const float4*>(a.parts + at * DP + c)[n];
-      }
-      float mx = m;
+      for (int n = 0; n < NT / 4; ++n) d[k][n] = reinterpret_cast<const float4*>(a.parts + at * DP + c)[n];
+    }
+    float mx = m;
 #pragma unroll
-      for (int k = 0; k < B; ++k) {
-        if (s0 + k >= a.splits) st[k] = make_float2(kNegInf, 0.0f);
-        mx = fmaxf(mx, st[k].x);
-      }
-      const float base = mx == kNegInf ? 0.0f : mx;
-      const float f0 = __builtin_amdgcn_exp2f(m - base);
-      m = mx;
-      l *= f0;
+    for (int k = 0; k < B; ++k) {
+      if (s0 + 4 * k >= a.splits) st[k] = make_float2(kNegInf, 0.0f);
+      mx = fmaxf(mx, st[k].x);
+    }
+    const float base = mx == kNegInf ? 0.0f : mx;
+    const float f0 = __builtin_amdgcn_exp2f(m - base);
+    m = mx;
+    l *= f0;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) v[n] *= f0;
+    for (int n = 0; n < NT; ++n) v[n] *= f0;
 #pragma unroll
-      for (int k = 0; k < B; ++k) {
-        const float f = __builtin_amdgcn_exp2f(st[k].x - base);
-        l += st[k].y * f;
+    for (int k = 0; k < B; ++k) {
+      const bool in = s0 + 4 * k < a.splits;  // (what stands in for a part behind the last one may hold anything)
+      const float f = __builtin_amdgcn_exp2f(st[k].x - base);
+      l += st[k].y * f;
 #pragma unroll
-        for (int n = 0; n < NT / 4; ++n) {
-          // (a part behind the last one may hold anything)
-          v[4 * n] += s0 + k < a.splits ? d[k][n].x * f : 0.0f;
-          v[4 * n + 1] += s0 + k < a.splits ? d[k][n].y * f : 0.0f;
-          v[4 * n + 2] += s0 + k < a.splits ? d[k][n].z * f : 0.0f;
-          v[4 * n + 3] += s0 + k < a.splits ? d[k][n].w * f : 0.0f;
-        }
+      for (int n = 0; n < NT / 4; ++n) {
+        v[4 * n] += in ? d[k][n].x * f : 0.0f;
+        v[4 * n + 1] += in ? d[k][n].y * f : 0.0f;
+        v[4 * n + 2] += in ? d[k][n].z * f : 0.0f;
+        v[4 * n + 3] += in ? d[k][n].w * f : 0.0f;
       }
     }
-    finish_row<NT, F32>(a, t.sp, head, t.row0 + row, c, v, m, l);
   }
+  float mx = fmaxf(m, lane_xorf<16>(m));
+  mx = fmaxf(mx, lane_xorf<32>(mx));
+  const float f = __builtin_amdgcn_exp2f(m - (mx == kNegInf ? 0.0f : mx));
+  l *= f;
+  l += lane_xorf<16>(l);
+  l += lane_xorf<32>(l);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    v[n] *= f;
+    v[n] += lane_xorf<16>(v[n]);
+    v[n] += lane_xorf<32>(v[n]);
+  }
+  if (sub == 0) finish_row<NT, F32>(a, t.sp, head, t.row0 + row, c, v, mx, l);
 }
 
 int padded_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
@@ -1104,8 +1116,11 @@ Plan plan_of(const gptq_kv_blocks* c, int q_heads, int dt, int64_t tokens, int64
   const int dp = padded_dim(c->head_dim);
   const int64_t group = q_heads / c->heads;
   const int64_t each = ceil_div(tokens * group, seqs);  // rows of a sequence on average
-  p.tiles = each > 64;
-  p.mt = p.tiles ? tile_mt(dp, f32) : each > 16 && !f32 && dp <= 128 ? 4 : 1;
+  // 8 sequences of 8000, 32 query heads on 8 of 128, 20 rows a key head: 32 rows a wave 47 us, twice 16
+  // 92, the tile kernel 74; 36 rows: 32 rows a wave 86, the tile kernel 63 (its waves with 16 rows); fp32,
+  // 20 rows: 16 rows a wave 74, the tile kernel 102
+  p.tiles = each > (f32 || dp <= 128 ? 32 : 16);
+  p.mt = p.tiles ? (each <= 64 ? 1 : tile_mt(dp, f32)) : each > 16 && !f32 ? 2 : 1;
   p.per = p.tiles ? 64 * p.mt : 16 * p.mt;
   p.tasks = tokens * group / p.per + seqs;
   // Splits: as many as give 512 workgroups, two a CU, whose waves' loads fill the memory's queue
@@ -1129,7 +1144,12 @@ hipError_t launch_tiles(const AttnArgs& a, const dim3& grid, hipStream_t stream)
 }
 
 template <int FMT, bool F32>
-hipError_t launch_tiles_of(int dp, const AttnArgs& a, const dim3& grid, hipStream_t stream) {
+hipError_t launch_tiles_of(int dp, int mt, const AttnArgs& a, const dim3& grid, hipStream_t stream) {
+  if (mt == 1) {
+    if (dp == 64) return launch_tiles<64, FMT, F32, 1>(a, grid, stream);
+    if (dp == 128) return launch_tiles<128, FMT, F32, 1>(a, grid, stream);
+    return launch_tiles<256, FMT, F32, 1>(a, grid, stream);
+  }
   if (dp == 64) return launch_tiles<64, FMT, F32, tile_mt(64, F32)>(a, grid, stream);
   if (dp == 128) return launch_tiles<128, FMT, F32, tile_mt(128, F32)>(a, grid, stream);
   return launch_tiles<256, FMT, F32, tile_mt(256, F32)>(a, grid, stream);
@@ -1179,8 +1199,8 @@ hipError_t launch_kv_attention(const KvAttention& t, const KvSequences& seqs,
     const dim3 tgrid((unsigned)(p.tasks * kb->heads), 1, (unsigned)p.splits);
     const hipError_t e =
         kb->format == GPTQ_KV_E4M3
-            ? (f32 ? launch_tiles_of<GPTQ_KV_E4M3, true>(dp, a, tgrid, stream) : launch_tiles_of<GPTQ_KV_E4M3, false>(dp, a, tgrid, stream))
-            : (f32 ? launch_tiles_of<GPTQ_KV_INT8, true>(dp, a, tgrid, stream) : launch_tiles_of<GPTQ_KV_INT8, false>(dp, a, tgrid, stream));
+            ? (f32 ? launch_tiles_of<GPTQ_KV_E4M3, true>(dp, p.mt, a, tgrid, stream) : launch_tiles_of<GPTQ_KV_E4M3, false>(dp, p.mt, a, tgrid, stream))
+            : (f32 ? launch_tiles_of<GPTQ_KV_INT8, true>(dp, p.mt, a, tgrid, stream) : launch_tiles_of<GPTQ_KV_INT8, false>(dp, p.mt, a, tgrid, stream));
     if (e != hipSuccess) return e;
   }
   const dim3 grid((unsigned)p.tasks, (unsigned)kb->heads, (unsigned)p.splits);
@@ -1198,7 +1218,7 @@ hipError_t launch_kv_attention(const KvAttention& t, const KvSequences& seqs,
   do {                                        \
     if (f32) GPTQ_ATTN_F(DP, true, 1);        \
     else if (p.mt == 1) GPTQ_ATTN_F(DP, false, 1); \
-    else GPTQ_ATTN_F(DP, false, 4);           \
+    else GPTQ_ATTN_F(DP, false, 2);           \
   } while (0)
   if (p.tiles) {}
   else if (dp == 64) GPTQ_ATTN(64);
@@ -1209,7 +1229,7 @@ hipError_t launch_kv_attention(const KvAttention& t, const KvSequences& seqs,
 #undef GPTQ_ATTN_F
 #undef GPTQ_ATTN_E
   if (p.splits > 1) {
-    const dim3 jgrid((unsigned)p.tasks, (unsigned)kb->heads);
+    const dim3 jgrid((unsigned)p.tasks, (unsigned)kb->heads, (unsigned)(p.per / kWaves));
 #define GPTQ_JOIN(DP)                                                                                     \
   do {                                                                                                    \
     if (f32) hipLaunchKernelGGL((kv_attention_join_kernel<DP, true>), jgrid, block, 0, stream, a, p.per); \
