@@ -199,4 +199,26 @@ __device__ __forceinline__ uint2 int_codes8(const Vals8& x, float scale, float z
   return make_uint2(w[0], BITS == 4 ? 0u : w[8 / PER - 1]);
 }
 
+// Logits col .. col + 7 of n (col may lie up to 7 in front), 16-byte aligned where all
+// of them are inside; 0 outside.
+template <int DT>
+__device__ __forceinline__ Raw8<DT> load_chunk(const char* x, int64_t col, int64_t n) {
+  Raw8<DT> o;
+  if (col >= 0 && col + 8 <= n) return load_raw8<DT>(x, col, n, true);
+  if constexpr (DT == GPTQ_BF16) {
+    const uint16_t* e = reinterpret_cast<const uint16_t*>(x);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t i = col + 2 * k;
+      o.w[k] = i >= 0 && i < n ? e[i] : 0;
+      if (i + 1 >= 0 && i + 1 < n) o.w[k] |= (uint32_t)e[i + 1] << 16;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      o.w[k] = col + k >= 0 && col + k < n ? reinterpret_cast<const uint32_t*>(x)[col + k] : 0;
+  }
+  return o;
+}
+
 }  // namespace gptq
