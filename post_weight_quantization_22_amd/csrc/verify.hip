@@ -215,8 +215,8 @@ __device__ __forceinline__ double block_sum(double v, double* part) {
   return ((part[0] + part[1]) + part[2]) + part[3];
 }
 
-// A workgroup per sequence, segment and model: how many drafted tokens are accepted (the first one
-// writes what follows from it), then the segment's sum of the row that the next token is drawn from.
+// A workgroup per sequence and segment: how many drafted tokens are accepted (the first one writes what
+// follows from it), then the segment's sums of the row that the next token is drawn from.
 template <int TD, int DD>
 __global__ __launch_bounds__(kThreads) void verify_accept_kernel(VerifyCall a) {
   constexpr int EACH = 2, ROUND = EACH * kWaves;  // rows of a wave, of the workgroup, at a time
@@ -225,7 +225,7 @@ __global__ __launch_bounds__(kThreads) void verify_accept_kernel(VerifyCall a) {
   __shared__ float seen_mq[ROUND];
   __shared__ double part[kWaves];
   const int seq = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const bool draft = blockIdx.z == 1, writes = blockIdx.y == 0 && !draft;
+  const bool writes = blockIdx.y == 0;
   const int T = (int)a.v.tokens;
   const int s0 = min(max(a.v.starts[seq], 0), T), n = min(max(a.v.starts[seq + 1], 0), T) - s0;
   const float t = temperature(a, seq);
@@ -307,23 +307,39 @@ __global__ __launch_bounds__(kThreads) void verify_accept_kernel(VerifyCall a) {
     a.draws[seq] = make_int4(law && !sure ? (int)row : -1, judged, __float_as_int(top.m), __float_as_int(mq));
     if (law && sure) a.v.out[row] = top.at;
   }
-  if (sure || !law || (draft && !judged)) return;
-  constexpr int AHEAD = 8;  // logits of a thread under way
-  const double it = 1.0 / (double)t, m = draft ? mq : top.m;
+  if (sure || !law) return;
+  constexpr int AHEAD = 8;  // logits of a thread and model under way
+  const bool both = judged && a.v.draft;
+  const double it = 1.0 / (double)t, m = top.m, md = mq;
   const int64_t c0 = blockIdx.y * a.dseg, c1 = min(c0 + a.dseg, a.v.vocab);
-  double s = 0.0;
+  double s = 0.0, sq = 0.0;
   for (int64_t i = c0 + tid; i < c1; i += AHEAD * kThreads) {
-    float x[AHEAD];
+    float x[AHEAD], y[AHEAD];
 #pragma unroll
-    for (int e = 0; e < AHEAD; ++e) x[e] = logit<TD, DD>(a, draft, row, min(i + e * kThreads, c1 - 1));
+    for (int e = 0; e < AHEAD; ++e) {
+      const int64_t k = min(i + e * kThreads, c1 - 1);
+      x[e] = logit<TD, DD>(a, false, row, k);
+      y[e] = both ? logit<TD, DD>(a, true, row, k) : 0.0f;
+    }
 #pragma unroll
     for (int e = 0; e < AHEAD; ++e) {
       const double v = exp64(((double)x[e] - m) * it);
       if (i + e * kThreads < c1) s += v;
     }
+    if (both) {
+#pragma unroll
+      for (int e = 0; e < AHEAD; ++e) {
+        const double v = exp64(((double)y[e] - md) * it);
+        if (i + e * kThreads < c1) sq += v;
+      }
+    }
   }
   s = block_sum(s, part);
-  if (tid == 0) a.sums[(int64_t)(draft ? a.v.seqs + seq : seq) * a.dsegs + blockIdx.y] = s;
+  if (both) sq = block_sum(sq, part);
+  if (tid == 0) {
+    a.sums[(int64_t)seq * a.dsegs + blockIdx.y] = s;
+    a.sums[(a.v.seqs + seq) * a.dsegs + blockIdx.y] = sq;
+  }
 }
 
 struct Law {  // of the row that is drawn from
@@ -546,10 +562,10 @@ hipError_t launch_verify(const VerifyArgs& v, hipStream_t stream) {
   if (v.tokens > 0)
     hipLaunchKernelGGL(verify_stats_kernel, dim3((unsigned)v.tokens, (unsigned)a.segs, models), block, 0,
                        stream, a);
-  const dim3 agrid((unsigned)v.seqs, (unsigned)a.dsegs, models), dgrid((unsigned)v.seqs, (unsigned)a.dsegs);
+  const dim3 dgrid((unsigned)v.seqs, (unsigned)a.dsegs);
 #define GPTQ_DRAW(TD, DD)                                                                  \
   do {                                                                                     \
-    hipLaunchKernelGGL((verify_accept_kernel<TD, DD>), agrid, block, 0, stream, a);        \
+    hipLaunchKernelGGL((verify_accept_kernel<TD, DD>), dgrid, block, 0, stream, a);        \
     hipLaunchKernelGGL((verify_draw_kernel<TD, DD>), dgrid, block, 0, stream, a);          \
   } while (0)
   if (v.tdt == GPTQ_BF16 && (!v.draft || v.ddt == GPTQ_BF16)) GPTQ_DRAW(GPTQ_BF16, GPTQ_BF16);
