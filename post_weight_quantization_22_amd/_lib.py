@@ -305,7 +305,7 @@ def load() -> ctypes.CDLL:
     lib.kv_pages_compact.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64,
                                      _vp, _vp, _sz, _vp]
     lib.kv_pages_copy.restype = _i32
-    lib.kv_pages_copy.argtypes = [_vp, _i64, _vp, _vp, _i64, _vp, _vp]
+    lib.kv_pages_copy.argtypes = [ctypes.c_char_p, _i64, _vp, _vp, _i64, _vp, _vp]
     lib.verify_drafts_workspace_size.restype = _i32
     lib.verify_drafts_workspace_size.argtypes = [_i64, _i64, _i64, ctypes.POINTER(_sz)]
     lib.verify_drafts.restype = _i32
@@ -758,19 +758,25 @@ _KIND = {}
 _FLOAT = {"b": GPTQ_BF16, "f": GPTQ_F32}
 
 
+_I32 = None  # torch.int32
+
+
 def _kinds() -> None:
+    global _I32
     if not _KIND:
         import torch
 
+        _I32 = torch.int32
         _KIND.update({torch.bfloat16: "b", torch.float32: "f", torch.float8_e4m3fn: "8",
                       torch.uint8: "u", torch.int64: "l", torch.int32: "i"})
 
 
 def _on_gpu(t, name: str):
     """The device of an operand, which has to be a GPU."""
-    _kinds()
+    if not _KIND:
+        _kinds()
     d = t.device
-    if d.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} is on {d}, expected a GPU tensor")
     return d
 
@@ -797,12 +803,21 @@ def _plane(t, name: str, rows: int, cols: int, kinds: str, device, exact: str = 
     return stride[0] if shape[0] > 1 else max(stride[0], shape[1])
 
 
+_C = None  # torch._C, set on first use
+
+
+def _torch_c():
+    global _C
+    import torch
+
+    _C = torch._C
+    return _C
+
+
 def _launch(name: str, device, stream, *args) -> None:
     """Calls an entry point on ``stream`` (default: the current stream of the
     tensors' device), with that device current."""
-    import torch
-
-    c = torch._C
+    c = _C or _torch_c()
     index = device.index
     if stream is None:
         raw = c._cuda_getCurrentRawStream(index)
@@ -813,6 +828,8 @@ def _launch(name: str, device, stream, *args) -> None:
     if index == c._cuda_getDevice():
         status = getattr(_lib, name)(*args, raw)
     else:
+        import torch
+
         with torch.cuda.device(index):
             status = getattr(_lib, name)(*args, raw)
     if status:
@@ -1015,7 +1032,7 @@ def _kv_rows(t, name: str, cache: Optional[GPTQKVCache], tokens: int, device, dt
     if len(shape) != 3 or stride[2] != 1 or shape[0] != tokens or shape[1:] != cache.row:
         raise ValueError(f"{name}: shape {tuple(shape)} strides {stride}, expected "
                          f"{(tokens, *cache.row)} with a dense last dimension")
-    if cache.device != device or t.device != device:
+    if not cache.device.index == t.get_device() == device.index:
         raise ValueError(f"{name}: rows on {t.device}, cache on {cache.device}, "
                          f"expected {device}")
     return t.data_ptr(), stride[0], stride[1]
@@ -1154,8 +1171,27 @@ def make_kv_blocks(codes, scales, fmt: str = "e4m3") -> GPTQKVBlocks:
     return c
 
 
+def _vectors(device, *buffers) -> None:
+    """_vector for each (tensor, name, count, kind), None allowed for names that end in '?'."""
+    index = device.index
+    for t, name, count, kind in buffers:
+        if t is None:
+            if name[-1] != "?":
+                raise ValueError(f"{name} is required")
+        elif (_KIND.get(t.dtype) != kind or t.get_device() != index or not t.is_contiguous()
+              or t.numel() < count):
+            _vector(t, name.rstrip("?"), count, kind, device)
+
+
 def _kv_sequences(table, lengths, starts, device):
     """(table, ldt, width, lengths, starts, seqs) of a call's sequences."""
+    shape, i32, index = table.shape, _I32, device.index
+    if (len(shape) == 2 and table.dtype is i32 and lengths.dtype is i32 and starts.dtype is i32
+            and index == table.get_device() == lengths.get_device() == starts.get_device()
+            and table.is_contiguous() and lengths.is_contiguous() and starts.is_contiguous()
+            and lengths.numel() == shape[0] and starts.numel() == shape[0] + 1):
+        return table.data_ptr(), shape[1], shape[1], lengths.data_ptr(), starts.data_ptr(), shape[0]
+    # what the quick look does not take: tables with longer rows, or an error to name
     if table.dim() != 2:
         raise ValueError(f"table: shape {tuple(table.shape)}, expected [seqs, width]")
     seqs, width = table.shape
@@ -1230,6 +1266,7 @@ def kv_block_attention(Q, kb, vb, table, lengths, starts, out, lse=None, causal:
     ``window`` of them; else all of its sequence.  scale: head_dim ** -0.5 unless given.
     lse[tokens, q_heads] (fp32): the logarithm of each row's denominator."""
     d = _on_gpu(Q, "Q")
+    shape, qs, os_ = Q.shape, Q.stride(), out.stride()
     dt = _FLOAT.get(_KIND.get(Q.dtype))
     if dt is None:
         raise TypeError(f"Q: dtype {Q.dtype}, expected bfloat16 or float32")
@@ -1240,18 +1277,17 @@ def kv_block_attention(Q, kb, vb, table, lengths, starts, out, lse=None, causal:
     if kb.device != d or vb.device != d:
         raise ValueError(f"caches on {kb.device} and {vb.device}, expected {d}")
     heads, dim = kb.row
-    shape, qs = Q.shape, Q.stride()
     if len(shape) != 3 or shape[2] != dim or shape[1] == 0 or shape[1] % heads or qs[2] != 1:
         raise ValueError(f"Q: shape {tuple(shape)} strides {qs}, expected [tokens, a multiple of "
                          f"{heads}, {dim}] with a dense last dimension")
     tokens, q_heads = shape[:2]
     if out.dtype is not Q.dtype:
         raise TypeError(f"out: dtype {out.dtype}, expected {Q.dtype}")
-    os_ = out.stride()
-    if out.shape != shape or os_[2] != 1 or out.device != d:
+    if out.shape != shape or os_[2] != 1 or out.get_device() != d.index:
         raise ValueError(f"out: shape {tuple(out.shape)} strides {os_} on {out.device}, expected "
                          f"{tuple(shape)} with a dense last dimension on {d}")
-    _vector(lse, "lse", tokens * q_heads, "f", d)
+    if lse is not None:
+        _vectors(d, (lse, "lse", tokens * q_heads, "f"))
     s = _kv_sequences(table, lengths, starts, d)
     p, nbytes, ws = _space(_attention_space(kb, q_heads, dt, tokens, s[5], s[2]), ws, d, stream)
     _launch("kv_block_attention", d, stream, Q.data_ptr(), qs[0], qs[1], dt, tokens, q_heads, kb.ref,
@@ -1272,10 +1308,9 @@ def kv_pages_fork(table, lengths, refs, parents, page_size: int, new_table, new_
     ldt = _plane(table, "table", rows, width, "i", d)
     ldn = _plane(new_table, "new_table", new_rows, width, "i", d, "c")
     pages = refs.numel()
-    for t, name, n in ((lengths, "lengths", rows), (parents, "parents", new_rows),
-                       (new_lengths, "new_lengths", new_rows), (refs, "refs", pages),
-                       (new_refs, "new_refs", pages)):
-        _vector(t, name, n, "i", d, optional=False)
+    _vectors(d, (lengths, "lengths", rows, "i"), (parents, "parents", new_rows, "i"),
+             (new_lengths, "new_lengths", new_rows, "i"), (refs, "refs", pages, "i"),
+             (new_refs, "new_refs", pages, "i"))
     _launch("kv_pages_fork", d, stream, table.data_ptr(), ldt, lengths.data_ptr(), rows, width,
             refs.data_ptr(), pages, parents.data_ptr(), new_rows, page_size, new_table.data_ptr(),
             ldn, new_lengths.data_ptr(), new_refs.data_ptr(), _info(info, d))
@@ -1298,9 +1333,8 @@ def kv_pages_resize(table, lengths, refs, new_lengths, page_size: int, src, dst,
     rows, width = table.shape
     ldt = _plane(table, "table", rows, width, "i", d)
     pages = refs.numel()
-    for t, name, n in ((lengths, "lengths", rows), (new_lengths, "new_lengths", rows),
-                       (src, "src", rows), (dst, "dst", rows), (refs, "refs", pages)):
-        _vector(t, name, n, "i", d, optional=False)
+    _vectors(d, (lengths, "lengths", rows, "i"), (new_lengths, "new_lengths", rows, "i"),
+             (src, "src", rows, "i"), (dst, "dst", rows, "i"), (refs, "refs", pages, "i"))
     p, nbytes, ws = _space(kv_pages_resize_workspace_size(rows, pages), ws, d, stream)
     _launch("kv_pages_resize", d, stream, table.data_ptr(), ldt, lengths.data_ptr(), rows, width,
             refs.data_ptr(), pages, new_lengths.data_ptr(), page_size, src.data_ptr(),
@@ -1323,47 +1357,44 @@ def kv_pages_compact(table, refs, new_table, new_refs, src, dst, count, ws=None,
     ldn = _plane(new_table, "new_table", rows, width, "i", d, "rc")
     pages = refs.numel()
     capacity = src.numel()
-    for t, name, n in ((refs, "refs", pages), (new_refs, "new_refs", pages), (src, "src", pages // 2),
-                       (dst, "dst", capacity), (count, "count", 1)):
-        _vector(t, name, n, "i", d, optional=False)
+    _vectors(d, (refs, "refs", pages, "i"), (new_refs, "new_refs", pages, "i"),
+             (src, "src", pages // 2, "i"), (dst, "dst", capacity, "i"), (count, "count", 1, "i"))
     p, nbytes, ws = _space(kv_pages_compact_workspace_size(pages), ws, d, stream)
     _launch("kv_pages_compact", d, stream, table.data_ptr(), ldt, rows, width, refs.data_ptr(), pages,
             new_table.data_ptr(), ldn, new_refs.data_ptr(), src.data_ptr(), dst.data_ptr(), capacity,
             count.data_ptr(), p, nbytes)
 
 
-def _page_arrays(cache):
-    """The arrays of a cache's handle, as kv_pages_copy takes them."""
-    known = cache.__dict__.get("arrays")
-    if known is None:
-        known = []
-        for t in cache.tensors:
-            if t is None:
+def _page_arrays(cache) -> bytes:
+    """The arrays of a cache's handle as kv_pages_copy takes them, kept with the handle."""
+    known = b""
+    for t in cache.tensors:
+        if t is None:
+            continue
+        size, shape, stride = t.element_size(), list(t.shape[1:]), list(t.stride()[1:])
+        # dimensions that lie one behind the other are one
+        rows = [(shape[-1], stride[-1] * size)]
+        if rows[0][0] == 1 or rows[0][1] == size:
+            run = shape[-1] * size
+            rows = []
+        else:
+            run = size
+        for n, s in zip(reversed(shape[:-1]), reversed(stride[:-1])):
+            if n == 1:
                 continue
-            size, shape, stride = t.element_size(), list(t.shape[1:]), list(t.stride()[1:])
-            # dimensions that lie one behind the other are one
-            rows = [(shape[-1], stride[-1] * size)]
-            if rows[0][0] == 1 or rows[0][1] == size:
-                run = shape[-1] * size
-                rows = []
+            if not rows and s * size == run:
+                run *= n
+            elif rows and s * size == rows[-1][0] * rows[-1][1]:
+                rows[-1] = (rows[-1][0] * n, rows[-1][1])
             else:
-                run = size
-            for n, s in zip(reversed(shape[:-1]), reversed(stride[:-1])):
-                if n == 1:
-                    continue
-                if not rows and s * size == run:
-                    run *= n
-                elif rows and s * size == rows[-1][0] * rows[-1][1]:
-                    rows[-1] = (rows[-1][0] * n, rows[-1][1])
-                else:
-                    rows.append((n, s * size))
-            while len(rows) < 2:
-                rows.append((1, 0))
-            if len(rows) > 2:
-                raise ValueError("kv_pages_copy: a cache whose pages lie in more than three runs of strides")
-            known.append(GPTQPageArray(t.data_ptr(), t.shape[0], t.stride(0) * size, rows[1][0],
-                                       rows[1][1], rows[0][0], rows[0][1], run))
-        cache.arrays = known
+                rows.append((n, s * size))
+        while len(rows) < 2:
+            rows.append((1, 0))
+        if len(rows) > 2:
+            raise ValueError("kv_pages_copy: a cache whose pages lie in more than three runs of strides")
+        known += bytes(GPTQPageArray(t.data_ptr(), t.shape[0], t.stride(0) * size, rows[1][0],
+                                     rows[1][1], rows[0][0], rows[0][1], run))
+    cache.arrays = known
     return known
 
 
@@ -1372,18 +1403,17 @@ def kv_pages_copy(caches, src, dst, info=None, stream=None) -> None:
     make_kv_blocks or make_kv_cache, any number: keys and values of all layers in one call)."""
     d = _on_gpu(src, "src")
     pairs = src.numel()
-    _vector(src, "src", pairs, "i", d, optional=False)
-    _vector(dst, "dst", pairs, "i", d, optional=False)
+    _vectors(d, (src, "src", pairs, "i"), (dst, "dst", pairs, "i"))
     if dst.numel() != pairs:
         raise ValueError(f"dst: {dst.numel()} elements, expected {pairs}")
-    arrays = []
+    parts = []
     for c in caches:
-        if c.device != d:
+        if c.device is not d and c.device != d:
             raise ValueError(f"a cache is on {c.device}, expected {d}")
-        arrays += _page_arrays(c)
-    call = (GPTQPageArray * len(arrays))(*arrays)
-    _launch("kv_pages_copy", d, stream, ctypes.addressof(call), len(arrays), src.data_ptr(),
-            dst.data_ptr(), pairs, _info(info, d))
+        parts.append(c.__dict__.get("arrays") or _page_arrays(c))
+    call = b"".join(parts)  # the structures, one behind the other
+    _launch("kv_pages_copy", d, stream, call, len(call) // ctypes.sizeof(GPTQPageArray),
+            src.data_ptr(), dst.data_ptr(), pairs, _info(info, d))
 
 
 def verify_drafts_workspace_size(tokens: int, vocab: int, seqs: int) -> int:
@@ -1413,12 +1443,10 @@ def verify_drafts(target, draft, ids, starts, u, u_next, accepted, tokens, logpr
     seqs = starts.numel() - 1
     if seqs < 0:
         raise ValueError("starts: expected [seqs + 1]")
-    for t, name, n, kind in ((ids, "ids", rows, "l"), (starts, "starts", seqs + 1, "i"),
-                             (u, "u", rows, "f"), (u_next, "u_next", seqs, "f"),
-                             (accepted, "accepted", seqs, "i"), (tokens, "tokens", rows, "l")):
-        _vector(t, name, n, kind, d, optional=False)
-    _vector(logprobs, "logprobs", rows, "f", d)
-    _vector(temperatures, "temperatures", seqs, "f", d)
+    _vectors(d, (ids, "ids", rows, "l"), (starts, "starts", seqs + 1, "i"), (u, "u", rows, "f"),
+             (u_next, "u_next", seqs, "f"), (accepted, "accepted", seqs, "i"),
+             (tokens, "tokens", rows, "l"), (logprobs, "logprobs?", rows, "f"),
+             (temperatures, "temperatures?", seqs, "f"))
     p, nbytes, ws = _space(verify_drafts_workspace_size(rows, vocab, seqs), ws, d, stream)
     _launch("verify_drafts", d, stream, target.data_ptr(), _FLOAT[_KIND[target.dtype]], ldt,
             _ptr(draft), ddt, ldd, rows, vocab, ids.data_ptr(), starts.data_ptr(), seqs,

@@ -15,11 +15,9 @@ namespace {
 
 constexpr int kWide = 1024;   // threads of the kernels that settle pages
 constexpr int kPer = 4;       // pages that a thread looks at in one step
-
-// values that other waves of the workgroup have changed by atomics
-__device__ __forceinline__ int32_t fresh(const int32_t* p) {
-  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
+constexpr int kStep = kWide * kPer;
+constexpr int kRows = 4096;   // rows whose last pages are compared at a time
+constexpr int kHeld = 8192;   // fresh pages that LDS holds
 
 __device__ __forceinline__ int pages_of(int len, int page_size) {
   return (int)(((int64_t)max(len, 0) + page_size - 1) / page_size);
@@ -112,10 +110,8 @@ struct ResizeArgs {
   int32_t* src;
   int32_t* dst;
   int32_t* info;
-  int32_t* writers;  // [pages]: rows that write into a page
-  int32_t* top;      // [pages]: the last of them
-  int32_t* taken;    // [pages]: the free pages in use from now on, in order
-  int32_t* base;     // [rows]: where a row's fresh pages begin in `taken`
+  int32_t* taken;    // [pages]: the free pages in use from now on, in order (kHeld of them at most: in LDS)
+  int32_t* base;     // [rows]: where a row's fresh pages begin among those (more than kWide rows)
   int64_t ldt;
   int32_t rows, width, pages, page_size;
 };
@@ -151,71 +147,80 @@ __global__ __launch_bounds__(256) void pages_drop_kernel(ResizeArgs a) {
   if (lane == 0) a.lengths[row] = want;
 }
 
-// One workgroup: who gets which free pages.
+// One workgroup: who gets which free pages.  A step of a batch waits for it, so it is one chain of few
+// round trips: rows and the first free pages are read at once, shared pages are found among the rows'
+// last ones in LDS, nothing is fenced (what waves exchange in memory goes through one first-level cache).
 __global__ __launch_bounds__(kWide) void pages_grow_kernel(ResizeArgs a) {
   __shared__ int part[kWide / 64];
-  __shared__ int short_of;
-  const int tid = threadIdx.x;
-  // the last page of a row that grows inside it, -1 for the others
-  auto last_page = [&](int row, int& len, int& want) {
-    bool bad;
-    len = max(a.lengths[row], 0);
-    want = wanted(a, row, len, bad);
-    const int rest = len % a.page_size;
-    if (want <= len || rest == 0) return -1;
-    const int j = len / a.page_size;
-    const int page = j < a.width ? a.table[row * a.ldt + j] : -1;
-    if (page >= 0 && page < a.pages) return page;
-    if (a.info) atomicOr(a.info, 1);
-    return -1;
+  __shared__ __align__(16) int lasts[kRows];
+  __shared__ int held_taken[kHeld];
+  const int tid = threadIdx.x, lane = tid & 63;
+  struct Row {
+    int len, want, last, held;  // last: the page that it grows inside of, -1: none
   };
-  int len, want;
-  for (int row = tid; row < a.rows; row += kWide) {
-    const int p = last_page(row, len, want);
-    if (p >= 0) {
-      atomicExch(a.writers + p, 0);
-      atomicExch(a.top + p, -1);
+  auto row_at = [&](int row) {
+    Row r{0, 0, -1, 0};
+    if (row >= a.rows) return r;
+    r.len = max(a.lengths[row], 0);
+    bool bad;
+    r.want = wanted(a, row, r.len, bad);
+    const int j = r.len / a.page_size;
+    if (r.want > r.len && j * (int64_t)a.page_size < r.len) {
+      const int page = j < a.width ? a.table[row * a.ldt + j] : -1;
+      if (page >= 0 && page < a.pages) r.last = page;
+      else if (a.info) atomicOr(a.info, 1);
     }
-  }
-  __threadfence();
-  __syncthreads();
-  for (int row = tid; row < a.rows; row += kWide) {
-    const int p = last_page(row, len, want);
-    if (p >= 0) {
-      atomicAdd(a.writers + p, 1);
-      atomicMax(a.top + p, row);
-    }
-  }
-  __threadfence();
-  __syncthreads();
-  // a shared page stays with the last of its holders if all of them write into it
-  int total = 0;
-  for (int r0 = 0; r0 < a.rows; r0 += kWide) {
-    const int row = r0 + tid;
-    int need = 0;
-    bool copy = false;
-    if (row < a.rows) {
-      const int p = last_page(row, len, want);
-      if (p >= 0) {
-        const int held = fresh(a.refs + p);
-        copy = held > 1 && !(fresh(a.writers + p) == held && fresh(a.top + p) == row);
-      }
-      need = max(pages_of(want, a.page_size) - pages_of(len, a.page_size), 0) + (copy ? 1 : 0);
-    }
-    int sum;
-    const int before = scan_wide(need, part, sum);
-    if (row < a.rows) a.base[row] = (total + before) << 1 | (copy ? 1 : 0);
-    total += sum;
-  }
-  // the lowest free pages, as many as that
-  int found = 0;
-  for (int p0 = 0; p0 < a.pages && found < total; p0 += kWide * kPer) {
-    int free[kPer], n = 0;
+    return r;
+  };
+  auto free_at = [&](int p0, int (&free)[kPer]) {
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const int p = p0 + tid * kPer + k;
-      free[k] = p < a.pages && fresh(a.refs + p) == 0;
+      free[k] = p < a.pages && a.refs[p] == 0;
     }
+  };
+  int free[kPer];
+  free_at(0, free);
+  // A shared page stays with the last of its holders if all of them write into it.
+  Row r;
+  bool copy = false;
+  int total = 0, base = 0;
+  for (int r0 = 0; r0 < a.rows; r0 += kWide) {
+    r = row_at(r0 + tid);
+    r.held = r.last >= 0 ? a.refs[r.last] : 0;
+    const bool shared = r.held > 1;
+    int writers = 0, top = -1;
+    if (__syncthreads_or(shared)) {
+      for (int t0 = 0; t0 < a.rows; t0 += kRows) {
+        const int n = min(kRows, a.rows - t0);
+        __syncthreads();
+        for (int i = tid; i < (n + 3) / 4 * 4; i += kWide)
+          lasts[i] = i >= n ? -1 : t0 + i == r0 + tid ? r.last : row_at(t0 + i).last;
+        __syncthreads();
+        if (shared)
+          for (int i = 0; i < n; i += 4) {
+            const int4 x = *reinterpret_cast<const int4*>(lasts + i);
+            writers += (x.x == r.last) + (x.y == r.last) + (x.z == r.last) + (x.w == r.last);
+            if (x.x == r.last) top = t0 + i;
+            if (x.y == r.last) top = t0 + i + 1;
+            if (x.z == r.last) top = t0 + i + 2;
+            if (x.w == r.last) top = t0 + i + 3;
+          }
+      }
+    }
+    copy = shared && !(writers == r.held && top == r0 + tid);
+    const int need = max(pages_of(r.want, a.page_size) - pages_of(r.len, a.page_size), 0) + (copy ? 1 : 0);
+    int sum;
+    base = total + scan_wide(need, part, sum);
+    if (a.rows > kWide && r0 + tid < a.rows) a.base[r0 + tid] = base << 1 | (copy ? 1 : 0);
+    total += sum;
+  }
+  // the lowest free pages, as many as that
+  int* const taken = total <= kHeld ? held_taken : a.taken;
+  int found = 0;
+  for (int p0 = 0; p0 < a.pages && found < total; p0 += kStep) {
+    if (p0 > 0) free_at(p0, free);
+    int n = 0;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) n += free[k];
     int sum;
@@ -223,42 +228,56 @@ __global__ __launch_bounds__(kWide) void pages_grow_kernel(ResizeArgs a) {
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
       if (free[k]) {
-        if (at < total) a.taken[at] = p0 + tid * kPer + k;
+        if (at < total) taken[at] = p0 + tid * kPer + k;
         ++at;
       }
     found += sum;
   }
-  if (tid == 0) short_of = found < total;
-  __threadfence();
   __syncthreads();
-  if (short_of) {  // nobody grows
+  if (found < total) {  // nobody grows
     if (tid == 0 && a.info) atomicOr(a.info, 2);
     return;
   }
-  // a wave per row hands them out
-  for (int row = tid >> 6; row < a.rows; row += kWide / 64) {
-    bool bad;
-    const int lane = tid & 63, l0 = max(a.lengths[row], 0);
-    const int w = wanted(a, row, l0, bad);
-    if (w <= l0) continue;
-    const int o = pages_of(l0, a.page_size), n = pages_of(w, a.page_size);
-    const int b = fresh(a.base + row), copy = b & 1, at = b >> 1;
-    int32_t* e = a.table + row * a.ldt;
-    if (lane == 0) {
-      a.lengths[row] = w;
+  for (int r0 = 0; r0 < a.rows; r0 += kWide) {
+    const int row = r0 + tid;
+    if (a.rows > kWide) {
+      r = row_at(row);
+      const int b = row < a.rows ? a.base[row] : 0;
+      base = b >> 1;
+      copy = b & 1;
+    }
+    const bool grows = row < a.rows && r.want > r.len;
+    const int o = pages_of(r.len, a.page_size), n = grows ? pages_of(r.want, a.page_size) : o;
+    int32_t* const e = a.table + (int64_t)row * a.ldt;
+    if (grows) {
+      a.lengths[row] = r.want;
       if (copy) {
-        const int old = e[o - 1], page = fresh(a.taken + at);
-        a.src[row] = old;
+        const int page = taken[base];
+        a.src[row] = r.last;
         a.dst[row] = page;
         e[o - 1] = page;
-        atomicSub(a.refs + old, 1);
-        atomicExch(a.refs + page, 1);
+        atomicSub(a.refs + r.last, 1);
+        a.refs[page] = 1;
       }
     }
-    for (int j = o + lane; j < n; j += 64) {
-      const int page = fresh(a.taken + at + copy + j - o);
-      e[j] = page;
-      atomicExch(a.refs + page, 1);
+    // a few pages a row by its thread, many by its wave
+    constexpr int kFew = 4;
+    const int first = base + (copy ? 1 : 0), more = n - o;
+    if (more > 0 && more <= kFew)
+      for (int k = 0; k < more; ++k) {
+        const int page = taken[first + k];
+        e[o + k] = page;
+        a.refs[page] = 1;
+      }
+    for (uint64_t many = __ballot(more > kFew); many; many &= many - 1) {
+      const int of = __ffsll((unsigned long long)many) - 1;
+      const int f = __shfl(first, of), m = __shfl(more, of), at = __shfl(o, of);
+      int32_t* const w = a.table + (int64_t)(r0 + (tid & ~63) + of) * a.ldt + at;
+      for (int k = lane; k < m; k += 64) {
+        const int page = taken[f + k];
+        w[k] = page;
+        a.refs[page] = 1;
+      }
     }
   }
 }
@@ -276,38 +295,64 @@ struct CompactArgs {
   int32_t rows, width, pages;
 };
 
-// One workgroup: the k-th page in use behind their count goes into the k-th hole in front of it.
+// One workgroup: the k-th page in use behind their count goes into the k-th hole in front of it.  With r the
+// pages in use in front of page p, a hole is the (p - r)-th, a page behind the count the (r - r0)-th one to
+// move, r0 the pages in use in front of the count: one running sum gives both lists.
 __global__ __launch_bounds__(kWide) void pages_place_kernel(CompactArgs a) {
   __shared__ int part[kWide / 64];
+  __shared__ int in_front;
   const int tid = threadIdx.x;
-  int live = 0;
-  for (int p = tid; p < a.pages; p += kWide) live += a.refs[p] > 0;
-  int total;
-  scan_wide(live, part, total);
-  for (int pass = 0; pass < 2; ++pass) {  // holes, then the pages that fill them
-    int32_t* const list = pass == 0 ? a.dst : a.src;
-    int found = 0;
-    const int from = pass == 0 ? 0 : total, to = pass == 0 ? total : a.pages;
-    for (int p0 = from; p0 < to; p0 += kWide) {
-      const int p = p0 + tid;
-      const bool hit = p < to && (a.refs[p] > 0) == (pass == 1);
-      int sum;
-      const int at = found + scan_wide(hit, part, sum);
-      if (hit && at < a.capacity) list[at] = p;
-      found += sum;
+  auto refs_at = [&](int p0, int (&refs)[kPer]) {
+    int live = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int p = p0 + tid * kPer + k;
+      refs[k] = p < a.pages ? a.refs[p] : 0;
+      live += refs[k] > 0;
     }
-    for (int64_t i = found + tid; i < a.capacity; i += kWide) list[i] = -1;
+    return live;
+  };
+  int refs[kPer], live = 0, total;
+  for (int p0 = 0; p0 < a.pages; p0 += kStep) live += refs_at(p0, refs);
+  scan_wide(live, part, total);
+  if (tid == 0) in_front = 0;
+  int found = 0;
+  for (int p0 = 0; p0 < a.pages; p0 += kStep) {
+    live = a.pages > kStep ? refs_at(p0, refs) : live;
+    int sum;
+    const int before = found + scan_wide(live, part, sum);
+    int r = before;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (p0 + tid * kPer + k == total) in_front = r;
+      r += refs[k] > 0;
+    }
+    __syncthreads();
+    const int r0 = in_front;
+    r = before;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int p = p0 + tid * kPer + k;
+      if (p >= a.pages) break;
+      const bool used = refs[k] > 0;
+      if (p < total && used) a.new_refs[p] = refs[k];
+      if (p >= total) a.new_refs[p] = 0;
+      if (!(p >= total && used)) a.place[p] = p;
+      if (p < total && !used) a.dst[p - r] = p;
+      if (p >= total && used) a.src[r - r0] = p;
+      r += used;
+    }
+    found += sum;
   }
-  for (int p = tid; p < a.pages; p += kWide) {
-    a.place[p] = p;
-    const int n = a.refs[p];
-    a.new_refs[p] = p < total ? n : 0;
-  }
-  __threadfence();
   __syncthreads();
+  // (as many holes in front as pages behind: the count less those in use in front)
+  const int moves = total < a.pages ? total - in_front : 0;
   for (int64_t i = tid; i < a.capacity; i += kWide) {
-    const int s = fresh(a.src + i), d = fresh(a.dst + i);
-    if (s < 0 || d < 0) break;
+    if (i >= moves) {
+      a.src[i] = a.dst[i] = -1;
+      continue;
+    }
+    const int s = a.src[i], d = a.dst[i];
     a.place[s] = d;
     a.new_refs[d] = a.refs[s];
   }
@@ -332,18 +377,32 @@ struct CopyArgs {
   int64_t pairs;
 };
 
-// A workgroup copies pairs of one array in turn, V bytes a lane.
+// A workgroup copies pairs of one array in turn, V bytes a lane; rows of several runs of strides
+// are counted through.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 template <typename V>
 __device__ __forceinline__ void copy_page(const gptq_page_array& v, int64_t s, int64_t d) {
   const char* from = static_cast<const char*>(v.data) + s * v.page_stride;
   char* to = static_cast<char*>(v.data) + d * v.page_stride;
   const int64_t n = v.row_bytes / (int)sizeof(V);
-  for (int64_t o = 0; o < v.outer; ++o)
-    for (int64_t i = 0; i < v.inner; ++i) {
-      const V* f = reinterpret_cast<const V*>(from + o * v.outer_stride + i * v.inner_stride);
-      V* t = reinterpret_cast<V*>(to + o * v.outer_stride + i * v.inner_stride);
-      for (int64_t b = threadIdx.x; b < n; b += 256) t[b] = f[b];
+  constexpr int AHEAD = 4;
+  if (v.outer * v.inner == 1) {
+    const V* f = reinterpret_cast<const V*>(from);
+    V* t = reinterpret_cast<V*>(to);
+    int64_t b = threadIdx.x;
+    for (; b + (AHEAD - 1) * 256 < n; b += AHEAD * 256) {
+      const V x0 = f[b], x1 = f[b + 256], x2 = f[b + 512], x3 = f[b + 768];
+      t[b] = x0; t[b + 256] = x1; t[b + 512] = x2; t[b + 768] = x3;
     }
+    for (; b < n; b += 256) t[b] = f[b];
+    return;
+  }
+  for (int64_t u = threadIdx.x; u < v.outer * v.inner * n; u += 256) {
+    const int64_t row = u / n, o = row / v.inner, i = row - o * v.inner;
+    const int64_t at = o * v.outer_stride + i * v.inner_stride + (u - row * n) * (int)sizeof(V);
+    *reinterpret_cast<V*>(to + at) = *reinterpret_cast<const V*>(from + at);
+  }
 }
 
 __global__ __launch_bounds__(256) void pages_copy_kernel(CopyArgs a) {
@@ -357,7 +416,7 @@ __global__ __launch_bounds__(256) void pages_copy_kernel(CopyArgs a) {
       if (a.info && threadIdx.x == 0) *a.info = 1;
       continue;
     }
-    if (all % 16 == 0) copy_page<uint4>(v, s, d);
+    if (all % 16 == 0) copy_page<u32x4>(v, s, d);
     else if (all % 4 == 0) copy_page<uint32_t>(v, s, d);
     else copy_page<uint8_t>(v, s, d);
   }
@@ -381,15 +440,17 @@ hipError_t launch_kv_pages_fork(const int32_t* table, int64_t ldt, const int32_t
   return hipGetLastError();
 }
 
-size_t kv_pages_resize_ws_bytes(int64_t rows, int64_t pages) { return (size_t)(3 * pages + rows) * 4; }
+size_t kv_pages_resize_ws_bytes(int64_t rows, int64_t pages) {
+  return (size_t)((pages > kHeld ? pages : 0) + (rows > kWide ? rows : 0)) * 4;
+}
 
 hipError_t launch_kv_pages_resize(int32_t* table, int64_t ldt, int64_t width, int32_t* lengths,
                                   int64_t rows, int32_t* refs, int64_t pages,
                                   const int32_t* new_lengths, int page_size, int32_t* src,
                                   int32_t* dst, int32_t* info, void* ws, hipStream_t stream) {
   int32_t* w = static_cast<int32_t*>(ws);
-  ResizeArgs a{table, lengths, refs, new_lengths, src, dst, info, w, w + pages, w + 2 * pages,
-               w + 3 * pages, ldt, (int32_t)rows, (int32_t)width, (int32_t)pages, page_size};
+  ResizeArgs a{table, lengths, refs, new_lengths, src, dst, info, w, w + (pages > kHeld ? pages : 0),
+               ldt, (int32_t)rows, (int32_t)width, (int32_t)pages, page_size};
   hipLaunchKernelGGL(pages_drop_kernel, dim3((unsigned)ceil_div(rows, 4)), dim3(256), 0, stream, a);
   hipLaunchKernelGGL(pages_grow_kernel, dim3(1), dim3(kWide), 0, stream, a);
   return hipGetLastError();

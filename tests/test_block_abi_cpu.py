@@ -120,7 +120,10 @@ def test_pages():
     for kw in (dict(table=None), dict(lens=None), dict(refs=None), dict(new=None), dict(new=FAKE), dict(src=None), dict(dst=None),
                dict(dst=FAKE), dict(rows=-1), dict(width=0), dict(pages=0), dict(page=0), dict(ldt=7), dict(ws=FAKE + 2)):
         assert resize(**kw) == BAD, kw
-    assert resize(ws=None) == WS and resize(nbytes=64) == WS and resize(pages=1 << 25) == UNSUP
+    # (few rows and pages need no workspace)
+    many = dict(pages=10000)
+    assert resize(**many, ws=None) == WS and resize(**many, nbytes=64) == WS and resize(pages=1 << 25) == UNSUP
+    assert gq.kv_pages_resize_workspace_size(1024, 8192) == 0 and gq.kv_pages_resize_workspace_size(1025, 8192) > 0
 
     def compact(table=FAKE, ldt=8, rows=4, width=8, refs=FAKE, pages=100, nt=2 * FAKE, ldn=8, nr=2 * FAKE, src=FAKE, dst=2 * FAKE, cap=50,
                 count=FAKE, ws=FAKE, nbytes=1 << 30):
@@ -142,7 +145,7 @@ def test_page_copies():
 
     def copy(n=1, src=FAKE, dst=FAKE, pairs=3, arrays=True, **kw):
         v = (_lib.GPTQPageArray * 1)(_lib.GPTQPageArray(**{**a, **kw}))
-        return so.kv_pages_copy(ctypes.addressof(v) if arrays else None, n, src, dst, pairs, None, None)
+        return so.kv_pages_copy(bytes(v) if arrays else None, n, src, dst, pairs, None, None)
 
     assert copy(pairs=0) == OK and copy(n=0) == OK and copy(n=0, arrays=False) == OK
     for kw in (dict(arrays=False), dict(n=-1), dict(pairs=-1), dict(src=None), dict(dst=None), dict(data=None), dict(pages=0), dict(outer=0),
