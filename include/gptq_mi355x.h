@@ -570,7 +570,8 @@ gptq_status token_logprobs(const void* logits, gptq_dtype dt, int64_t tokens, in
  * and neither read nor written.  A page number that a position needs and that is not a
  * page (or a position past the table) is not accessed, and *info (a device int32 that the
  * caller has cleared, may be NULL) becomes 1.  seqs <= tokens is not needed; a
- * sequence may have no rows.
+ * sequence may have no rows.  GPTQ_ERR_UNSUPPORTED where a call would be of 2^24
+ * workgroups or more (millions of sequences).
  *
  * kv_block_write: rows K, V [tokens][heads][head_dim] (strides in elements, fp32 or
  * bf16) to their sequences' places in kb and vb (either may be NULL with its rows).  With a
@@ -654,7 +655,8 @@ gptq_status kv_block_attention(const void* Q, int64_t q_token_stride, int64_t q_
  * kv_pages_copy: page dst[k] = page src[k] in each of n arrays, for every pair with both
  *   not negative.  A page that is written is neither read nor written by another pair.  An array's page is
  *   outer x inner rows of row_bytes, their strides in bytes.
- * rows, new_rows, pages, pairs <= 2^24, rows * width < 2^30, pages * page_size < 2^31.
+ * rows, new_rows, pages, pairs <= 2^24, rows * width < 2^30, pages * page_size < 2^31;
+ * fork: rows and new_rows + pages / 256 below 2^24 (GPTQ_ERR_UNSUPPORTED).
  * ---------------------------------------------------------------------- */
 typedef struct gptq_page_array {
   void* data;
@@ -701,7 +703,8 @@ gptq_status kv_pages_copy(const gptq_page_array* arrays, int64_t n, const int32_
  * target, draft [tokens][vocab] (row strides ldt, ldd; fp32 or bf16 each).  -inf is a masked
  * logit.  An id outside the vocabulary is refused, as is one whose rows hold a NaN or +inf or
  * nothing but -inf; from such a target row nothing is drawn (-1).  Acceptance sums in fp32, the
- * draw in fp64.  Workspace (16-byte aligned): verify_drafts_workspace_size(tokens, vocab, seqs).
+ * draw in fp64.  tokens, seqs < 2^24 (else GPTQ_ERR_UNSUPPORTED).  Workspace (16-byte aligned):
+ * verify_drafts_workspace_size(tokens, vocab, seqs).
  * ---------------------------------------------------------------------- */
 gptq_status verify_drafts_workspace_size(int64_t tokens, int64_t vocab, int64_t seqs,
                                          size_t* bytes);

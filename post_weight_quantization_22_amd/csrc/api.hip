@@ -126,6 +126,11 @@ gptq_status kv_sequences_ok(const KvSequences& q) {
   return GPTQ_OK;
 }
 
+// what a launcher says whose grid would be larger than the hardware's counters
+gptq_status grid_status(hipError_t e) {
+  return e == hipErrorInvalidConfiguration ? GPTQ_ERR_UNSUPPORTED : hip_status(e);
+}
+
 // tables of pages: their sizes
 gptq_status pages_ok(int64_t rows, int64_t width, int64_t pages, int32_t page_size) {
   if (rows < 0 || width <= 0 || pages <= 0 || page_size <= 0) return GPTQ_ERR_INVALID_ARG;
@@ -641,7 +646,7 @@ gptq_status kv_block_write(const void* K, int64_t k_token_stride, int64_t k_head
     return GPTQ_ERR_INVALID_ARG;
   const KvRows k{const_cast<void*>(K), k_token_stride, k_head_stride};
   const KvRows v{const_cast<void*>(V), v_token_stride, v_head_stride};
-  return hip_status(launch_kv_block_write(k, v, dt, q, kb, vb, info, stream));
+  return grid_status(launch_kv_block_write(k, v, dt, q, kb, vb, info, stream));
 }
 
 gptq_status kv_block_attention_workspace_size(const gptq_kv_blocks* kb, int32_t q_heads,
@@ -688,7 +693,7 @@ gptq_status kv_block_attention(const void* Q, int64_t q_token_stride, int64_t q_
   t.out = KvRows{out, o_token_stride, o_head_stride};
   t.lse = lse;
   t.dt = dt; t.q_heads = q_heads; t.causal = causal; t.window = window; t.scale = scale;
-  return hip_status(launch_kv_attention(t, q, kb, vb, info, ws, stream));
+  return grid_status(launch_kv_attention(t, q, kb, vb, info, ws, stream));
 }
 
 gptq_status kv_pages_fork(const int32_t* table, int64_t ldt, const int32_t* lengths, int64_t rows,
@@ -704,7 +709,7 @@ gptq_status kv_pages_fork(const int32_t* table, int64_t ldt, const int32_t* leng
       (new_rows > 0 && (!parents || !new_table || !new_lengths || (new_rows > 1 && ldn < width) ||
                         new_table == table || new_lengths == lengths)))
     return GPTQ_ERR_INVALID_ARG;
-  return hip_status(launch_kv_pages_fork(table, ldt, lengths, rows, refs, pages, parents, new_rows,
+  return grid_status(launch_kv_pages_fork(table, ldt, lengths, rows, refs, pages, parents, new_rows,
                                          page_size, new_table, ldn, width, new_lengths, new_refs,
                                          info, stream));
 }
@@ -804,7 +809,7 @@ gptq_status verify_drafts(const void* target, gptq_dtype tdt, int64_t ldt, const
   a.tokens = tokens; a.vocab = vocab; a.seqs = seqs;
   a.ids = ids; a.starts = starts; a.u = u; a.u_next = u_next; a.temps = temperatures;
   a.accepted = accepted; a.out = tokens_out; a.logprobs = logprobs; a.ws = ws;
-  return hip_status(launch_verify(a, stream));
+  return grid_status(launch_verify(a, stream));
 }
 
 }  // extern "C"

@@ -110,6 +110,8 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t hmin(int64_t a, int64_t b) { return a < b ? a : b; }
 inline int64_t hmax(int64_t a, int64_t b) { return a > b ? a : b; }
+// whether the threads of a grid's first dimension can be counted in 32 bits
+inline bool grid_fits(int64_t groups, int64_t threads) { return groups * threads <= UINT32_MAX; }
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 

@@ -169,6 +169,7 @@ struct TileRows {  // what a workgroup works on
   Span sp;
   int row0, rows;  // of the sequence's rows * group
   int lo, hi;      // its keys, lo a multiple of 16
+  bool bad;        // keys that the table has no entry for
 };
 
 __device__ __forceinline__ TileRows tile_rows(const AttnArgs& a, int task, int per) {
@@ -184,8 +185,10 @@ __device__ __forceinline__ TileRows tile_rows(const AttnArgs& a, int task, int p
   if (t.rows > 0 && a.causal) {
     const int p0 = base + divided(t.row0, a.by_group), p1 = base + divided(t.row0 + t.rows - 1, a.by_group);
     t.hi = max(min(t.hi, p1 + 1), 0);
-    if (a.window > 0) t.lo = max(p0 - a.window + 1, 0) & ~15;
+    if (a.window > 0) t.lo = max(max(p0, 0) - a.window + 1, 0) & ~15;  // (a row in front of position 0 sees nothing)
   }
+  t.bad = t.hi > a.s.room;
+  t.hi = min(t.hi, a.s.room);
   return t;
 }
 
@@ -468,7 +471,7 @@ __global__ __launch_bounds__(kThreads, F32 || DP == 256 ? 1 : MT == 1 ? 3 : 2) v
   const int32_t* table = a.s.table + t.sp.seq * a.s.ldt;
   const int kfirst = kb + kTile * wave;
   const Side kc = side_of(a.k, head), vc = side_of(a.v, head);
-  bool bad = false;
+  bool bad = t.bad;
 
   const int zero = lane_zero();
   uint32_t kraw[2][KW], vraw[VW][8];
@@ -811,7 +814,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 && F32 ? 1 : 2) void kv_attenti
   const int64_t tpage = of_keys ? kc.cpage : vc.cpage, tppage = of_keys ? kc.ppage : vc.ppage;
   const int32_t tslot = of_keys ? kc.cslot : vc.cslot, tblock = of_keys ? kc.pblock : vc.pblock;
   const float* const tscales = of_keys ? kc.scales : vc.scales;
-  bool bad = false, known = false;
+  bool bad = t.bad, known = false;
   float sc = 0.0f;
   auto entry_of = [&](int k0) {
     return looks ? table[min(divided(min(k0 + ti, ke - 1), a.s.by_page), a.s.width - 1)] : 0;
@@ -864,7 +867,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 && F32 ? 1 : 2) void kv_attenti
     for (int h = 0; h < KEYS / 32; ++h) {
       const int kh = k0 + 32 * h;
       // keys that none of the wave's rows sees
-      if (idle || kh >= ke || (a.causal && (kh > pos_last || (a.window > 0 && kh + 31 <= pos_first - a.window)))) continue;
+      if (idle || kh >= ke || (a.causal && (kh > pos_last || (a.window > 0 && kh + 31 <= max(pos_first, 0) - a.window)))) continue;
       f32x4 s[MT][2];
       {
         uint4 kw[2][STEPS];
@@ -1168,6 +1171,7 @@ hipError_t launch_kv_attention(const KvAttention& t, const KvSequences& seqs,
                                const gptq_kv_blocks* kb, const gptq_kv_blocks* vb, int32_t* info,
                                void* ws, hipStream_t stream) {
   const Plan p = plan_of(kb, t.q_heads, t.dt, seqs.tokens, seqs.seqs, seqs.width);
+  if (!grid_fits(p.tiles ? p.tasks * kb->heads : p.tasks, kThreads)) return hipErrorInvalidConfiguration;
   const bool f32 = t.dt == GPTQ_F32;
   const int dp = padded_dim(kb->head_dim), per16 = f32 ? 4 : 8;
   AttnArgs a = {};

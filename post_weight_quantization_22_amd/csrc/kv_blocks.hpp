@@ -40,6 +40,7 @@ struct Sequences {
   int64_t ldt;
   int32_t width, seqs, tokens;
   int32_t pages, page_size, block;
+  int32_t room;  // positions that the table has entries for
   Divisor by_page, by_block;
   int32_t* info;
 };
@@ -89,6 +90,7 @@ inline Sequences sequences_of(const KvSequences& q, const gptq_kv_blocks* c, int
   s.table = q.table; s.lengths = q.lengths; s.starts = q.starts;
   s.ldt = q.ldt; s.width = (int32_t)q.width; s.seqs = (int32_t)q.seqs; s.tokens = (int32_t)q.tokens;
   s.pages = (int32_t)c->pages; s.page_size = c->page_size; s.block = c->block;
+  s.room = (int32_t)hmin(q.width * c->page_size, INT32_MAX - 65536);  // (tiles are counted past the end)
   s.by_page = divisor_of(c->page_size);
   s.by_block = divisor_of(c->block);
   s.info = info;

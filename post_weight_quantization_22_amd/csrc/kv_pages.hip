@@ -216,7 +216,7 @@ __global__ __launch_bounds__(kWide) void pages_grow_kernel(ResizeArgs a) {
     total += sum;
   }
   // the lowest free pages, as many as that
-  int* const taken = total <= kHeld ? held_taken : a.taken;
+  int* const taken = total <= kHeld || a.pages <= kHeld ? held_taken : a.taken;
   int found = 0;
   for (int p0 = 0; p0 < a.pages && found < total; p0 += kStep) {
     if (p0 > 0) free_at(p0, free);
@@ -434,8 +434,9 @@ hipError_t launch_kv_pages_fork(const int32_t* table, int64_t ldt, const int32_t
              new_refs,  info,      ldt,  ldn,           (int32_t)rows,     (int32_t)new_rows,
              (int32_t)width, (int32_t)pages, page_size};
   const dim3 block(256);
-  hipLaunchKernelGGL(pages_rows_kernel, dim3((unsigned)(new_rows + ceil_div(pages, 256))), block, 0,
-                     stream, a);
+  const int64_t groups = new_rows + ceil_div(pages, 256);
+  if (!grid_fits(hmax(groups, rows), 256)) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL(pages_rows_kernel, dim3((unsigned)groups), block, 0, stream, a);
   if (rows > 0) hipLaunchKernelGGL(pages_refs_kernel, dim3((unsigned)rows), block, 0, stream, a);
   return hipGetLastError();
 }

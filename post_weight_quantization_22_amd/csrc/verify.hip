@@ -546,6 +546,7 @@ size_t verify_ws_bytes(int64_t tokens, int64_t vocab, int64_t seqs) {
 }
 
 hipError_t launch_verify(const VerifyArgs& v, hipStream_t stream) {
+  if (!grid_fits(hmax(v.tokens, v.seqs), kThreads)) return hipErrorInvalidConfiguration;
   VerifyCall a;
   a.v = v;
   const Segments ss = segments(2 * v.tokens, v.vocab), ds = segments(v.seqs, v.vocab);

@@ -186,3 +186,20 @@ def test_the_binding_refuses_host_tensors():
             bad()
     with pytest.raises(ValueError, match="fmt"):
         gq.make_kv_blocks(None, None, "int4")
+
+
+def test_grids_past_the_hardware():
+    """Calls whose workgroups' threads could not be counted in 32 bits (pointers are not looked at)."""
+    so = _lib.load()
+    N = 1 << 24
+    kb, vb = _cache(head_dim=256, slot_stride=512, head_stride=256, page_stride=16 * 512, block=4, param_page_stride=8), _cache(
+        **OTHER, head_dim=256, slot_stride=512, head_stride=256, page_stride=16 * 512, block=4, param_page_stride=8)
+    assert so.kv_block_write(FAKE, 512, 256, FAKE, 512, 256, 1, N, FAKE, 3, 3, FAKE, FAKE, N // 2 - 1, ctypes.byref(kb),
+                             ctypes.byref(vb), None, None) == UNSUP
+    assert so.kv_block_attention(FAKE, 512, 256, 1, 2, 2, ctypes.byref(kb), ctypes.byref(vb), FAKE, 3, 3, FAKE, FAKE, N, 1, 0, 0.1,
+                                 3 * FAKE, 512, 256, None, None, FAKE, 1 << 50, None) == UNSUP
+    for rows, new in ((N, 4), (4, N)):
+        assert so.kv_pages_fork(FAKE, 8, FAKE, rows, 8, FAKE, 100, FAKE, new, 16, 2 * FAKE, 8, 2 * FAKE, 2 * FAKE, None, None) == UNSUP
+    for t, seqs in ((N, 1), (1, N)):
+        assert so.verify_drafts(FAKE, 1, 100, None, 0, 0, t, 100, FAKE, FAKE, seqs, FAKE, FAKE, None, FAKE, 2 * FAKE, None, FAKE,
+                                1 << 50, None) == UNSUP
