@@ -7,6 +7,13 @@
 // Forking copies no page.  A page is copied when a sequence is about to write into it while
 // others hold it: kv_pages_resize gives that sequence a page of its own and names the pair,
 // which kv_pages_copy then copies in every layer's arrays.  Pages are taken lowest first.
+//
+// Launches bound all of this but the copies (a call's host time, some 2 us between kernels, a few round
+// trips in each): a table of some thousand entries is settled by one workgroup in one launch (fork 3.5
+// us, growth with what it takes back 7, compaction 4 to 6), which a larger one would keep waiting for
+// one workgroup's loads (6 rows forked, grown and copied: two launches for a fork and for a resize 26 us,
+// one 22; 250 pages compacted and copied 17.5 and 15.8).  Copies go at the memory's rate (2000 pages' halves of
+// 64 KB in 8 arrays: 4.8 TB/s).
 #include "kernels.hpp"
 
 namespace gptq {
@@ -18,6 +25,8 @@ constexpr int kPer = 4;       // pages that a thread looks at in one step
 constexpr int kStep = kWide * kPer;
 constexpr int kRows = 4096;   // rows whose last pages are compared at a time
 constexpr int kHeld = 8192;   // fresh pages that LDS holds
+constexpr int kSmall = 8192;  // pages and table entries that one workgroup forks or renames by itself
+constexpr int kEntries = 32768;  // .. takes back
 
 __device__ __forceinline__ int pages_of(int len, int page_size) {
   return (int)(((int64_t)max(len, 0) + page_size - 1) / page_size);
@@ -102,6 +111,62 @@ __global__ __launch_bounds__(256) void pages_refs_kernel(ForkArgs a) {
   }
 }
 
+// Both for few rows and pages, in one workgroup: a launch less, and what pages gain is added up in LDS.
+__global__ __launch_bounds__(kWide) void pages_fork_kernel(ForkArgs a) {
+  __shared__ int children[kWide];
+  __shared__ int gain[kSmall];
+  const int tid = threadIdx.x;
+  children[tid] = -1;  // (less the row itself)
+  for (int i = tid; i < a.pages; i += kWide) gain[i] = 0;
+  __syncthreads();
+  auto parent = [&](int row) {
+    const int p = a.parents[row];
+    return p < a.rows ? p : -1;
+  };
+  auto outside = [&] {
+    if (a.info) atomicOr(a.info, 1);
+  };
+  for (int i = tid; i < a.new_rows; i += kWide) {
+    const int p = parent(i);
+    if (p >= 0) atomicAdd(children + p, 1);
+    const int len = p < 0 ? 0 : max(a.lengths[p], 0);
+    a.new_lengths[i] = len;
+    if (a.parents[i] >= a.rows || pages_of(len, a.page_size) > a.width) outside();
+  }
+  // four entries of a thread under way
+  for (int u0 = tid; u0 < a.new_rows * a.width; u0 += 4 * kWide) {
+    int p[4], len[4], page[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int u = min(u0 + k * kWide, a.new_rows * a.width - 1);
+      p[k] = parent(u / a.width);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int u = min(u0 + k * kWide, a.new_rows * a.width - 1);
+      len[k] = p[k] < 0 ? 0 : a.lengths[p[k]];
+      page[k] = p[k] < 0 ? -1 : a.table[p[k] * a.ldt + u % a.width];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int u = u0 + k * kWide;
+      if (u >= a.new_rows * a.width) break;
+      const int row = u / a.width, j = u - row * a.width;
+      a.new_table[row * a.ldn + j] = j < pages_of(len[k], a.page_size) ? page[k] : -1;
+    }
+  }
+  __syncthreads();
+  for (int u = tid; u < a.rows * a.width; u += kWide) {
+    const int row = u / a.width, j = u - row * a.width, c = children[row];
+    const int n = pages_of(a.lengths[row], a.page_size), page = a.table[row * a.ldt + j];
+    if (c == 0 || j >= n) continue;
+    if (page >= 0 && page < a.pages) atomicAdd(gain + page, c);
+    else outside();
+  }
+  __syncthreads();
+  for (int i = tid; i < a.pages; i += kWide) a.new_refs[i] = a.refs[i] + gain[i];
+}
+
 struct ResizeArgs {
   int32_t* table;
   int32_t* lengths;
@@ -147,12 +212,19 @@ __global__ __launch_bounds__(256) void pages_drop_kernel(ResizeArgs a) {
   if (lane == 0) a.lengths[row] = want;
 }
 
+// A load that sees what the same kernel's atomics have done (past the first-level cache).
+__device__ __forceinline__ int settled(const int* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // One workgroup: who gets which free pages.  A step of a batch waits for it, so it is one chain of few
 // round trips: rows and the first free pages are read at once, shared pages are found among the rows'
 // last ones in LDS, nothing is fenced (what waves exchange in memory goes through one first-level cache).
+// DROP: few rows and entries, whose shorter ends it takes back first, a launch less.
+template <bool DROP>
 __global__ __launch_bounds__(kWide) void pages_grow_kernel(ResizeArgs a) {
   __shared__ int part[kWide / 64];
-  __shared__ __align__(16) int lasts[kRows];
+  __shared__ __align__(16) int lasts[kRows];  // (DROP: where the rows' entries to take back begin and end first)
   __shared__ int held_taken[kHeld];
   const int tid = threadIdx.x, lane = tid & 63;
   struct Row {
@@ -172,22 +244,58 @@ __global__ __launch_bounds__(kWide) void pages_grow_kernel(ResizeArgs a) {
     }
     return r;
   };
+  bool dropped = false;
+  auto refs_at = [&](int p) { return DROP && dropped ? settled(a.refs + p) : a.refs[p]; };
   auto free_at = [&](int p0, int (&free)[kPer]) {
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const int p = p0 + tid * kPer + k;
-      free[k] = p < a.pages && a.refs[p] == 0;
+      free[k] = p < a.pages && refs_at(p) == 0;
     }
   };
   int free[kPer];
   free_at(0, free);
+  if constexpr (DROP) {  // (a thread's row: kWide of them at most)
+    const int len = tid < a.rows ? a.lengths[tid] : 0;
+    bool bad = false;
+    const int want = tid < a.rows ? wanted(a, tid, len, bad) : 0;
+    if (tid < a.rows) a.src[tid] = a.dst[tid] = -1;
+    if (bad && a.info) atomicOr(a.info, 1);
+    if (want < len) a.lengths[tid] = want;
+    const int from = pages_of(want, a.page_size), to = want < len ? min(pages_of(len, a.page_size), a.width) : 0;
+    lasts[tid] = from;
+    lasts[kWide + tid] = to;
+    dropped = __syncthreads_or(from < to);
+    if (dropped) {
+      for (int u0 = tid; u0 < a.rows * a.width; u0 += 4 * kWide) {  // entries, four of a thread under way
+        int32_t* e[4];
+        int page[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int u = u0 + k * kWide, row = u / a.width, j = u - row * a.width;
+          e[k] = u < a.rows * a.width && j >= lasts[row] && j < lasts[kWide + row] ? a.table + row * a.ldt + j : nullptr;
+          if (e[k]) page[k] = *e[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (!e[k]) continue;
+          *e[k] = -1;
+          if (page[k] >= 0 && page[k] < a.pages) atomicSub(a.refs + page[k], 1);
+          else if (a.info) atomicOr(a.info, 1);
+        }
+      }
+      __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (they have arrived in front of the barrier)
+      __syncthreads();
+      free_at(0, free);
+    }
+  }
   // A shared page stays with the last of its holders if all of them write into it.
   Row r;
   bool copy = false;
   int total = 0, base = 0;
   for (int r0 = 0; r0 < a.rows; r0 += kWide) {
     r = row_at(r0 + tid);
-    r.held = r.last >= 0 ? a.refs[r.last] : 0;
+    r.held = r.last < 0 ? 0 : refs_at(r.last);
     const bool shared = r.held > 1;
     int writers = 0, top = -1;
     if (__syncthreads_or(shared)) {
@@ -298,9 +406,13 @@ struct CompactArgs {
 // One workgroup: the k-th page in use behind their count goes into the k-th hole in front of it.  With r the
 // pages in use in front of page p, a hole is the (p - r)-th, a page behind the count the (r - r0)-th one to
 // move, r0 the pages in use in front of the count: one running sum gives both lists.
+// SMALL: few pages and entries, whose new names it writes too, from the places that it keeps in LDS.
+template <bool SMALL>
 __global__ __launch_bounds__(kWide) void pages_place_kernel(CompactArgs a) {
   __shared__ int part[kWide / 64];
   __shared__ int in_front;
+  __shared__ int places[SMALL ? kSmall : 1];
+  int* const place = SMALL ? places : a.place;
   const int tid = threadIdx.x;
   auto refs_at = [&](int p0, int (&refs)[kPer]) {
     int live = 0;
@@ -337,7 +449,7 @@ __global__ __launch_bounds__(kWide) void pages_place_kernel(CompactArgs a) {
       const bool used = refs[k] > 0;
       if (p < total && used) a.new_refs[p] = refs[k];
       if (p >= total) a.new_refs[p] = 0;
-      if (!(p >= total && used)) a.place[p] = p;
+      if (!(p >= total && used)) place[p] = p;
       if (p < total && !used) a.dst[p - r] = p;
       if (p >= total && used) a.src[r - r0] = p;
       r += used;
@@ -353,10 +465,17 @@ __global__ __launch_bounds__(kWide) void pages_place_kernel(CompactArgs a) {
       continue;
     }
     const int s = a.src[i], d = a.dst[i];
-    a.place[s] = d;
+    place[s] = d;
     a.new_refs[d] = a.refs[s];
   }
   if (tid == 0) *a.count = total;
+  if constexpr (SMALL) {
+    __syncthreads();
+    for (int u = tid; u < a.rows * a.width; u += kWide) {
+      const int row = u / a.width, j = u - row * a.width, p = a.table[row * a.ldt + j];
+      a.new_table[row * a.ldn + j] = p >= 0 && p < a.pages ? places[p] : p;
+    }
+  }
 }
 
 __global__ __launch_bounds__(256) void pages_rename_kernel(CompactArgs a) {
@@ -434,6 +553,10 @@ hipError_t launch_kv_pages_fork(const int32_t* table, int64_t ldt, const int32_t
              new_refs,  info,      ldt,  ldn,           (int32_t)rows,     (int32_t)new_rows,
              (int32_t)width, (int32_t)pages, page_size};
   const dim3 block(256);
+  if (rows <= kWide && pages <= kSmall && hmax(rows, new_rows) * width <= kSmall) {
+    hipLaunchKernelGGL(pages_fork_kernel, dim3(1), dim3(kWide), 0, stream, a);
+    return hipGetLastError();
+  }
   const int64_t groups = new_rows + ceil_div(pages, 256);
   if (!grid_fits(hmax(groups, rows), 256)) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL(pages_rows_kernel, dim3((unsigned)groups), block, 0, stream, a);
@@ -452,8 +575,12 @@ hipError_t launch_kv_pages_resize(int32_t* table, int64_t ldt, int64_t width, in
   int32_t* w = static_cast<int32_t*>(ws);
   ResizeArgs a{table, lengths, refs, new_lengths, src, dst, info, w, w + (pages > kHeld ? pages : 0),
                ldt, (int32_t)rows, (int32_t)width, (int32_t)pages, page_size};
-  hipLaunchKernelGGL(pages_drop_kernel, dim3((unsigned)ceil_div(rows, 4)), dim3(256), 0, stream, a);
-  hipLaunchKernelGGL(pages_grow_kernel, dim3(1), dim3(kWide), 0, stream, a);
+  if (rows <= kWide && rows * width <= kEntries) {
+    hipLaunchKernelGGL(pages_grow_kernel<true>, dim3(1), dim3(kWide), 0, stream, a);
+  } else {
+    hipLaunchKernelGGL(pages_drop_kernel, dim3((unsigned)ceil_div(rows, 4)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(pages_grow_kernel<false>, dim3(1), dim3(kWide), 0, stream, a);
+  }
   return hipGetLastError();
 }
 
@@ -465,7 +592,11 @@ hipError_t launch_kv_pages_compact(const int32_t* table, int64_t ldt, int64_t ro
                                    int64_t capacity, int32_t* count, void* ws, hipStream_t stream) {
   CompactArgs a{table, refs, new_table, new_refs, src, dst, count, static_cast<int32_t*>(ws), ldt, ldn,
                 capacity, (int32_t)rows, (int32_t)width, (int32_t)pages};
-  hipLaunchKernelGGL(pages_place_kernel, dim3(1), dim3(kWide), 0, stream, a);
+  if (pages <= kSmall && rows * width <= kSmall) {
+    hipLaunchKernelGGL(pages_place_kernel<true>, dim3(1), dim3(kWide), 0, stream, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(pages_place_kernel<false>, dim3(1), dim3(kWide), 0, stream, a);
   if (rows > 0)
     hipLaunchKernelGGL(pages_rename_kernel, dim3((unsigned)hmin(rows, 4096)), dim3(256), 0, stream, a);
   return hipGetLastError();

@@ -186,6 +186,45 @@ def test_large_growth(rows, width, page, pages):
     assert got[5] == 0
 
 
+@pytest.mark.parametrize("rows,width,pages", [(900, 9, 8192), (911, 9, 8193), (1024, 8, 8190), (1025, 7, 8000), (20, 400, 7001), (64, 512, 14000), (65, 512, 14000)])
+def test_shrinking_and_growing_at_once(rows, width, pages):
+    """Pages that some rows give back go to others in the same call (tables that one workgroup settles and
+    larger ones; counts of holders that begin off any border)."""
+    q = need_gpu()
+    rng = np.random.default_rng(rows)
+    lens = [int(v) for v in rng.integers(0, width + 1, size=rows)]
+    while sum(lens) > pages:
+        lens[int(rng.integers(0, rows))] = 0
+    order, table, refs, at = rng.permutation(pages), [], [0] * pages, 0
+    for n in lens:
+        table.append([int(p) for p in order[at:at + n]] + [-1] * (width - n))
+        at += n
+    for row in table:
+        for p in row:
+            if p >= 0:
+                refs[p] = 1
+    # beams of one page's holders among them
+    for i in range(0, rows - 1, 5):
+        for p in table[i + 1]:
+            if p >= 0:
+                refs[p] -= 1
+        table[i + 1], lens[i + 1] = list(table[i]), lens[i]
+        for p in table[i]:
+            if p >= 0:
+                refs[p] += 1
+    page = 3
+    lens = [max(page * n - int(rng.integers(0, 3)), 0) if n else 0 for n in lens]
+    for turn in range(3):
+        new = [int(rng.integers(0, n + 1)) if rng.integers(0, 2) else min(n + int(rng.integers(0, 8)), page * width) for n in lens]
+        want = blocks.resize(table, lens, refs, new, page)
+        t, n, r = ints(table), ints(lens), ints([0] + refs)[1:]
+        src, dst, info = ints([7] * rows), ints([7] * rows), ints([0])
+        say("shrink and grow", rows, width, pages, turn)
+        q.kv_pages_resize(t, n, r, ints(new), page, src, dst, info=info)
+        assert tuple(host(x).tolist() for x in (t, n, r, src, dst)) + (int(info),) == want
+        table, lens, refs = want[:3]
+
+
 # ---- calls beside each other
 
 def _work_of(q, rng, S, rows, ctx):
