@@ -11,6 +11,11 @@
 // a few 2^-24, which moves a token across u q = p with that chance).  The draw compares a sum
 // over up to the whole vocabulary with a border; fp32's error would be as wide as many a token's
 // share, so the one row per sequence that is drawn from is summed in fp64.
+//
+// Three kernels: statistics of every row (the logits' stream: 64 sequences of 8 rows, 32000 fp32 logits of
+// both models in 20 us, 6 TB/s), acceptance with the sums of the row that is drawn from (12 us) and the draw
+// (16): chains of four and six round trips to memory, with some 50 fp64 operations a logit between them.
+// 4 sequences of 5 rows, 128000 bf16 logits: 6, 9 and 13 us.
 #include "kv_blocks.hpp"
 
 namespace gptq {
@@ -34,7 +39,6 @@ struct VerifyCall {
   double* sums;    // [3][seqs][dsegs]: e^((x - m) / temperature) of the target, of the drafter, the weights
   int4* draws;     // [seqs]: the row that is drawn from (-1: none), whether the drafter's law is taken off,
                    // the bits of both maxima
-  int32_t* done;   // [seqs]: segments whose weights are summed
   int32_t segs, dsegs;
   int64_t seg, dseg;  // logits of a segment
 };
@@ -223,13 +227,13 @@ __global__ __launch_bounds__(kThreads) void verify_accept_kernel(VerifyCall a) {
   __shared__ int refused;
   __shared__ Stat seen[ROUND];
   __shared__ float seen_mq[ROUND];
+  __shared__ bool seen_in[ROUND];  // the id is in the vocabulary
   __shared__ double part[kWaves];
   const int seq = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const bool writes = blockIdx.y == 0;
   const int T = (int)a.v.tokens;
   const int s0 = min(max(a.v.starts[seq], 0), T), n = min(max(a.v.starts[seq + 1], 0), T) - s0;
   const float t = temperature(a, seq);
-  if (writes && tid == 0) a.done[seq] = 0;
   if (n <= 0) {
     if (writes && tid == 0) {
       a.v.accepted[seq] = 0;
@@ -278,6 +282,7 @@ __global__ __launch_bounds__(kThreads) void verify_accept_kernel(VerifyCall a) {
         if (!good) atomicMin(&refused, j);
         seen[e * kWaves + wave] = p;
         seen_mq[e * kWaves + wave] = q.m;
+        seen_in[e * kWaves + wave] = in[e];
         if (writes && j < n - 1) {
           a.v.out[row[e]] = id[e];
           if (a.v.logprobs) a.v.logprobs[row[e]] = sure ? 0.0f : (xt[e] - p.m) / t - logf(p.sum);
@@ -296,8 +301,7 @@ __global__ __launch_bounds__(kThreads) void verify_accept_kernel(VerifyCall a) {
       a.v.out[s0 + j] = -1;
       if (a.v.logprobs) a.v.logprobs[s0 + j] = 0.0f;
     }
-  const int64_t id = a.v.ids[row];
-  const bool judged = taken < n - 1 && (a.v.draft || (id >= 0 && id < a.v.vocab));
+  const bool judged = taken < n - 1 && (a.v.draft || seen_in[at]);
   const Stat top = seen[at];
   const float mq = seen_mq[at];
   const bool law = top.sum > 0.0f && top.sum < __builtin_inff();  // numbers, one of them finite
@@ -339,6 +343,7 @@ __global__ __launch_bounds__(kThreads) void verify_accept_kernel(VerifyCall a) {
   if (tid == 0) {
     a.sums[(int64_t)seq * a.dsegs + blockIdx.y] = s;
     a.sums[(a.v.seqs + seq) * a.dsegs + blockIdx.y] = sq;
+    a.sums[(2 * a.v.seqs + seq) * a.dsegs + blockIdx.y] = -1.0;  // (not known yet)
   }
 }
 
@@ -358,28 +363,35 @@ __device__ __forceinline__ double weight_of(const Law& w, int64_t i, float xt, f
   return fmax(p - q, 0.0);
 }
 
-// weights of tokens i, i + kThreads, .., 0 from c1 on
-template <int TD, int DD, int N>
-__device__ __forceinline__ void weights_at(const VerifyCall& a, const Law& w, int64_t i, int64_t c1, double (&v)[N]) {
-  const bool both = w.judged && w.draft;
+// logits of tokens i, i + kThreads, .. (behind c1: the last one's)
+template <int N>
+struct Pairs {
   float xt[N], xd[N];
+};
+template <int TD, int DD, int N>
+__device__ __forceinline__ Pairs<N> pairs_at(const VerifyCall& a, int64_t row, bool both, int64_t i, int64_t c1) {
+  Pairs<N> p;
 #pragma unroll
   for (int e = 0; e < N; ++e) {
     const int64_t k = min(i + e * kThreads, c1 - 1);
-    xt[e] = logit<TD, DD>(a, false, w.row, k);
-    xd[e] = both ? logit<TD, DD>(a, true, w.row, k) : 0.0f;
+    p.xt[e] = logit<TD, DD>(a, false, row, k);
+    p.xd[e] = both ? logit<TD, DD>(a, true, row, k) : 0.0f;
   }
+  return p;
+}
+
+// their weights, 0 from c1 on
+template <int N>
+__device__ __forceinline__ void weights_of(const Law& w, const Pairs<N>& p, int64_t i, int64_t c1, double (&v)[N]) {
 #pragma unroll
   for (int e = 0; e < N; ++e) {
-    const double x = weight_of(w, i + e * kThreads, xt[e], xd[e]);
+    const double x = weight_of(w, i + e * kThreads, p.xt[e], p.xd[e]);
     v[e] = i + e * kThreads < c1 ? x : 0.0;
   }
 }
 
-// the sum of n <= 64 numbers, the same in every wave
-__device__ __forceinline__ double total_of(const double* p, int n) {
-  const int lane = threadIdx.x & 63;
-  double v = lane < n ? p[lane] : 0.0;
+// the sum of the lanes' numbers
+__device__ __forceinline__ double total_of(double v) {
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) v += lane_xor_d(v, m);
   return v;
@@ -396,60 +408,67 @@ __device__ __forceinline__ double wave_scan(double v) {
   return v;
 }
 
-// A workgroup per sequence and segment sums the segment's weights; the last one of a sequence to be
-// done finds the segment that holds the border, and in it the token.
+// A workgroup per sequence and segment sums the segment's weights; one that finds all of the sequence's
+// sums there finds the segment that holds the border, and in it the token.  That is the last one to be
+// done; others that are done at the same time may find them too, and write the same.
 template <int TD, int DD>
 __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyCall a) {
   constexpr int AHEAD = 8, CHUNK = AHEAD * kThreads;
   __shared__ double part[kWaves];
   __shared__ double held[CHUNK + CHUNK / AHEAD];  // a thread's run of 8 apart from the next one's, by a place
-  __shared__ int last, chosen;
+  __shared__ int chosen;
   const int seq = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  // two round trips in front of the sums: what hangs on the sequence alone, what hangs on the row
   const int4 d = a.draws[seq];
+  const float t = temperature(a, seq), next = a.v.u_next[seq];
+  const double sum_p = lane < a.dsegs ? a.sums[(int64_t)seq * a.dsegs + lane] : 0.0;
+  const double sum_q = lane < a.dsegs ? a.sums[(a.v.seqs + seq) * a.dsegs + lane] : 0.0;
   if (d.x < 0) return;
   Law w;
-  w.it = 1.0 / (double)temperature(a, seq);
-  w.m = __int_as_float(d.z);
-  w.mq = __int_as_float(d.w);
   w.row = d.x;
   w.judged = d.y != 0;
   w.draft = a.v.draft != nullptr;
+  const bool both = w.judged && w.draft;
+  const int64_t s0 = blockIdx.y * a.dseg, s1 = min(s0 + a.dseg, a.v.vocab);
+  Pairs<AHEAD> pairs = pairs_at<TD, DD, AHEAD>(a, w.row, both, s0 + tid, s1);
   w.id = a.v.ids[d.x];
-  w.zp = 1.0 / total_of(a.sums + (int64_t)seq * a.dsegs, a.dsegs);
-  w.zq = w.judged && w.draft ? 1.0 / total_of(a.sums + (a.v.seqs + seq) * a.dsegs, a.dsegs) : 1.0;
+  w.it = 1.0 / (double)t;
+  w.m = __int_as_float(d.z);
+  w.mq = __int_as_float(d.w);
+  w.zp = 1.0 / total_of(sum_p);
+  w.zq = both ? 1.0 / total_of(sum_q) : 1.0;
   double* const sums = a.sums + (2 * a.v.seqs + seq) * a.dsegs;
   {
-    const int64_t c0 = blockIdx.y * a.dseg, c1 = min(c0 + a.dseg, a.v.vocab);
     double s = 0.0;
-    for (int64_t i = c0 + tid; i < c1; i += CHUNK) {
+    for (int64_t b = s0; b < s1; b += CHUNK) {
+      if (b > s0) pairs = pairs_at<TD, DD, AHEAD>(a, w.row, both, b + tid, s1);
       double v[AHEAD];
-      weights_at<TD, DD, AHEAD>(a, w, i, c1, v);
+      weights_of(w, pairs, b + tid, s1, v);
 #pragma unroll
       for (int e = 0; e < AHEAD; ++e) s += v[e];
     }
     s = block_sum(s, part);
     if (tid == 0) {
-      // The sum goes past the caches by itself and has arrived before the count is raised; a fence would
+      // The sum goes past the caches by itself and has arrived before the others' are read; a fence would
       // write back everything that this part of the chip holds (64 sequences: 37 us, not 14).
       __hip_atomic_store(sums + blockIdx.y, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      last = __hip_atomic_fetch_add(a.done + seq, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == a.dsegs - 1;
     }
     __syncthreads();
   }
-  if (!last) return;
   double mine = lane < a.dsegs ? __hip_atomic_load(sums + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
+  if (__syncthreads_or(mine < 0.0)) return;
   double total = mine;
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) total += lane_xor_d(total, m);
   if (!(total > 0.0)) {  // p = q, or no number among the drafter's: the target's own law
     w.judged = false;
-    mine = lane < a.dsegs ? a.sums[(int64_t)seq * a.dsegs + lane] * w.zp : 0.0;
+    mine = sum_p * w.zp;
     total = mine;
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) total += lane_xor_d(total, m);
   }
-  const double border = fmin(fmax((double)a.v.u_next[seq], 0.0), 0x1.fffffep-1) * total;
+  const double border = fmin(fmax((double)next, 0.0), 0x1.fffffep-1) * total;
   // running sums over the segments: the first one that passes the border (rounding may leave it behind
   // all of them: the last one with any weight)
   const double upto = wave_scan(mine);
@@ -462,7 +481,7 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyCall a) {
   int token = -1;
   for (int64_t b = c0; b < c1; b += CHUNK) {
     double v[AHEAD];
-    weights_at<TD, DD, AHEAD>(a, w, b + tid, c1, v);
+    weights_of(w, pairs_at<TD, DD, AHEAD>(a, w.row, w.judged && w.draft, b + tid, c1), b + tid, c1, v);
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < AHEAD; ++e) held[(tid + e * kThreads) / AHEAD + tid + e * kThreads] = v[e];
@@ -527,15 +546,14 @@ Segments segments(int64_t rows, int64_t vocab) {
 }
 
 struct Layout {
-  size_t draws, sums, done, bytes;
+  size_t draws, sums, bytes;
 };
 
 Layout layout_of(int64_t tokens, int64_t seqs, int64_t segs, int64_t dsegs) {
   Layout l;
   l.draws = align_up(2 * tokens * segs * sizeof(Stat), 16);
   l.sums = l.draws + seqs * sizeof(int4);
-  l.done = l.sums + 3 * seqs * dsegs * sizeof(double);
-  l.bytes = l.done + seqs * 4;
+  l.bytes = l.sums + 3 * seqs * dsegs * sizeof(double);
   return l;
 }
 
@@ -557,7 +575,6 @@ hipError_t launch_verify(const VerifyArgs& v, hipStream_t stream) {
   a.stats = reinterpret_cast<Stat*>(ws);
   a.draws = reinterpret_cast<int4*>(ws + l.draws);
   a.sums = reinterpret_cast<double*>(ws + l.sums);
-  a.done = reinterpret_cast<int32_t*>(ws + l.done);
   const dim3 block(kThreads);
   const unsigned models = v.draft ? 2 : 1;
   if (v.tokens > 0)
