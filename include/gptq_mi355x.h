@@ -656,7 +656,7 @@ gptq_status kv_block_attention(const void* Q, int64_t q_token_stride, int64_t q_
  *   not negative.  A page that is written is neither read nor written by another pair.  An array's page is
  *   outer x inner rows of row_bytes, their strides in bytes.
  * rows, new_rows, pages, pairs <= 2^24, rows * width < 2^30, pages * page_size < 2^31;
- * fork: rows and new_rows + pages / 256 below 2^24 (GPTQ_ERR_UNSUPPORTED).
+ * fork, resize: rows and new_rows + pages / 256 below 2^24 (GPTQ_ERR_UNSUPPORTED).
  * ---------------------------------------------------------------------- */
 typedef struct gptq_page_array {
   void* data;

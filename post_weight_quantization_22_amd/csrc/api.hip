@@ -733,7 +733,7 @@ gptq_status kv_pages_resize(int32_t* table, int64_t ldt, int32_t* lengths, int64
   const gptq_status w = check_ws(ws, ws_bytes, kv_pages_resize_ws_bytes(rows, pages));
   if (w != GPTQ_OK) return w;
   if ((reinterpret_cast<uintptr_t>(ws) & 3) != 0) return GPTQ_ERR_INVALID_ARG;
-  return hip_status(launch_kv_pages_resize(table, ldt, width, lengths, rows, refs, pages,
+  return grid_status(launch_kv_pages_resize(table, ldt, width, lengths, rows, refs, pages,
                                            new_lengths, page_size, src, dst, info, ws, stream));
 }
 

@@ -25,8 +25,7 @@ constexpr int kPer = 4;       // pages that a thread looks at in one step
 constexpr int kStep = kWide * kPer;
 constexpr int kRows = 4096;   // rows whose last pages are compared at a time
 constexpr int kHeld = 8192;   // fresh pages that LDS holds
-constexpr int kSmall = 8192;  // pages and table entries that one workgroup forks or renames by itself
-constexpr int kEntries = 32768;  // .. takes back
+constexpr int kSmall = 8192;  // pages and table entries that one workgroup settles by itself
 
 __device__ __forceinline__ int pages_of(int len, int page_size) {
   return (int)(((int64_t)max(len, 0) + page_size - 1) / page_size);
@@ -88,7 +87,14 @@ __global__ __launch_bounds__(256) void pages_rows_kernel(ForkArgs a) {
   if (tid == 0) a.new_lengths[row] = len;
   const int32_t* from = a.table + max(p, 0) * a.ldt;
   int32_t* to = a.new_table + row * a.ldn;
-  for (int j = tid; j < a.width; j += 256) to[j] = j < n ? from[j] : -1;
+  for (int j0 = tid; j0 < a.width; j0 += 4 * 256) {
+    int page[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) page[k] = j0 + k * 256 < min(n, a.width) ? from[j0 + k * 256] : -1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (j0 + k * 256 < a.width) to[j0 + k * 256] = page[k];
+  }
 }
 
 // A workgroup per old row: its pages have as many more holders as it has children, less itself.
@@ -104,10 +110,17 @@ __global__ __launch_bounds__(256) void pages_refs_kernel(ForkArgs a) {
   c = part[0] + part[1] + part[2] + part[3] - 1;
   if (c == 0) return;
   const int n = min(pages_of(a.lengths[row], a.page_size), a.width);
-  for (int j = tid; j < n; j += 256) {
-    const int page = a.table[row * a.ldt + j];
-    if (page >= 0 && page < a.pages) atomicAdd(a.new_refs + page, c);
-    else if (a.info) atomicOr(a.info, 1);
+  const int32_t* const entries = a.table + row * a.ldt;
+  for (int j0 = tid; j0 < n; j0 += 4 * 256) {
+    int page[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) page[k] = entries[min(j0 + k * 256, n - 1)];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (j0 + k * 256 >= n) break;
+      if (page[k] >= 0 && page[k] < a.pages) atomicAdd(a.new_refs + page[k], c);
+      else if (a.info) atomicOr(a.info, 1);
+    }
   }
 }
 
@@ -188,28 +201,34 @@ __device__ __forceinline__ int wanted(const ResizeArgs& a, int row, int len, boo
   return n < 0 || bad ? len : n;
 }
 
-// A wave per row: pages past a shorter end go back.
+// A workgroup per row: pages past a shorter end go back, four entries of a thread under way.
 __global__ __launch_bounds__(256) void pages_drop_kernel(ResizeArgs a) {
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (row >= a.rows) return;
+  const int row = blockIdx.x, tid = threadIdx.x;
   const int len = a.lengths[row];
   bool bad;
   const int want = wanted(a, row, len, bad);
-  if (bad && a.info && lane == 0) atomicOr(a.info, 1);
-  if (lane == 0) {
+  if (bad && a.info && tid == 0) atomicOr(a.info, 1);
+  if (tid == 0) {
     a.src[row] = -1;
     a.dst[row] = -1;
   }
   if (want >= len) return;
   const int o = min(pages_of(len, a.page_size), a.width), n = pages_of(want, a.page_size);
-  for (int j = n + lane; j < o; j += 64) {
-    int32_t* e = a.table + row * a.ldt + j;
-    const int page = *e;
-    *e = -1;
-    if (page >= 0 && page < a.pages) atomicSub(a.refs + page, 1);
-    else if (a.info) atomicOr(a.info, 1);
+  int32_t* const entries = a.table + row * a.ldt;
+  for (int j0 = n + tid; j0 < o; j0 += 4 * 256) {
+    int page[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) page[k] = entries[min(j0 + k * 256, o - 1)];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (j0 + k * 256 >= o) break;
+      entries[j0 + k * 256] = -1;
+      if (page[k] >= 0 && page[k] < a.pages) atomicSub(a.refs + page[k], 1);
+      else if (a.info) atomicOr(a.info, 1);
+    }
   }
-  if (lane == 0) a.lengths[row] = want;
+  __syncthreads();  // (everyone has read the length)
+  if (tid == 0) a.lengths[row] = want;
 }
 
 // A load that sees what the same kernel's atomics have done (past the first-level cache).
@@ -575,10 +594,11 @@ hipError_t launch_kv_pages_resize(int32_t* table, int64_t ldt, int64_t width, in
   int32_t* w = static_cast<int32_t*>(ws);
   ResizeArgs a{table, lengths, refs, new_lengths, src, dst, info, w, w + (pages > kHeld ? pages : 0),
                ldt, (int32_t)rows, (int32_t)width, (int32_t)pages, page_size};
-  if (rows <= kWide && rows * width <= kEntries) {
+  if (!grid_fits(rows, 256)) return hipErrorInvalidConfiguration;
+  if (rows <= kWide && rows * width <= kSmall) {
     hipLaunchKernelGGL(pages_grow_kernel<true>, dim3(1), dim3(kWide), 0, stream, a);
   } else {
-    hipLaunchKernelGGL(pages_drop_kernel, dim3((unsigned)ceil_div(rows, 4)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(pages_drop_kernel, dim3((unsigned)rows), dim3(256), 0, stream, a);
     hipLaunchKernelGGL(pages_grow_kernel<false>, dim3(1), dim3(kWide), 0, stream, a);
   }
   return hipGetLastError();

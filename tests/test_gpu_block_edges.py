@@ -399,3 +399,33 @@ def test_a_serving_loop():
         assert (host(t2).tolist(), host(n2).tolist(), host(r2).tolist()) == (table, lens, refs)
         for c, w in zip(caches, want):
             _same_cache(c, w)
+
+
+# ---- NaN among many rows
+
+@pytest.mark.parametrize("window", [0, 70])
+@pytest.mark.parametrize("page,block", [(64, 64), (10, 5)])
+@pytest.mark.parametrize("dt,dim,news", [("bf16", 128, 100), ("bf16", 64, 300), ("f32", 128, 40), ("bf16", 256, 50)])
+def test_nan_in_tiles(dt, dim, news, page, block, window):
+    """A NaN among the values reaches the rows that see it, in tiles that all rows see as in the others."""
+    q = need_gpu()
+    rng = np.random.default_rng(71)
+    n = 330
+    table, pages = scattered(rng, [n], page)
+    kb, vb = (BlockCache(q, rng, pages, page, block, 1, dim, "e4m3") for _ in range(2))
+    x = torch.from_numpy(rng.normal(size=(news, 2, dim))).to(DT[dt]).cuda()
+    args = (ints(table), ints([n]), ints([0, news]))
+    clean, out = torch.empty_like(x), torch.empty_like(x)
+    q.kv_block_attention(x, kb.h, vb.h, *args, clean, window=window)
+    for p, col in ((3, 5), (n - news + 20, dim - 1), (n - 1, 0)):
+        place = table[0][p // page], p % page, 0, col
+        kept = vb.codes[place].clone()
+        vb.codes[place] = 0x7F
+        say("nan in tiles", dt, dim, news, page, window, p)
+        q.kv_block_attention(x, kb.h, vb.h, *args, out, window=window)
+        vb.codes[place] = kept
+        pos = torch.arange(n - news, n, device="cuda")
+        want = torch.zeros(x.shape, dtype=torch.bool, device="cuda")
+        want[(pos >= p) & ((pos < p + window) if window else (pos >= 0)), :, col] = True
+        assert torch.equal(torch.isnan(out), want), p
+        assert torch.equal(out[~want], clean[~want]), p
