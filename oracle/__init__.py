@@ -25,6 +25,9 @@ It is a plain, slow, obviously-correct restatement of the method on these pages:
   §4 (block_size a multiple of group_size, perc_damp 0.01; layers quantized in
   order on the quantized network's activations, in ``stack.py``).
 
+``lowp.py`` holds the low-precision operators, ``blocks.py`` the cache with a scale per block of
+tokens and head, its pages, and the verification of drafted tokens.
+
 Floating point is fp64 throughout, except where a floating value decides an
 integer (a code, a zero-point): there the decision is taken in fp32, the
 precision of the device kernels, emulated exactly (each fp32 operation is the
@@ -58,6 +61,7 @@ from .gptq import (  # noqa: F401
 )
 from .pack import pack_ref, unpack_ref  # noqa: F401
 from .dequant import dequant_weights, dequant_matmul  # noqa: F401
+from . import blocks  # noqa: F401
 from . import stack  # noqa: F401,E402  (layer-sequential MLP stack)
 from . import awq  # noqa: F401,E402  (AWQ-lite scale search and clip)
 from . import lowp  # noqa: F401,E402  (e4m3 products, key/value cache, log probabilities)

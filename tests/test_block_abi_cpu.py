@@ -200,6 +200,7 @@ def test_grids_past_the_hardware():
                                  3 * FAKE, 512, 256, None, None, FAKE, 1 << 50, None) == UNSUP
     for rows, new in ((N, 4), (4, N)):
         assert so.kv_pages_fork(FAKE, 8, FAKE, rows, 8, FAKE, 100, FAKE, new, 16, 2 * FAKE, 8, 2 * FAKE, 2 * FAKE, None, None) == UNSUP
+    assert so.kv_pages_resize(FAKE, 8, FAKE, N, 8, FAKE, 100, 2 * FAKE, 16, FAKE, 2 * FAKE, None, FAKE, 1 << 30, None) == UNSUP
     for t, seqs in ((N, 1), (1, N)):
         assert so.verify_drafts(FAKE, 1, 100, None, 0, 0, t, 100, FAKE, FAKE, seqs, FAKE, FAKE, None, FAKE, 2 * FAKE, None, FAKE,
                                 1 << 50, None) == UNSUP
