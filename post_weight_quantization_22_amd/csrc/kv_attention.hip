@@ -876,18 +876,21 @@ __global__ __launch_bounds__(kThreads, DP == 256 && F32 ? 1 : 2) void kv_attenti
     __syncthreads();  // tile b's operands, the next one's places
     const uint32_t odd = __builtin_amdgcn_readfirstlane(sh.odd[mark]);
     load_codes(b ^ 1);  // (behind the last tile: somewhere)
+    uint4 kw[2][STEPS];
+    auto read_keys = [&](int h, int i) { kw[i / STEPS][i % STEPS] = sh.k[b][2 * h + i / STEPS][i % STEPS][lane]; };
+#pragma unroll
+    for (int i = 0; i < 2 * STEPS; ++i) read_keys(0, i);
 #pragma unroll 1
     for (int h = 0; h < KEYS / 32; ++h) {
-      const int kh = k0 + 32 * h;
+      const int kh = k0 + 32 * h, ahead = min(h + 1, KEYS / 32 - 1);
       // keys that none of the wave's rows sees
-      if (idle || kh >= ke || (a.causal && (kh > pos_last || (a.window > 0 && kh + 31 <= max(pos_first, 0) - a.window)))) continue;
+      if (idle || kh >= ke || (a.causal && (kh > pos_last || (a.window > 0 && kh + 31 <= max(pos_first, 0) - a.window)))) {
+#pragma unroll
+        for (int i = 0; i < 2 * STEPS; ++i) read_keys(ahead, i);
+        continue;
+      }
       f32x4 s[MT][2];
       {
-        uint4 kw[2][STEPS];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int st = 0; st < STEPS; ++st) kw[u][st] = sh.k[b][2 * h + u][st][lane];
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
@@ -988,6 +991,10 @@ __global__ __launch_bounds__(kThreads, DP == 256 && F32 ? 1 : 2) void kv_attenti
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int k = 0; k < TERMS; ++k) o[n][mt] = mfma(f, p[mt][k], o[n][mt]);
+        if (KEYS > 32) {  // (the next half's keys travel beside these products)
+#pragma unroll
+          for (int i = n * 2 * STEPS / NT; i < (n + 1) * 2 * STEPS / NT; ++i) read_keys(ahead, i);
+        }
       }
       __builtin_amdgcn_s_setprio(0);
       if (FMT == GPTQ_KV_E4M3 && (odd >> (P * h) & ((1u << P) - 1)) != 0) {
