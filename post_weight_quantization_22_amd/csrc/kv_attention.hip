@@ -728,8 +728,8 @@ __global__ __launch_bounds__(kThreads, F32 || DP == 256 ? 1 : MT == 1 ? 3 : 2) v
 // maxima exchanged and sums rescaled.  The weights are then up to 2^kSlack, which fp32 sums and
 // bf16 weights hold as well as 1.
 //
-// 2 sequences of 2048 rows over 4096 tokens, 32 query heads on 8 of 128, e4m3: 280 us, 0.73 PFLOP/s (int8
-// 295; 4 x 2048 rows over themselves 210 us, 0.65; fp32 0.25; head_dim 64 0.48, 256 0.39).  No unit is full:
+// 2 sequences of 2048 rows over 4096 tokens, 32 query heads on 8 of 128, e4m3: 277 us, 0.74 PFLOP/s (int8
+// 293; 4 x 2048 rows over themselves 212 us, 0.65; fp32 0.25; head_dim 64 0.48, 256 0.40).  No unit is full:
 // matrix cores 30% of the time, vector units 46%, LDS 31%; two waves a SIMD hide each other's chains only in
 // part, and a third has no registers (it spills: 656 us).  8 waves that share a tile: 269 us here, but 230
 // for 4 x 2048, whose beginnings and ends nothing else fills.  Codes are unpacked once for four waves
@@ -1130,7 +1130,7 @@ struct Plan {
 };
 
 // 16 rows each of a wave in the tile kernel: as many as 256 registers hold beside the operands that
-// are read ahead (2 x 2048 rows over 4096 tokens: 2 279 us, 3, which spills, 373).
+// are read ahead (2 x 2048 rows over 4096 tokens: 2 277 us, 3, which spills, 373).
 constexpr int tile_mt(int dp, bool f32) { return dp == 64 ? (f32 ? 2 : 3) : f32 ? 1 : dp == 128 ? 2 : 1; }
 
 Plan plan_of(const gptq_kv_blocks* c, int q_heads, int dt, int64_t tokens, int64_t seqs, int64_t width) {
