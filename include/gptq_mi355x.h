@@ -566,8 +566,8 @@ gptq_status token_logprobs(const void* logits, gptq_dtype dt, int64_t tokens, in
  * lengths[seqs] their lengths with the call's new rows, starts[seqs + 1] (ascending)
  * where their rows begin: row r of sequence i is row starts[i] + r of the call and
  * stands at position lengths[i] - (starts[i + 1] - starts[i]) + r (rows at positions
- * below 0 are left out of writes, and see no key).  Rows behind starts[seqs] are padding
- * and neither read nor written.  A page number that a position needs and that is not a
+ * below 0 are left out of writes, and see no key).  Rows in front of starts[0] and behind
+ * starts[seqs] are neither read nor written.  A page number that a position needs and that is not a
  * page (or a position past the table) is not accessed, and *info (a device int32 that the
  * caller has cleared, may be NULL) becomes 1.  seqs <= tokens is not needed; a
  * sequence may have no rows.  GPTQ_ERR_UNSUPPORTED where a call would be of 2^24
@@ -688,7 +688,7 @@ gptq_status kv_pages_copy(const gptq_page_array* arrays, int64_t n, const int32_
  * full one verifies, and the tokens are distributed as if the full one had drawn each
  * ("Quantized deployment, 1.5 TB to 250 GB", section 3.1, judges a quantized model by
  * the same probabilities).  Sequence i has rows starts[i] .. starts[i + 1] - 1 (ascending,
- * rows behind starts[seqs] are padding): ids[t] is the drafted token that row t judges;
+ * rows in front of starts[0] and behind starts[seqs] are left alone): ids[t] is the drafted token that row t judges;
  * the last row judges none (its id is not used).  With p = softmax(target[t] / temperature)
  * and q = softmax(draft[t] / temperature), or certainty of ids[t] where draft is NULL:
  *   ids[t] is accepted while u[t] * q(ids[t]) < p(ids[t]);

@@ -183,7 +183,7 @@ __device__ __forceinline__ TileRows tile_rows(const AttnArgs& a, int task, int p
   int first;
   t.sp = span_of(a.s, task, a.group, a.by_rows, 1, first);
   t.row0 = (task - first) * per;
-  t.rows = max(min(per, t.sp.rows * a.group - t.row0), 0);
+  t.rows = task < first ? 0 : max(min(per, t.sp.rows * a.group - t.row0), 0);
   // positions of the first and last row; keys that any of them sees
   const int base = t.sp.length - t.sp.rows;
   t.hi = t.sp.length;

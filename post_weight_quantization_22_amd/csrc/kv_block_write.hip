@@ -83,7 +83,7 @@ __global__ __launch_bounds__(kThreads) void kv_block_write_kernel(BlockWriteArgs
   const Span sp = span_of(q, task, 1, q.by_block, 2, first);
   const int skip = max(sp.rows - sp.length, 0);  // rows in front of position 0
   const int p_new = max(sp.length - sp.rows, 0);
-  if (sp.rows <= skip) return;
+  if (sp.rows <= skip || task < first) return;
   const int64_t begin = (int64_t)(divided(p_new, q.by_block) + (task - first)) * q.block;
   if (begin >= sp.length) return;
   const int b0 = (int)begin;

@@ -51,7 +51,8 @@ struct Span {  // a sequence's new rows (none where the starts do not ascend)
 
 // The sequence that task t belongs to, and its first task: sequence i has the tasks from
 // starts[i] * num / den + i * extra on (each wave finds it by itself, 64 sequences a step;
-// starts that do not ascend lead to some sequence of the call all the same).
+// starts that do not ascend lead to some sequence of the call all the same).  Tasks of rows in front of
+// starts[0] have a first task behind them: nothing is to be done for those.
 // tokens * num < 2^31.
 __device__ __forceinline__ Span span_of(const Sequences& q, int t, int num, const Divisor& den,
                                         int extra, int& first) {
@@ -62,7 +63,7 @@ __device__ __forceinline__ Span span_of(const Sequences& q, int t, int num, cons
   while (n > 64) {
     const int step = (n + 63) / 64, i = lo + min(lane * step, n - 1);
     const bool below = (lane * step < n) & (task_at(start_at(i), i) <= t);
-    const int k = max(__popcll(__ballot(below)) - 1, 0);
+    const int k = max((int)__popcll(__ballot(below)) - 1, 0);
     n = min(step, n - k * step);
     lo += k * step;
   }
@@ -70,7 +71,7 @@ __device__ __forceinline__ Span span_of(const Sequences& q, int t, int num, cons
   const int i = lo + min(lane, n - 1);
   const int s0 = start_at(i), s1 = start_at(i + 1), len = q.lengths[i];
   // (& and no branch: what is computed on both sides of one counts as different in every lane)
-  const int k = max(__popcll(__ballot((lane < n) & (task_at(s0, i) <= t))) - 1, 0);
+  const int k = max((int)__popcll(__ballot((lane < n) & (task_at(s0, i) <= t))) - 1, 0);  // (it counts without a sign)
   Span s;
   s.seq = __builtin_amdgcn_readfirstlane(lo + k);
   s.start = __builtin_amdgcn_readlane(s0, k);

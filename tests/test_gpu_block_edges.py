@@ -55,6 +55,61 @@ def test_many_sequences(seqs, most):
     _same_cache(c, want)
 
 
+# ---- a call for some of a batch's sequences
+
+@pytest.mark.parametrize("rows", [1, 3, 70])
+@pytest.mark.parametrize("dt,fmt", [("bf16", "e4m3"), ("f32", "int8")])
+def test_starts_that_begin_later(rows, dt, fmt):
+    """starts, lengths and table of the last sequences of a batch, with the whole batch's rows: the others'
+    rows, codes and scales stay as they are."""
+    q = need_gpu()
+    rng = np.random.default_rng(rows)
+    lens = [int(v) for v in rng.integers(rows, rows + 200, size=9)]
+    news = [rows] * 9
+    H, G, D, page, block, skip = 2, 3, 64, 16, 8, 6
+    table, pages = scattered(rng, lens, page)
+    kb, vb = (BlockCache(q, rng, pages, page, block, H, D, fmt) for _ in range(2))
+    st = starts_of(news)
+    T = st[-1]
+    kv = torch.from_numpy(rng.normal(size=(T, 2 * H, D)) * 4).to(DT[dt])
+    x = torch.from_numpy(rng.normal(size=(T, H * G, D))).to(DT[dt])
+    want = [c.host() for c in (kb, vb)]
+    for w, r in zip(want, (kv[:, :H], kv[:, H:])):
+        blocks.write(*w, fmt, r.double().numpy(), table[skip:], lens[skip:], st[skip:])
+    some = (ints(table)[skip:], ints(lens)[skip:], ints(st)[skip:])
+    d = kv.cuda()
+    say("starts that begin later", rows, dt, fmt)
+    q.kv_block_write(d[:, :H], d[:, H:], kb.h, vb.h, *some)
+    _same_cache(kb, want[0])
+    _same_cache(vb, want[1])
+    out = torch.full((T, H * G, D), 7.0, dtype=DT[dt], device="cuda")
+    info = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q.kv_block_attention(x.cuda(), kb.h, vb.h, *some, out, info=info)
+    assert int(info) == 0
+    assert bool((out[:st[skip]] == 7).all())
+    ref, _, mag, smax = blocks.attention(x.double().numpy(), *kb.host(), *vb.host(), fmt, table[skip:], lens[skip:], st[skip:])
+    got, ref, mag, smax = (v[st[skip]:] for v in (host(out.double()), ref, mag, smax))
+    e = 2 * ((D + 8) * 2.0 ** -23 * smax + 2.0 ** -21) + (max(lens) + 16) * 2.0 ** -23
+    w, half = (2.0 ** -8, 2.0 ** -8) if dt == "bf16" else (2.0 ** -22, 2.0 ** -24)
+    assert np.all(np.abs(got - ref) <= half * np.abs(ref) + (1 + half) * (w * (1 + e) + e)[..., None] * mag + max(lens) * 2.0 ** -122)
+
+
+def test_verification_of_some_sequences():
+    q = need_gpu()
+    rng = np.random.default_rng(72)
+    counts = [3, 4, 2, 5]
+    t, d, ids, u, un = _case(rng, counts, 300)
+    st = starts_of(counts)
+    a, b, i, uu, nn = t.float().cuda(), d.float().cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(u).cuda(), torch.from_numpy(un).cuda()
+    whole = ints([7] * 4), torch.full((st[-1],), 7, dtype=torch.int64, device="cuda")
+    some = ints([7] * 2), torch.full((st[-1],), 7, dtype=torch.int64, device="cuda")
+    say("verification of some sequences")
+    q.verify_drafts(a, b, i, ints(st), uu, nn, *whole)
+    q.verify_drafts(a, b, i, ints(st)[2:], uu, nn[2:], *some)
+    assert torch.equal(some[0], whole[0][2:]) and torch.equal(some[1][st[2]:], whole[1][st[2]:])
+    assert bool((some[1][:st[2]] == 7).all())
+
+
 # ---- growing blocks, by units of each size
 
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
