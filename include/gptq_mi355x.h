@@ -566,7 +566,7 @@ gptq_status token_logprobs(const void* logits, gptq_dtype dt, int64_t tokens, in
  * lengths[seqs] their lengths with the call's new rows, starts[seqs + 1] (ascending)
  * where their rows begin: row r of sequence i is row starts[i] + r of the call and
  * stands at position lengths[i] - (starts[i + 1] - starts[i]) + r (rows at positions
- * below 0 are left out of writes, and see no key).  Rows in front of starts[0] and behind
+ * below 0 are left out of writes and, where causal, see no key).  Rows in front of starts[0] and behind
  * starts[seqs] are neither read nor written.  A page number that a position needs and that is not a
  * page (or a position past the table) is not accessed, and *info (a device int32 that the
  * caller has cleared, may be NULL) becomes 1.  seqs <= tokens is not needed; a
