@@ -484,3 +484,40 @@ def test_nan_in_tiles(dt, dim, news, page, block, window):
         want[(pos >= p) & ((pos < p + window) if window else (pos >= 0)), :, col] = True
         assert torch.equal(torch.isnan(out), want), p
         assert torch.equal(out[~want], clean[~want]), p
+
+
+# ---- rows off any border
+
+@pytest.mark.parametrize("rows", [2, 60])
+@pytest.mark.parametrize("dt,fmt", [("bf16", "e4m3"), ("bf16", "int8"), ("f32", "e4m3")])
+@pytest.mark.parametrize("dim", [16, 112, 128, 256])
+def test_unaligned_rows(rows, dt, fmt, dim):
+    """Rows, queries and outputs of matrices with odd strides, beginning off 16-byte borders: bit for bit what
+    aligned ones give; nothing beside them changes."""
+    q = need_gpu()
+    rng = np.random.default_rng(rows + dim)
+    lens, H, G, page = [rows + 37, rows + 5], 2, 2, 16
+    table, pages = scattered(rng, lens, page)
+    caches = [[BlockCache(q, np.random.default_rng(s), pages, page, page, H, dim, fmt) for s in (1, 2)] for _ in range(2)]
+    args = (ints(table), ints(lens), ints([0, rows, 2 * rows]))
+    kv = torch.from_numpy(rng.normal(size=(2 * rows, 2 * H, dim))).to(DT[dt]).cuda()
+    x = torch.from_numpy(rng.normal(size=(2 * rows, H * G, dim))).to(DT[dt]).cuda()
+
+    def odd(t, fill=3.0):
+        wide = torch.full((t.shape[0], t.shape[1], dim + 5), fill, dtype=t.dtype, device="cuda")
+        wide[..., 3:dim + 3] = t
+        return wide, wide[..., 3:dim + 3]
+
+    outs = []
+    say("unaligned rows", rows, dt, fmt, dim)
+    for (kb, vb), f in zip(caches, (lambda t: (t, t), odd)):
+        k, v, y = (f(t.contiguous())[1] for t in (kv[:, :H], kv[:, H:], x))
+        wide, out = f(torch.zeros_like(x))
+        q.kv_block_write(k, v, kb.h, vb.h, *args)
+        q.kv_block_attention(y, kb.h, vb.h, *args, out)
+        outs.append(out)
+        if wide is not out:
+            assert bool((wide[..., :3] == 3).all()) and bool((wide[..., dim + 3:] == 3).all())
+    for a, b in zip(*caches):
+        assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)
+    assert torch.equal(*outs)
