@@ -581,10 +581,12 @@ hipError_t launch_verify(const VerifyArgs& v, hipStream_t stream) {
     hipLaunchKernelGGL(verify_stats_kernel, dim3((unsigned)v.tokens, (unsigned)a.segs, models), block, 0,
                        stream, a);
   const dim3 dgrid((unsigned)v.seqs, (unsigned)a.dsegs);
+  // (a call without rows writes accepted = 0 and draws nothing: its u_next may be null)
 #define GPTQ_DRAW(TD, DD)                                                                  \
   do {                                                                                     \
     hipLaunchKernelGGL((verify_accept_kernel<TD, DD>), dgrid, block, 0, stream, a);        \
-    hipLaunchKernelGGL((verify_draw_kernel<TD, DD>), dgrid, block, 0, stream, a);          \
+    if (v.tokens > 0)                                                                      \
+      hipLaunchKernelGGL((verify_draw_kernel<TD, DD>), dgrid, block, 0, stream, a);        \
   } while (0)
   if (v.tdt == GPTQ_BF16 && (!v.draft || v.ddt == GPTQ_BF16)) GPTQ_DRAW(GPTQ_BF16, GPTQ_BF16);
   else if (v.tdt == GPTQ_BF16) GPTQ_DRAW(GPTQ_BF16, GPTQ_F32);
