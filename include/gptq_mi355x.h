@@ -586,7 +586,7 @@ gptq_status token_logprobs(const void* logits, gptq_dtype dt, int64_t tokens, in
  * fp32), at most the largest; E4M3: a non-finite x becomes the NaN code; INT8: an
  * infinity the largest code of its sign, a NaN code 0.  Nothing else is written; rows behind a
  * sequence's last one keep their bytes.  Blocks that are written belong to one sequence
- * of the call.
+ * of the call.  block * head_dim / 8 <= 2^31 - 1025 (GPTQ_ERR_UNSUPPORTED).
  *
  * kv_block_attention: out[t][h] = sum_j w_j V_j, w = softmax_j(scale * Q[t][h] . K_j), over
  * the keys j of t's sequence at positions 0 .. lengths[i] - 1; causal: those up to t's

@@ -635,6 +635,8 @@ gptq_status kv_block_write(const void* K, int64_t k_token_stride, int64_t k_head
     if (c) {
       const gptq_status ok = kv_blocks_ok(c);
       if (ok != GPTQ_OK) return ok;
+      // a block's earlier codes are counted in chunks of 8 and 32 bits, some steps past their end
+      if ((int64_t)c->block * (c->head_dim / 8) > INT32_MAX - 1024) return GPTQ_ERR_UNSUPPORTED;
     }
   // (one cache for both: keys and values would race for its places)
   if (kb && vb && (!kv_blocks_alike(kb, vb) || kb->codes == vb->codes || kb->scales == vb->scales))
