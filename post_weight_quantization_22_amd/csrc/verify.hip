@@ -73,12 +73,13 @@ __device__ __forceinline__ int wave_min(int v) {
   return v;
 }
 
-// the wave's parts as one; c: log2(e) / temperature
+// the wave's parts as one; c: log2(e) / temperature, 0 where only the largest logit counts
 __device__ __forceinline__ Stat wave_join(Stat s, float c) {
   Stat o;
   o.m = lanes_max<64>(s.m);
-  // (a part that holds nothing finite has sum 0, or NaN where it holds a NaN or +inf)
-  o.sum = wave_sum(s.m == kNegInf ? s.sum : s.sum * __builtin_amdgcn_exp2f((s.m - o.m) * c));
+  // (a part that holds nothing finite has sum 0, or NaN where it holds a NaN or +inf; maxima may be farther
+  // apart than any number, and infinity times 0 is none)
+  o.sum = wave_sum(s.m == kNegInf || c == 0.0f ? s.sum : s.sum * __builtin_amdgcn_exp2f((s.m - o.m) * c));
   o.at = wave_min(s.m == o.m ? s.at : INT32_MAX);
   return o;
 }

@@ -4,7 +4,9 @@ import ctypes
 import numpy as np
 import pytest
 
-from block_util import ints
+from oracle import blocks
+
+from block_util import DT, ints
 from gpu_util import host, need_gpu, say, torch
 
 pytestmark = pytest.mark.gpu
@@ -34,3 +36,38 @@ def test_sequences_without_rows(vocab, temps):
                         torch.zeros(S, device="cuda"), acc, torch.empty(0, dtype=torch.int64, device="cuda"), temperatures=t)
         torch.cuda.synchronize()
         assert np.all(host(acc) == 0)
+
+
+def _same_as_the_oracle(q, target, draft, ids, starts, u, un, temps):
+    f = lambda x: None if x is None else x.double().numpy()  # noqa: E731
+    acc, tok, lp, margin = blocks.verify(f(target), f(draft), ids, starts, u.astype(float), un.astype(float), temps)
+    assert margin > 2.0 ** -12, "a decision on its border"
+    T, S = target.shape[0], len(starts) - 1
+    ga, gt, gl = ints([77] * S), torch.full((T,), 77, dtype=torch.int64, device="cuda"), torch.full((T,), 77.0, device="cuda")
+    d = lambda x: None if x is None else torch.as_tensor(x).cuda()  # noqa: E731
+    q.verify_drafts(d(target), d(draft), d(ids), ints(starts), d(u), d(un), ga, gt, logprobs=gl,
+                    temperatures=d(np.asarray(temps, dtype=np.float32)))
+    torch.cuda.synchronize()
+    assert np.array_equal(host(ga), acc)
+    assert np.array_equal(host(gt), tok)
+    assert np.all(np.abs(host(gl) - lp) <= 2.0 ** -18 * (1 + np.abs(lp)))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab", [70, 3000, 70000])
+def test_logits_farther_apart_than_fp32_reaches(vocab, dt):
+    """Masks of the type's lowest value beside a logit near its largest: their difference is no finite number.  The
+    largest counts all the same, at temperature 0 as at others."""
+    q = need_gpu()
+    rng = np.random.default_rng(vocab)
+    S = 4
+    info = torch.finfo(DT[dt])
+    target = torch.full((2 * S, vocab), info.min, dtype=DT[dt])
+    ids = rng.integers(0, vocab, size=2 * S).astype(np.int64)
+    target[torch.arange(2 * S), torch.from_numpy(ids)] = info.max
+    target[2, ids[2]] = info.min
+    target[2, (int(ids[2]) + vocab // 2) % vocab] = info.max  # a refusal
+    u, un = np.full(2 * S, 0.5, np.float32), np.full(S, 0.5, np.float32)
+    say("verify, far logits", vocab, dt)
+    for temps in ([0.0] * S, [1.0, 0.0, 0.5, 2.0]):
+        _same_as_the_oracle(q, target, None, ids, list(range(0, 2 * S + 1, 2)), u, un, temps)
