@@ -47,6 +47,13 @@ __device__ __forceinline__ float temperature(const VerifyCall& a, int seq) {
   return a.v.temps ? a.v.temps[seq] : 1.0f;
 }
 
+// log2(e) / t, at most fp32's largest number (which t < 2^-127 would pass): logits 2^-100 apart are then far apart
+// still, and a difference of 0 stays 0
+__device__ __forceinline__ float exponent_scale(float t) {
+  const float c = kLog2e / t;
+  return c == __builtin_inff() ? 0x1.fffffep127f : c;
+}
+
 // TD, DD: the types of the target's and the drafter's logits
 template <int TD, int DD>
 __device__ __forceinline__ float logit(const VerifyCall& a, bool draft, int64_t row, int64_t i) {
@@ -170,7 +177,7 @@ __global__ __launch_bounds__(kThreads) void verify_stats_kernel(VerifyCall a) {
   if (draft && row == sp.start + sp.rows - 1) return;  // its logits judge nothing
   const float t = temperature(a, sp.seq);
   if (draft && t == 0.0f) return;
-  const float c = kLog2e / t;
+  const float c = exponent_scale(t);
   const int64_t c0 = blockIdx.y * a.seg, n = min(a.seg, a.v.vocab - c0);
   const int dt = draft ? a.v.ddt : a.v.tdt;
   const char* x = static_cast<const char*>(draft ? a.v.draft : a.v.target) +
@@ -243,7 +250,7 @@ __global__ __launch_bounds__(kThreads) void verify_accept_kernel(VerifyCall a) {
     return;
   }
   const bool sure = t == 0.0f, law_q = a.v.draft != nullptr && !sure;
-  const float c = sure ? 0.0f : kLog2e / t;
+  const float c = sure ? 0.0f : exponent_scale(t);
   if (tid == 0) refused = n - 1;  // (the last row judges nothing)
   __syncthreads();
   int taken = 0, at = 0;

@@ -71,3 +71,23 @@ def test_logits_farther_apart_than_fp32_reaches(vocab, dt):
     say("verify, far logits", vocab, dt)
     for temps in ([0.0] * S, [1.0, 0.0, 0.5, 2.0]):
         _same_as_the_oracle(q, target, None, ids, list(range(0, 2 * S + 1, 2)), u, un, temps)
+
+
+@pytest.mark.parametrize("tiny", [1e-37, 5e-39, 4e-39, 1e-42, 1e-45])
+def test_the_smallest_temperatures(tiny):
+    """Towards 0 the law becomes the largest logit's (or that of those that tie for it); the reciprocal of a temperature
+    below 2^-128 is no finite number."""
+    q = need_gpu()
+    rng = np.random.default_rng(5)
+    S, vocab = 6, 2000
+    target, draft = (torch.from_numpy(rng.normal(size=(2 * S, vocab))).float() for _ in range(2))
+    ids = draft.argmax(1).numpy().astype(np.int64)
+    ids[0::4] = target[0::4].argmax(1).numpy()
+    draft[torch.arange(2 * S), torch.from_numpy(ids)] = 9.0
+    target[3, :2] = target[3, 1990] = 50.0  # three tie
+    target[6, -500:] = -np.inf
+    u, un = np.full(2 * S, 0.5, np.float32), np.full(S, 0.5, np.float32)
+    say("verify, tiny temperatures", tiny)
+    temps = np.full(S, tiny, np.float32).astype(np.float64)
+    for d in (draft, None):
+        _same_as_the_oracle(q, target, d, ids, list(range(0, 2 * S + 1, 2)), u, un, temps)
