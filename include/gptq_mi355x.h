@@ -702,8 +702,9 @@ gptq_status kv_pages_copy(const gptq_page_array* arrays, int64_t n, const int32_
  * logprobs[t] (may be NULL): log p of tokens_out[t], 0 where that is -1 or the temperature 0.
  * target, draft [tokens][vocab] (row strides ldt, ldd; fp32 or bf16 each).  -inf is a masked
  * logit.  An id outside the vocabulary is refused, as is one whose rows hold a NaN or +inf or
- * nothing but -inf; from such a target row nothing is drawn (-1).  Acceptance sums in fp32, the
- * draw in fp64.  tokens, seqs < 2^24 (else GPTQ_ERR_UNSUPPORTED).  Workspace (16-byte aligned):
+ * nothing but -inf; from such a target row nothing is drawn (-1).  Temperatures are 0 or positive and
+ * finite.  Acceptance sums in fp32 (a probability is off by some 4 (d + ln vocab) 2^-24, d = the token's distance
+ * from the largest logit over the temperature), the draw in fp64.  tokens, seqs < 2^24 (else GPTQ_ERR_UNSUPPORTED).  Workspace (16-byte aligned):
  * verify_drafts_workspace_size(tokens, vocab, seqs).
  * ---------------------------------------------------------------------- */
 gptq_status verify_drafts_workspace_size(int64_t tokens, int64_t vocab, int64_t seqs,

@@ -205,10 +205,18 @@ def softmax(x: np.ndarray, temperature: float) -> np.ndarray:
 def verify(target, draft, ids, starts, u, u_next, temperatures=None):
     """(accepted, tokens, logprobs, margin): margin = how near the closest decision was to going
     the other way, relative to the probabilities it compares."""
+    *out, accepts, draws = verify_margins(target, draft, ids, starts, u, u_next, temperatures)
+    return *out, min([m for m, _ in accepts] + [draws])
+
+
+def verify_margins(target, draft, ids, starts, u, u_next, temperatures=None):
+    """(accepted, tokens, logprobs, accepts, draws): accepts = for each acceptance or refusal by two
+    numbers, |u q / p - 1| and how far the token's logits are below their rows' largest, in
+    temperatures (the target's and the drafter's in all); draws = how near the closest draw came to its border."""
     T, V = target.shape
     S = len(starts) - 1
     accepted, tokens, logprobs = np.zeros(S, np.int64), np.full(T, -1, np.int64), np.zeros(T)
-    margin = math.inf
+    accepts, draws = [], math.inf
     for i in range(S):
         temp = 1.0 if temperatures is None else float(temperatures[i])
         r, end = starts[i], starts[i + 1]
@@ -226,7 +234,10 @@ def verify(target, draft, ids, starts, u, u_next, temperatures=None):
                         q = softmax(draft[r], temp)
                     good = p[x] == 1.0 if temp == 0 else u[r] * q[x] < p[x]
                     if temp != 0 and np.isfinite(p[x]) and np.isfinite(q[x]) and p[x] > 0:
-                        margin = min(margin, abs(u[r] * q[x] / p[x] - 1.0))
+                        below = (target[r].max() - target[r][x]) / temp
+                        if draft is not None:
+                            below += (draft[r].max() - draft[r][x]) / temp
+                        accepts.append((abs(u[r] * q[x] / p[x] - 1.0), below))
                     if good:
                         tokens[r], logprobs[r] = x, 0.0 if temp == 0 else math.log(p[x])
                         accepted[i] += 1
@@ -243,7 +254,7 @@ def verify(target, draft, ids, starts, u, u_next, temperatures=None):
             border = u_next[i] * c[-1]
             v = int(np.searchsorted(c, border, side="right"))
             if temp != 0:
-                margin = min(margin, np.abs(c[:-1][w[:-1] > 0] - border).min(initial=np.inf) / c[-1])
+                draws = min(draws, np.abs(c[:-1][w[:-1] > 0] - border).min(initial=np.inf) / c[-1])
             tokens[r], logprobs[r] = v, 0.0 if temp == 0 else math.log(p[v])
             break
-    return accepted, tokens, logprobs, margin
+    return accepted, tokens, logprobs, accepts, draws

@@ -7,8 +7,9 @@
 // smallest v with C(v) > u' C(vocab - 1), C the running sum of the weights: the tokens are
 // then distributed as if the target had drawn each of them.
 //
-// The acceptance needs both models' logits once, one sum over each row (fp32, relative error
-// a few 2^-24, which moves a token across u q = p with that chance).  The draw compares a sum
+// The acceptance needs both models' logits once, one sum over each row, in fp32: with d = (m - x) / temperature a
+// probability is off by 4 (d + ln vocab) 2^-24 and some roundings more at most, four of them in each exponent and the
+// mean of d over the sum at most ln vocab.  A token moves across u q = p with that chance.  The draw compares a sum
 // over up to the whole vocabulary with a border; fp32's error would be as wide as many a token's
 // share, so the one row per sequence that is drawn from is summed in fp64.
 //
