@@ -645,7 +645,9 @@ gptq_status kv_block_attention(const void* Q, int64_t q_token_stride, int64_t q_
  *   before the row is written (-1, -1: none).  If all holders of a page grow in one call,
  *   the last row keeps it.  Fresh pages are the lowest free ones (those that the call
  *   gives back among them), rows in order, a row's own copy first.  If they do not suffice,
- *   no row grows.  A length that the table row cannot hold is left out (bit 0).
+ *   no row grows (bit 1): lengths do not hold the new rows then, which must not be written, as they would
+ *   take the last rows' places, also in pages that others hold.  A length that the table row cannot hold is
+ *   left out (bit 0).
  *   Workspace (4-byte aligned): kv_pages_resize_workspace_size(rows, pages).
  * kv_pages_compact: *count = pages in use (refs > 0); the k-th page in use behind the
  *   first *count ones moves to the k-th free one among them: src[k], dst[k], -1 behind the last

@@ -1326,7 +1326,7 @@ def kv_pages_resize(table, lengths, refs, new_lengths, page_size: int, src, dst,
     pages behind shorter ends are given back, longer rows get the lowest free pages, and a shared
     last page that a row grows in is replaced by one of its own: page src[i] has to be
     copied to dst[i] (both -1: none) by kv_pages_copy.  All int32; info: 2 where pages ran out (no
-    row has grown)."""
+    row has grown, and new rows must not be written: they would take the last ones' places)."""
     d = _on_gpu(table, "table")
     if table.dim() != 2:
         raise ValueError("table: expected [rows, width]")
