@@ -638,7 +638,8 @@ gptq_status kv_block_attention(const void* Q, int64_t q_token_stride, int64_t q_
  * kv_pages_fork: new row i continues old row parents[i] (negative: an empty row): its pages
  * and its length, pages behind its end -1; new_refs = refs with the new rows' holdings in the
  * place of the old rows'.  No page is copied.  The outputs apart from the inputs.
- * kv_pages_resize, in place: row i gets new_lengths[i] (negative: it stays as it is).
+ * kv_pages_resize, in place: row i gets new_lengths[i] (negative: it stays as it is); src and dst apart from
+ *   the others.
  *   Pages behind a shorter end go back (entries become -1; 0 frees the row).  A row that grows gets
  *   fresh pages, and where its last page is partly filled and held by others too, a page
  *   of its own in the place of that one: src[i], dst[i] name the pair that has to be copied
@@ -707,7 +708,7 @@ gptq_status kv_pages_copy(const gptq_page_array* arrays, int64_t n, const int32_
  * nothing but -inf; from such a target row nothing is drawn (-1).  Temperatures are 0 or positive and
  * finite.  Acceptance sums in fp32 (a probability is off by some 4 (d + ln vocab) 2^-24, d = the token's distance
  * from the largest logit over the temperature), the draw in fp64.  tokens, seqs < 2^24 (else GPTQ_ERR_UNSUPPORTED).  Workspace (16-byte aligned):
- * verify_drafts_workspace_size(tokens, vocab, seqs).
+ * verify_drafts_workspace_size(tokens, vocab, seqs).  The outputs apart from the inputs.
  * ---------------------------------------------------------------------- */
 gptq_status verify_drafts_workspace_size(int64_t tokens, int64_t vocab, int64_t seqs,
                                          size_t* bytes);

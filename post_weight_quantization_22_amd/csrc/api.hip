@@ -684,7 +684,7 @@ gptq_status kv_block_attention(const void* Q, int64_t q_token_stride, int64_t q_
     return GPTQ_ERR_INVALID_ARG;
   ok = kv_sequences_ok(q);
   if (ok != GPTQ_OK || tokens == 0 || seqs == 0) return ok;
-  if (!Q || !out || out == Q || q_token_stride < 0 || q_head_stride < 0 ||
+  if (!Q || !out || out == Q || (lse && (lse == Q || lse == out)) || q_token_stride < 0 || q_head_stride < 0 ||
       (tokens > 1 && o_token_stride <= 0) || (q_heads > 1 && o_head_stride <= 0))
     return GPTQ_ERR_INVALID_ARG;
   ok = check_ws(ws, ws_bytes, need);
@@ -709,7 +709,7 @@ gptq_status kv_pages_fork(const int32_t* table, int64_t ldt, const int32_t* leng
   if (!refs || !new_refs || refs == new_refs ||
       (rows > 0 && (!table || !lengths || (rows > 1 && ldt < width))) ||
       (new_rows > 0 && (!parents || !new_table || !new_lengths || (new_rows > 1 && ldn < width) ||
-                        new_table == table || new_lengths == lengths)))
+                        new_table == table || new_lengths == lengths || new_lengths == parents)))
     return GPTQ_ERR_INVALID_ARG;
   return grid_status(launch_kv_pages_fork(table, ldt, lengths, rows, refs, pages, parents, new_rows,
                                          page_size, new_table, ldn, width, new_lengths, new_refs,
@@ -800,6 +800,7 @@ gptq_status verify_drafts(const void* target, gptq_dtype tdt, int64_t ldt, const
   if (!valid_dtype(tdt) || (draft && !valid_dtype(ddt))) return GPTQ_ERR_INVALID_ARG;
   if (seqs == 0) return GPTQ_OK;
   if (!starts || !accepted ||
+      (logprobs && (logprobs == u_next || logprobs == temperatures)) ||
       (tokens > 0 && (!target || ldt < vocab || (draft && ldd < vocab) || !ids || !u || !u_next ||
                       !tokens_out || tokens_out == ids || logprobs == u)))
     return GPTQ_ERR_INVALID_ARG;

@@ -28,3 +28,27 @@ def test_blocks_whose_values_do_not_count_in_32_bits(dim, fmt):
     for block in (most + 1, most + 2, min(4 * most, 2 ** 31 - 1)):
         for t in (0, 4):
             assert write(block, t) == UNSUP, block
+
+
+def test_outputs_in_the_place_of_operands():
+    """Arrays that a call writes while it still reads them as something else."""
+    so = _lib.load()
+    A, B, C, D = (k * FAKE for k in range(2, 6))
+
+    def fork(parents=A, nl=B):
+        return so.kv_pages_fork(FAKE, 8, C, 4, 8, FAKE, 100, parents, 4, 16, D, 8, nl, D, None, None)
+
+    assert fork(parents=B) == BAD
+
+    def verify(starts=A, un=B, temps=C, lp=None):
+        return so.verify_drafts(FAKE, 0, 100, None, 0, 0, 4, 100, FAKE, starts, 2, FAKE, un, temps, D, 9 * FAKE, lp, FAKE, 1 << 30, None)
+
+    for kw in (dict(lp=B), dict(lp=C)):
+        assert verify(**kw) == BAD, kw
+
+    def attend(lse, dt=0):
+        kb, vb = _cache(), _cache(**OTHER)
+        return so.kv_block_attention(A, 256, 64, dt, 4, 4, ctypes.byref(kb), ctypes.byref(vb), FAKE, 3, 3, FAKE, FAKE, 2, 1, 0, 0.1, B, 256,
+                                     64, lse, None, FAKE, 1 << 40, None)
+
+    assert attend(A) == BAD and attend(B) == BAD
