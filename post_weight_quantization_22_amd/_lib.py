@@ -1237,7 +1237,10 @@ def kv_block_attention_workspace_size(kb: GPTQKVBlocks, q_heads: int, dtype, tok
                                       width: int) -> int:
     """dtype: the queries' torch dtype; width: entries of a table row."""
     _kinds()
-    return _attention_space(kb, q_heads, _FLOAT[_KIND[dtype]], tokens, seqs, width)
+    dt = _FLOAT.get(_KIND.get(dtype))
+    if dt is None:
+        raise TypeError(f"dtype {dtype}, expected bfloat16 or float32")
+    return _attention_space(kb, q_heads, dt, tokens, seqs, width)
 
 
 def _attention_space(kb, q_heads, dt, tokens, seqs, width) -> int:

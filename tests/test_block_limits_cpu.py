@@ -52,3 +52,10 @@ def test_outputs_in_the_place_of_operands():
                                      64, lse, None, FAKE, 1 << 40, None)
 
     assert attend(A) == BAD and attend(B) == BAD
+
+
+def test_the_workspace_query_names_a_wrong_type():
+    with pytest.raises(TypeError, match="dtype"):
+        _lib.kv_block_attention_workspace_size(_cache(), 4, torch.float16, 1, 1, 1)
+    with pytest.raises(TypeError, match="dtype"):
+        _lib.kv_block_attention_workspace_size(_cache(), 4, torch.int32, 1, 1, 1)
