@@ -597,7 +597,9 @@ gptq_status token_logprobs(const void* logits, gptq_dtype dt, int64_t tokens, in
  * 0, its lse -inf.  Places that a row does not see do not reach it, whatever they hold.
  * Products are those of the codes' values, summed in fp32; with bf16 rows the
  * weights are rounded to bf16 before the second product, as Q came in bf16; with fp32 rows
- * both hold 24 bits.  tokens * q_heads < 2^31.  Workspace (16-byte aligned, also where a call
+ * both hold 24 bits.  How the work is dealt out goes by the call's average rows a sequence and by width: long
+ * chunks beside steps over long contexts, or one very long context among short ones, take less time
+ * in calls of their own.  tokens * q_heads < 2^31.  Workspace (16-byte aligned, also where a call
  * needs none of it): kv_block_attention_workspace_size.
  * ---------------------------------------------------------------------- */
 typedef struct gptq_kv_blocks {
@@ -705,9 +707,10 @@ gptq_status kv_pages_copy(const gptq_page_array* arrays, int64_t n, const int32_
  * logprobs[t] (may be NULL): log p of tokens_out[t], 0 where that is -1 or the temperature 0.
  * target, draft [tokens][vocab] (row strides ldt, ldd; fp32 or bf16 each).  -inf is a masked
  * logit.  An id outside the vocabulary is refused, as is one whose rows hold a NaN or +inf or
- * nothing but -inf; from such a target row nothing is drawn (-1).  Temperatures are 0 or positive and
- * finite.  Acceptance sums in fp32 (a probability is off by some 4 (d + ln vocab) 2^-24, d = the token's distance
- * from the largest logit over the temperature), the draw in fp64.  tokens, seqs < 2^24 (else GPTQ_ERR_UNSUPPORTED).  Workspace (16-byte aligned):
+ * nothing but -inf; from such a target row nothing is drawn (-1).  Temperatures are 0 or positive
+ * and finite.  Acceptance sums in fp32 (a probability is off by some 4 (d + ln vocab) 2^-24, d = the
+ * token's distance from the largest logit over the temperature), the draw in fp64.  tokens,
+ * seqs < 2^24 (else GPTQ_ERR_UNSUPPORTED).  Workspace (16-byte aligned):
  * verify_drafts_workspace_size(tokens, vocab, seqs).  The outputs apart from the inputs.
  * ---------------------------------------------------------------------- */
 gptq_status verify_drafts_workspace_size(int64_t tokens, int64_t vocab, int64_t seqs,

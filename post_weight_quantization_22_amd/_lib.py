@@ -1267,7 +1267,10 @@ def kv_block_attention(Q, kb, vb, table, lengths, starts, out, lse=None, causal:
 
     causal: a row sees its own position and those before it, with ``window`` > 0 only the last
     ``window`` of them; else all of its sequence.  scale: head_dim ** -0.5 unless given.
-    lse[tokens, q_heads] (fp32): the logarithm of each row's denominator."""
+    lse[tokens, q_heads] (fp32): the logarithm of each row's denominator.
+
+    How the work is dealt out goes by the call's average rows a sequence and the table's width: long chunks
+    beside steps over long contexts take less time in calls of their own."""
     d = _on_gpu(Q, "Q")
     shape, qs, os_ = Q.shape, Q.stride(), out.stride()
     dt = _FLOAT.get(_KIND.get(Q.dtype))

@@ -21,7 +21,7 @@
 // where rows are few, the keys are also split over workgroups and joined by a second kernel.
 //
 // With few rows the codes' stream bounds it: 16 sequences of 12000 tokens, 64 query heads on 8 of 128, e4m3,
-// a row each: 77 us and 4 for the join, 4.7 TB/s (integers, 1 x 131072: 3.5; e4m3 3.7).  A small step, 5
+// a row each: 76 us and 5 for the join, 4.7 TB/s (1 x 131072: 59 and 6, 4.1, integers too).  A small step, 5
 // sequences of 300 tokens on 32 heads, 9 us: a chain of four round trips (starts, table, keys and
 // values, the sum), the launch, the join of the waves.  fp32 rows (three terms each, three times the
 // products) of 13 sequences of up to 2777 in pages of 100, windows of 1000: 14.5 us and 4.
@@ -723,14 +723,14 @@ __global__ __launch_bounds__(kThreads, F32 || DP == 256 ? 1 : MT == 1 ? 3 : 2) v
 // next are on their way, and the places of the one behind it are looked up, a key a thread.
 // An operand read from LDS feeds MT matrix instructions: 4 waves read 1 KB each in 16 MT cycles.
 //
-// The running maximum is a reference that is at most 2^kSlack below the true one: scores are
-// compared with it lane by lane, and only where one of a wave passes it (the first tiles) are
+// The running maximum is a reference that the true one passes by kSlack at most (scores are powers of two): scores
+// are compared with it lane by lane, and only where one of a wave passes it (the first tiles) are
 // maxima exchanged and sums rescaled.  The weights are then up to 2^kSlack, which fp32 sums and
 // bf16 weights hold as well as 1.
 //
-// 2 sequences of 2048 rows over 4096 tokens, 32 query heads on 8 of 128, e4m3: 277 us, 0.74 PFLOP/s (int8
+// 2 sequences of 2048 rows over 4096 tokens, 32 query heads on 8 of 128, e4m3: 279 us, 0.74 PFLOP/s (int8
 // 293; 4 x 2048 rows over themselves 212 us, 0.65; fp32 0.25; head_dim 64 0.48, 256 0.40).  No unit is full:
-// matrix cores 30% of the time, vector units 46%, LDS 31%; two waves a SIMD hide each other's chains only in
+// matrix cores 28% of the time, vector units 46%, LDS 31%; two waves a SIMD hide each other's chains only in
 // part, and a third has no registers (it spills: 656 us).  8 waves that share a tile: 269 us here, but 230
 // for 4 x 2048, whose beginnings and ends nothing else fills.  Codes are unpacked once for four waves
 // in LDS (each wave by itself, without LDS: 730 us).
@@ -1148,7 +1148,9 @@ Plan plan_of(const gptq_kv_blocks* c, int q_heads, int dt, int64_t tokens, int64
   p.tasks = tokens * group / p.per + seqs;
   // Splits: as many as give 512 workgroups, two a CU, whose waves' loads fill the memory's queue
   // (16 sequences of 12000, 8 heads of 128: 128 workgroups 115 us, 512 80, 768 88, 1024 91, 2048 87),
-  // 512 keys each at least (5 sequences of 300: one 10.1 us, two and their join 13.5).
+  // 512 keys each at least (5 sequences of 300: one 8.7 us; the 13 that a table for 32768 tokens gives them and
+  // their join 12.9).  Kernel, tiles and splits go by the call's averages and its table, which the host knows:
+  // sequences of very different kinds are right in one call, but faster in calls of their own.
   const int64_t tiles = hmin(p.tasks, seqs * ceil_div(each, p.per)) * c->heads;
   const int64_t keys = hmin(width * c->page_size, int64_t(1) << 30);
   p.splits = (int)hmax(1, hmin(hmin(ceil_div(512, tiles), 64), keys / 512));

@@ -458,8 +458,11 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyCall a) {
     }
     s = block_sum(s, part);
     if (tid == 0) {
-      // The sum goes past the caches by itself and has arrived before the others' are read; a fence would
-      // write back everything that this part of the chip holds (64 sequences: 37 us, not 14).
+      // The sum goes past the caches by itself and has arrived before the others' are read: a store and loads at
+      // the device's scope with a wait between them, which is how sequentially consistent ones are made on this
+      // chip, less the fence in front of them, which nothing here needs and which would write back everything
+      // that this part of the chip holds (64 sequences: 37 us, not 14).  So of two workgroups one at least sees
+      // the other's sum, and the one whose sum arrives last sees them all.
       __hip_atomic_store(sums + blockIdx.y, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
